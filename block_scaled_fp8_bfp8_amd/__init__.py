@@ -28,6 +28,7 @@ __all__ = [
     "quant_act_ue8m0", "gemm_ue8m0", "grouped_gemm_contiguous_ue8m0", "ue8m0_scales",
     "moe_padded_rows", "moe_dispatch", "quant_act_gather", "quant_act_scatter", "swiglu_quant", "swiglu", "moe_combine", "moe_forward",
     "moe_forward_workspace_bytes", "nn_to_nt_weights", "pad_k", "expand_act_scales", "expand_weight_scale", "set_schedule", "get_schedule", "schedule_for",
+    "rmsnorm_quant", "rmsnorm_quant_ue8m0", "latent_cache_write", "latent_cache_read", "latent_cache_gather",
     "abi_version", "BfpError", "LibraryMissing",
 ]
 
@@ -779,6 +780,171 @@ def linear_fuses(m: int, n: int, k: int, ldx: int | None = None) -> bool:
     """Whether linear() with these sizes runs one kernel that quantizes the activations inside
     the GEMM (small M), rather than the quantizer and then the GEMM."""
     return bool(_native.lib().bfp8_linear_fuses(m, n, k, k if ldx is None else ldx))
+
+
+def _same_device(first: torch.Tensor, **others):
+    """Every tensor on the first one's device (the launch runs on that device's current stream)."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _rmsnorm_quant(x, weight, residual, eps, out, e8: bool):
+    what = "rmsnorm_quant_ue8m0" if e8 else "rmsnorm_quant"
+    dt = _in_dtype(x, what)
+    _require(x, "x", x.dtype, 2)
+    _require(weight, "weight", x.dtype, 1)
+    m, k = x.shape
+    if x.stride(1) != 1 or weight.stride(0) != 1:
+        raise ValueError("x must be contiguous along its columns, and weight contiguous")
+    if weight.shape[0] != k:
+        raise ValueError(f"weight has {weight.shape[0]} elements, x has {k} columns")
+    h = x
+    if residual is not None:
+        _require(residual, "residual", x.dtype, 2)
+        h = torch.empty((m, k), dtype=x.dtype, device=x.device) if out is None else out
+        _require(h, "out", x.dtype, 2)
+        if residual.shape != x.shape or h.shape != x.shape:
+            raise ValueError(f"residual and out must have x's shape {tuple(x.shape)}")
+        if residual.stride(1) != 1 or h.stride(1) != 1:
+            raise ValueError("residual and out must be contiguous along their columns")
+    elif out is not None:
+        raise ValueError("out holds x + residual: it needs a residual")
+    _same_device(x, weight=weight, residual=residual, out=out)
+    q = torch.empty((m, -(-k // 128) * 128), dtype=torch.uint8, device=x.device)[:, :k]
+    if e8:
+        ld = max(-(-m // 4) * 4, 4)
+        scales = torch.empty((-(-k // 128), ld), dtype=torch.uint8, device=x.device)[:, :m].t()
+    else:
+        ld = max(m, 1)
+        scales = torch.empty((-(-k // 128), m), dtype=torch.float32, device=x.device).t()
+    lib = _native.lib()
+    entry = lib.bfp8_rmsnorm_quant_ue8m0 if e8 else lib.bfp8_rmsnorm_quant
+    st = entry(x.data_ptr(), dt, m, k, x.stride(0), None if residual is None else residual.data_ptr(),
+               k if residual is None else residual.stride(0), weight.data_ptr(), eps, h.data_ptr(), h.stride(0),
+               q.data_ptr(), q.stride(0), scales.data_ptr(), ld, _stream(x.device))
+    _check(st, "bfp8_" + what)
+    return q, scales, h
+
+
+def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                  out: torch.Tensor | None = None):
+    """Residual addition, RMS norm and quant_act in one launch, for x [M, H] (fp32, bf16 or fp16;
+    H a multiple of 16), residual like x and weight [H] of x's dtype.
+
+    Returns (q, s, h): h = x + residual rounded to x's dtype (x itself without a residual), and
+    q, s the codes and scales (laid out as quant_act's) of h / sqrt(mean(h^2) + eps) * weight,
+    which is not rounded in between. out: where to put h; it may be residual or x themselves."""
+    return _rmsnorm_quant(x, weight, residual, eps, out, False)
+
+
+def rmsnorm_quant_ue8m0(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                        eps: float = 1e-6, out: torch.Tensor | None = None):
+    """rmsnorm_quant with power-of-two scales: q and the scale codes as quant_act_ue8m0 returns them."""
+    return _rmsnorm_quant(x, weight, residual, eps, out, True)
+
+
+LATENT_DIM, ROPE_DIM, LATENT_ROW = 512, 64, 640  # latents, rotary key, bytes of a cache row
+
+
+def _latent_cache_args(cache: torch.Tensor, scales: torch.Tensor):
+    """(rows, page stride, scales, scale stride, pages, page size) of cache [pages, page, 640] uint8
+    and its scale codes [pages, page]."""
+    scales = _codes(scales, "scales")
+    _require(cache, "cache", torch.uint8, 3)
+    _require(scales, "scales", torch.uint8, 2)
+    pages, page, row = cache.shape
+    if row != LATENT_ROW or tuple(scales.shape) != (pages, page):
+        raise ValueError(f"cache must be [pages, page, {LATENT_ROW}] and scales [pages, page], got "
+                         f"{tuple(cache.shape)} and {tuple(scales.shape)}")
+    if cache.stride(2) != 1 or (page > 1 and (cache.stride(1) != LATENT_ROW or scales.stride(1) != 1)):
+        raise ValueError("the rows of a page and their scales must be contiguous (pages may be apart)")
+    _same_device(cache, scales=scales)
+    # a single page's stride carries no meaning
+    ps, ss = (cache.stride(0), scales.stride(0)) if pages > 1 else (page * LATENT_ROW, page)
+    return cache.data_ptr(), ps, scales.data_ptr(), ss, pages, page
+
+
+def _page_table_args(table: torch.Tensor):
+    _require(table, "page_table", torch.int32, 2)
+    b, width = table.shape
+    if width > 1 and table.stride(1) != 1:
+        raise ValueError("page_table must be contiguous along its rows")
+    return table.data_ptr(), table.stride(0) if b > 1 else max(width, 1), width
+
+
+def _starts_arg(cu: torch.Tensor, name: str, b: int):
+    _require(cu, name, torch.int32, 1)
+    if cu.shape[0] != b + 1 or not cu.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {b} + 1 entries, got shape {tuple(cu.shape)}")
+
+
+def latent_cache_write(kv: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
+                       norm_weight: torch.Tensor | None = None, eps: float = 1e-6) -> None:
+    """Quantize tokens into a paged FP8 latent cache: kv [T, 576] bf16 (512 latents, then the rotary
+    key), slots int64 [T] = page * page_size + row (negative: a padding token, not written; all
+    others distinct), cache uint8 [pages, page_size, 640], scales uint8 or float8_e8m0fnu
+    [pages, page_size]. With norm_weight (bf16 [512]) the latents are RMS-normed first. Pages may be
+    apart (one layer's slice of a cache of all layers)."""
+    _require(kv, "kv", torch.bfloat16, 2)
+    _require(slots, "slots", torch.int64, 1)
+    t = kv.shape[0]
+    if kv.shape[1] != LATENT_DIM + ROPE_DIM or kv.stride(1) != 1:
+        raise ValueError(f"kv must be [T, {LATENT_DIM + ROPE_DIM}] with contiguous rows, got {tuple(kv.shape)}")
+    if slots.shape[0] != t or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous vector of {t} entries")
+    if norm_weight is not None:
+        _require(norm_weight, "norm_weight", torch.bfloat16, 1)
+        if norm_weight.shape[0] != LATENT_DIM or norm_weight.stride(0) != 1:
+            raise ValueError(f"norm_weight must be a contiguous vector of {LATENT_DIM} elements")
+    _same_device(kv, slots=slots, cache=cache, norm_weight=norm_weight)
+    rows, ps, sc, ss, pages, page = _latent_cache_args(cache, scales)
+    st = _native.lib().bfp8_latent_cache_write(
+        kv.data_ptr(), t, kv.stride(0), None if norm_weight is None else norm_weight.data_ptr(), eps,
+        slots.data_ptr(), rows, ps, sc, ss, pages, page, _stream(kv.device))
+    _check(st, "bfp8_latent_cache_write")
+
+
+def latent_cache_read(cache: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, cu_tokens: torch.Tensor,
+                      total: int, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The first cu_tokens[b + 1] - cu_tokens[b] cached tokens of every sequence b, back to back, as
+    bf16 [total, 576] (latents, then the rotary key). page_table int32 [B, width] names a
+    sequence's pages in order, cu_tokens is int32 [B + 1] on the GPU and total its last entry.
+    Tokens without a page of the cache read as NaN."""
+    rows, ps, sc, ss, pages, page = _latent_cache_args(cache, scales)
+    table, ts, width = _page_table_args(page_table)
+    _starts_arg(cu_tokens, "cu_tokens", page_table.shape[0])
+    if out is None:
+        out = torch.empty((total, LATENT_DIM + ROPE_DIM), dtype=torch.bfloat16, device=cache.device)
+    _require(out, "out", torch.bfloat16, 2)
+    if tuple(out.shape) != (total, LATENT_DIM + ROPE_DIM) or out.stride(1) != 1:
+        raise ValueError(f"out must be [{total}, {LATENT_DIM + ROPE_DIM}] with contiguous rows")
+    _same_device(cache, page_table=page_table, cu_tokens=cu_tokens, out=out)
+    st = _native.lib().bfp8_latent_cache_read(rows, ps, sc, ss, pages, page, table, ts, width, page_table.shape[0],
+                                              cu_tokens.data_ptr(), total, out.data_ptr(), out.stride(0),
+                                              _stream(cache.device))
+    _check(st, "bfp8_latent_cache_read")
+    return out
+
+
+def latent_cache_gather(cache: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, cu_tokens: torch.Tensor,
+                        total: int):
+    """The tokens latent_cache_read reads, as operands of gemm_ue8m0: (q [total, 512] codes, e
+    [total, 4] UE8M0 codes laid out as quant_act_ue8m0's, rope [total, 64] bf16)."""
+    rows, ps, sc, ss, pages, page = _latent_cache_args(cache, scales)
+    table, ts, width = _page_table_args(page_table)
+    _starts_arg(cu_tokens, "cu_tokens", page_table.shape[0])
+    _same_device(cache, page_table=page_table, cu_tokens=cu_tokens)
+    dev = cache.device
+    q = torch.empty((total, LATENT_DIM), dtype=torch.uint8, device=dev)
+    ld = max(-(-total // 4) * 4, 4)
+    e = torch.empty((LATENT_DIM // 128, ld), dtype=torch.uint8, device=dev)[:, :total].t()
+    rope = torch.empty((total, ROPE_DIM), dtype=torch.bfloat16, device=dev)
+    st = _native.lib().bfp8_latent_cache_gather(rows, ps, sc, ss, pages, page, table, ts, width, page_table.shape[0],
+                                                cu_tokens.data_ptr(), total, q.data_ptr(), LATENT_DIM, e.data_ptr(),
+                                                ld, rope.data_ptr(), ROPE_DIM, _stream(dev))
+    _check(st, "bfp8_latent_cache_gather")
+    return q, e, rope
 
 
 def set_schedule(name: str) -> None:

@@ -66,6 +66,16 @@ SIGNATURES = [
     ("bfp8_linear_fuses", ctypes.c_int, [_i64, _i64, _i64, _i64]),
     ("bfp8_linear_noalloc", ctypes.c_int,
      [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    ("bfp8_rmsnorm_quant", ctypes.c_int,
+     [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    ("bfp8_rmsnorm_quant_ue8m0", ctypes.c_int,
+     [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    ("bfp8_latent_cache_write", ctypes.c_int,
+     [_vp, _i64, _i64, _vp, ctypes.c_float, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp]),
+    ("bfp8_latent_cache_read", ctypes.c_int,
+     [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+    ("bfp8_latent_cache_gather", ctypes.c_int,
+     [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
     ("bfp8_set_schedule", ctypes.c_int, [ctypes.c_int]),
     ("bfp8_get_schedule", ctypes.c_int, []),
     ("bfp8_gemm_schedule_for", ctypes.c_int, [_i64, _i64, _i64]),

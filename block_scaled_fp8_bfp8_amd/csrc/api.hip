@@ -15,6 +15,7 @@
 #include <string>
 
 #include "bfp8.h"
+#include "latent.h"
 #include "launch.h"
 
 namespace {
@@ -138,6 +139,71 @@ bfp8_status_t check_quant_args(const void* x, int x_dtype, int64_t M, int64_t K,
   if (!aligned(x, 16) || !aligned(q, 16)) return fail(BFP8_ERR_MISALIGNED, "x and q must be 16-byte aligned");
   if (!e8 && !aligned(as, 4)) return fail(BFP8_ERR_MISALIGNED, "as must be 4-byte aligned");
   return ok();
+}
+
+// The paged latent cache (no device access).
+bfp8_status_t check_latent_cache(const void* rows, const void* scales, int64_t pages, int64_t page_size,
+                                 int64_t page_stride, int64_t scale_stride) {
+  if (pages < 1 || page_size < 1)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "pages = %lld and page_size = %lld must be >= 1", (long long)pages,
+                (long long)page_size);
+  if (pages > INT32_MAX / page_size) return fail(BFP8_ERR_UNSUPPORTED, "the cache holds 2^31 tokens or more");
+  if (!rows || !scales) return fail(BFP8_ERR_INVALID_ARGUMENT, "rows and scales must not be NULL");
+  if (page_stride < page_size * bfp8::kLatentRow)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "page_stride = %lld < page_size * %d = %lld", (long long)page_stride,
+                bfp8::kLatentRow, (long long)(page_size * bfp8::kLatentRow));
+  if (scale_stride < page_size)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "scale_stride = %lld < page_size = %lld", (long long)scale_stride,
+                (long long)page_size);
+  if (!aligned(rows, 16)) return fail(BFP8_ERR_MISALIGNED, "cache rows must be 16-byte aligned");
+  if (page_stride % 128) return fail(BFP8_ERR_MISALIGNED, "page_stride must be a multiple of 128 bytes");
+  // a row's place is a 32-bit count of 128-byte units
+  if (page_stride / 128 > INT64_MAX / pages || page_stride / 128 * pages > (int64_t)UINT32_MAX)
+    return fail(BFP8_ERR_UNSUPPORTED, "the cache spans 512 GiB or more");
+  return BFP8_OK;
+}
+
+// A page table of B sequences (no device access).
+bfp8_status_t check_page_table(const int32_t* table, int64_t B, int64_t table_stride, int64_t table_width) {
+  if (B < 0 || table_width < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "B and table_width must not be negative");
+  if (B > kMaxDim || table_width > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "B and table_width must be at most 2^30");
+  if (!table && B > 0 && table_width > 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "page_table must not be NULL");
+  if (B > 1 && table_stride < table_width)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "table_stride = %lld < table_width = %lld", (long long)table_stride,
+                (long long)table_width);
+  if (!aligned(table, 4)) return fail(BFP8_ERR_MISALIGNED, "page_table must be 4-byte aligned");
+  return BFP8_OK;
+}
+
+bfp8::LatentCache latent_cache(const uint8_t* rows, int64_t page_stride, const uint8_t* scales, int64_t scale_stride,
+                               int64_t pages, int64_t page_size, const int32_t* table, int64_t table_stride,
+                               int64_t table_width) {
+  return {rows, scales, page_stride, scale_stride, (int)pages, (int)page_size, table, table_stride, (int)table_width};
+}
+
+bfp8_status_t rmsnorm_quant(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
+                            int64_t ld_res, const void* weight, float eps, void* h, int64_t ld_h, uint8_t* q,
+                            int64_t ldq, void* as, int64_t ld_as, bool e8, void* stream, const char* what) {
+  bfp8_status_t st = check_quant_args(x, x_dtype, M, H, ldx, q, ldq, as, ld_as, e8);
+  if (st != BFP8_OK) return st;
+  if (H > bfp8::kNormMaxH) return fail(BFP8_ERR_UNSUPPORTED, "H = %lld > %d", (long long)H, bfp8::kNormMaxH);
+  if (!(eps >= 0.f) || eps > 3.0e38f) return fail(BFP8_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  if (M == 0) return st;
+  const int64_t esize = x_dtype == BFP8_IN_F32 ? 4 : 2;
+  if (!weight) return fail(BFP8_ERR_INVALID_ARGUMENT, "weight must not be NULL");
+  if (!aligned(weight, 16)) return fail(BFP8_ERR_MISALIGNED, "weight must be 16-byte aligned");
+  if (residual) {
+    if (!h) return fail(BFP8_ERR_INVALID_ARGUMENT, "h must not be NULL with a residual");
+    if (ld_res < H || ld_h < H)
+      return fail(BFP8_ERR_INVALID_ARGUMENT, "ld_res = %lld and ld_h = %lld must be >= H = %lld", (long long)ld_res,
+                  (long long)ld_h, (long long)H);
+    if (!aligned(residual, 16) || !aligned(h, 16) || (ld_res * esize) % 16 || (ld_h * esize) % 16)
+      return fail(BFP8_ERR_MISALIGNED, "residual and h rows must be 16-byte aligned");
+  }
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  const bfp8::RmsNormArgs args{x, ldx, residual, ld_res, weight, eps, h, ld_h, q, ldq, as, ld_as, (int)M, (int)H};
+  return launched(bfp8::launch_rmsnorm_quant(args, x_dtype, e8, (hipStream_t)stream), what);
 }
 
 // Workspace of the linear layer: the codes q [M][K] at offset 0, the scales As [K/128][M]
@@ -847,6 +913,98 @@ bfp8_status_t bfp8_expand_weight_scale(const float* s, int64_t N, int64_t K, flo
   bfp8_status_t st = check_device();
   if (st != BFP8_OK) return st;
   return launched(bfp8::launch_fill_weight_scales(s, NB, KB, bs, ld_bs, (hipStream_t)stream), "expand_weight_scale");
+}
+
+bfp8_status_t bfp8_rmsnorm_quant(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
+                                 int64_t ld_res, const void* weight, float eps, void* h, int64_t ld_h, uint8_t* q,
+                                 int64_t ldq, float* as, int64_t ld_as, void* stream) {
+  return rmsnorm_quant(x, x_dtype, M, H, ldx, residual, ld_res, weight, eps, h, ld_h, q, ldq, as, ld_as, false, stream,
+                       "rmsnorm_quant");
+}
+
+bfp8_status_t bfp8_rmsnorm_quant_ue8m0(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx,
+                                       const void* residual, int64_t ld_res, const void* weight, float eps, void* h,
+                                       int64_t ld_h, uint8_t* q, int64_t ldq, uint8_t* as, int64_t ld_as,
+                                       void* stream) {
+  return rmsnorm_quant(x, x_dtype, M, H, ldx, residual, ld_res, weight, eps, h, ld_h, q, ldq, as, ld_as, true, stream,
+                       "rmsnorm_quant_ue8m0");
+}
+
+bfp8_status_t bfp8_latent_cache_write(const uint16_t* kv, int64_t T, int64_t ld_kv, const uint16_t* norm_weight,
+                                      float eps, const int64_t* slots, uint8_t* rows, int64_t page_stride,
+                                      uint8_t* scales, int64_t scale_stride, int64_t pages, int64_t page_size,
+                                      void* stream) {
+  if (T < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "T = %lld is negative", (long long)T);
+  if (T > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "T must be at most 2^30");
+  if (T == 0) return ok();
+  bfp8_status_t st = check_latent_cache(rows, scales, pages, page_size, page_stride, scale_stride);
+  if (st != BFP8_OK) return st;
+  if (!kv || !slots) return fail(BFP8_ERR_INVALID_ARGUMENT, "kv and slots must not be NULL");
+  if (ld_kv < bfp8::kLatentDim + bfp8::kRopeDim)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "ld_kv = %lld < %d", (long long)ld_kv, bfp8::kLatentDim + bfp8::kRopeDim);
+  if (norm_weight && (!(eps >= 0.f) || eps > 3.0e38f))
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  if (!aligned(kv, 16) || ld_kv % 8 || !aligned(norm_weight, 16))
+    return fail(BFP8_ERR_MISALIGNED, "kv rows and norm_weight must be 16-byte aligned");
+  if (!aligned(slots, 8)) return fail(BFP8_ERR_MISALIGNED, "slots must be 8-byte aligned");
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  const bfp8::LatentCache cache = latent_cache(rows, page_stride, scales, scale_stride, pages, page_size, nullptr, 0, 0);
+  return launched(bfp8::launch_latent_write(kv, T, ld_kv, norm_weight, eps, slots, cache, rows, scales,
+                                            (hipStream_t)stream), "latent_cache_write");
+}
+
+bfp8_status_t bfp8_latent_cache_read(const uint8_t* rows, int64_t page_stride, const uint8_t* scales,
+                                     int64_t scale_stride, int64_t pages, int64_t page_size,
+                                     const int32_t* page_table, int64_t table_stride, int64_t table_width, int64_t B,
+                                     const int32_t* cu_tokens, int64_t T, uint16_t* out, int64_t ld_out,
+                                     void* stream) {
+  if (T < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "T = %lld is negative", (long long)T);
+  if (T > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "T must be at most 2^30");
+  if (T == 0) return ok();
+  bfp8_status_t st = check_latent_cache(rows, scales, pages, page_size, page_stride, scale_stride);
+  if (st == BFP8_OK) st = check_page_table(page_table, B, table_stride, table_width);
+  if (st != BFP8_OK) return st;
+  if (B < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "B must be >= 1 when T > 0");
+  if (!cu_tokens || !out) return fail(BFP8_ERR_INVALID_ARGUMENT, "cu_tokens and out must not be NULL");
+  if (ld_out < bfp8::kLatentDim + bfp8::kRopeDim)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "ld_out = %lld < %d", (long long)ld_out, bfp8::kLatentDim + bfp8::kRopeDim);
+  if (!aligned(cu_tokens, 4)) return fail(BFP8_ERR_MISALIGNED, "cu_tokens must be 4-byte aligned");
+  if (!aligned(out, 16) || ld_out % 8) return fail(BFP8_ERR_MISALIGNED, "out rows must be 16-byte aligned");
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  const bfp8::LatentCache cache =
+      latent_cache(rows, page_stride, scales, scale_stride, pages, page_size, page_table, table_stride, table_width);
+  return launched(bfp8::launch_latent_read(cache, cu_tokens, B, T, out, ld_out, (hipStream_t)stream),
+                  "latent_cache_read");
+}
+
+bfp8_status_t bfp8_latent_cache_gather(const uint8_t* rows, int64_t page_stride, const uint8_t* scales,
+                                       int64_t scale_stride, int64_t pages, int64_t page_size,
+                                       const int32_t* page_table, int64_t table_stride, int64_t table_width,
+                                       int64_t B, const int32_t* cu_tokens, int64_t T, uint8_t* q, int64_t ldq,
+                                       uint8_t* as, int64_t ld_as, uint16_t* rope, int64_t ld_rope, void* stream) {
+  if (T < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "T = %lld is negative", (long long)T);
+  if (T > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "T must be at most 2^30");
+  if (T == 0) return ok();
+  bfp8_status_t st = check_latent_cache(rows, scales, pages, page_size, page_stride, scale_stride);
+  if (st == BFP8_OK) st = check_page_table(page_table, B, table_stride, table_width);
+  if (st != BFP8_OK) return st;
+  if (B < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "B must be >= 1 when T > 0");
+  if (!cu_tokens || !q || !as || !rope)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "cu_tokens, q, as and rope must not be NULL");
+  if (ldq < bfp8::kLatentDim || ld_as < T || ld_rope < bfp8::kRopeDim)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "ldq must be >= %d, ld_as >= T and ld_rope >= %d", bfp8::kLatentDim,
+                bfp8::kRopeDim);
+  if (!aligned(cu_tokens, 4)) return fail(BFP8_ERR_MISALIGNED, "cu_tokens must be 4-byte aligned");
+  if (!aligned(q, 16) || ldq % 16 || !aligned(rope, 16) || ld_rope % 8)
+    return fail(BFP8_ERR_MISALIGNED, "q and rope rows must be 16-byte aligned");
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  const bfp8::LatentCache cache =
+      latent_cache(rows, page_stride, scales, scale_stride, pages, page_size, page_table, table_stride, table_width);
+  return launched(bfp8::launch_latent_gather(cache, cu_tokens, B, T, q, ldq, as, ld_as, rope, ld_rope,
+                                             (hipStream_t)stream), "latent_cache_gather");
 }
 
 bfp8_status_t bfp8_set_schedule(int schedule) {

@@ -62,6 +62,56 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return (u & 0x7fffffffu) > 0x7f800000u ? quiet_nan : rounded;
 }
 
+// Two float32 values as a pair of bf16 (low half first), rounded to nearest even by the hardware
+// conversion.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2f f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, v2bf));
+}
+
+// The larger of two values, NaN if either is NaN (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// Clamp to the e4m3 range; NaN stays NaN. The e4m3 conversion does not saturate by itself.
+__device__ __forceinline__ float clamp_e4m3(float y) {
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(y, -448.0f), 448.0f);
+}
+
+// Four values as e4m3 codes (round to nearest even), first in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3(const float* y) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+}
+
+// 8 bf16 values as float32.
+__device__ __forceinline__ void bf16x8_values(const uint4& r, float* f) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// 8 e4m3 codes as float32.
+__device__ __forceinline__ void e4m3x8_values(const uint2& c, float* f) {
+  f[0] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 0);
+  f[1] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 1);
+  f[2] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 2);
+  f[3] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 3);
+  f[4] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 0);
+  f[5] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 1);
+  f[6] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 2);
+  f[7] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 3);
+}
+
+// The value 2^(code - 127) of a UE8M0 code (255: NaN; 0: 2^-127, a float32 subnormal).
+__device__ __forceinline__ float e8_value(uint32_t code) {
+  return code == 255u ? __builtin_nanf("") : code == 0u ? __uint_as_float(0x400000u) : __uint_as_float(code << 23);
+}
+
 // Output element n as bf16 bits: the FP32 result rounded to bf16, then, with a bias, the
 // bf16 sum bf16(float(c) + float(bias[n])) (the result is formed in the output's dtype and
 // the bias added to it, as the linear layer of page "transformers/integrations/deepgemm.py",

@@ -1,0 +1,152 @@
+// The paged FP8 latent cache of latent attention: writing tokens, reading them back.
+//
+// A cached token is one row of kLatentRow = 640 bytes: the 512 latents as e4m3 codes, then the 64
+// values of the rotary key in bf16; and one UE8M0 scale code in a separate array. A page holds
+// page_size rows. The scale of a token is its 1x512 group's max(amax, 1e-10) / 448 rounded up to
+// a power of two, held within 2^-42 .. 2^40 (the codes saturate beyond): one code serves the
+// token in the hardware-scaled products of attention, and repeated four times it is the token's
+// row of 1x128 scales for the UE8M0 GEMM. A token whose latents hold a NaN or an infinity is
+// stored as zero codes with scale code 255 (NaN): rows that see it become NaN, rows that do not
+// multiply it by a zero weight and stay finite.
+//
+// All three kernels are HBM-bound (a token: 1152 bytes read and 641 written, or the reverse).
+#include "device_common.h"
+#include "latent.h"
+#include "launch.h"
+
+namespace bfp8 {
+
+namespace {
+
+constexpr int kTokensPerBlock = 4;  // one wave a token
+
+__global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* __restrict__ kv, int64_t ld_kv,
+                                                           const uint16_t* __restrict__ w, float eps,
+                                                           const int64_t* __restrict__ slots, int T, LatentCache cache,
+                                                           uint8_t* __restrict__ rows, uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * kTokensPerBlock + (threadIdx.x >> 6);
+  if (t >= T) return;
+  const int64_t slot = slots[t];
+  // negative: a padding token; past the cache: nothing there to write
+  if (slot < 0 || slot >= (int64_t)cache.pages * cache.page_size) return;
+  const int page = (int)slot / cache.page_size;
+  const int off = (int)slot - page * cache.page_size;
+  uint8_t* row = rows + page * cache.page_stride + (int64_t)off * kLatentRow;
+  const uint16_t* src = kv + t * ld_kv;
+
+  const uint4 r = *reinterpret_cast<const uint4*>(src + lane * 8);
+  uint4 rope = make_uint4(0, 0, 0, 0);
+  if (lane < 8) rope = *reinterpret_cast<const uint4*>(src + kLatentDim + lane * 8);
+  float y[8];
+  bf16x8_values(r, y);
+  if (w != nullptr) {
+    auto token_sum = [&](float f) {  // of the (y * f)^2
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(y[i] * f, y[i] * f, sum);
+#pragma unroll
+      for (int mask = 1; mask < 64; mask <<= 1) sum += __shfl_xor(sum, mask);
+      return sum;
+    };
+    const float sum = token_sum(1.0f);
+    float rstd = 1.0f / sqrtf(sum / (float)kLatentDim + eps);
+    // squares past float32: summed again 2^-64 smaller
+    if (!(sum < __builtin_inff())) rstd = 0x1p-64f / sqrtf(token_sum(0x1p-64f) / (float)kLatentDim);
+    float f[8];
+    bf16x8_values(*reinterpret_cast<const uint4*>(w + lane * 8), f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (y[i] * rstd) * f[i];
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(y[i]));
+#pragma unroll
+  for (int mask = 1; mask < 64; mask <<= 1) amax = max_nan(amax, __shfl_xor(amax, mask));
+  uint32_t code = 255;
+  uint2 codes = make_uint2(0, 0);
+  if (amax < __builtin_inff()) {
+    code = (__float_as_uint(max_nan(amax, 1e-10f) / 448.0f) + 0x7fffffu) >> 23;
+    code = min(max(code, kLatentMinCode), kLatentMaxCode);
+    const float inv = __uint_as_float((254u - code) << 23);  // exact
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = clamp_e4m3(y[i] * inv);
+    codes = make_uint2(pack_e4m3(y), pack_e4m3(y + 4));
+  }
+  *reinterpret_cast<uint2*>(row + lane * 8) = codes;
+  if (lane < 8) *reinterpret_cast<uint4*>(row + kLatentDim + lane * 16) = rope;
+  if (lane == 0) scales[page * cache.scale_stride + off] = (uint8_t)code;
+}
+
+// Reads tokens cu[b] .. cu[b+1) of the sequences b back in order. kRaw: codes, the scale code
+// four times and the rotary key as stored; otherwise bf16(code * scale) and the rotary key.
+// A token whose page the table does not name (an entry outside the cache, or a position past the
+// table) reads as NaN; tokens past cu[B] are left unwritten.
+template <bool kRaw>
+__global__ __launch_bounds__(256) void latent_read_kernel(LatentCache cache, const int32_t* __restrict__ cu, int B,
+                                                          int T, uint8_t* __restrict__ q, int64_t ldq,
+                                                          uint8_t* __restrict__ e, int64_t ld_e,
+                                                          uint16_t* __restrict__ out, int64_t ld_out) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * kTokensPerBlock + (threadIdx.x >> 6);
+  if (t >= T || t < cu[0] || t >= cu[B]) return;
+  int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int pos = t - cu[lo];
+  const int col = pos / cache.page_size;
+  const int page = col < cache.table_width ? cache.table[lo * cache.table_stride + col] : -1;
+  const bool bad = page < 0 || page >= cache.pages;
+  const int off = pos - col * cache.page_size;
+  const uint8_t* row = cache.rows + (bad ? 0 : page) * cache.page_stride + (int64_t)(bad ? 0 : off) * kLatentRow;
+  const uint32_t code = bad ? 255u : cache.scales[page * cache.scale_stride + off];
+  uint4 rope = make_uint4(0, 0, 0, 0);
+  if (lane < 8) {
+    rope = *reinterpret_cast<const uint4*>(row + kLatentDim + lane * 16);
+    if (bad) rope = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+  }
+  uint2 c = *reinterpret_cast<const uint2*>(row + lane * 8);
+  if (bad) c = make_uint2(0, 0);
+  if constexpr (kRaw) {
+    *reinterpret_cast<uint2*>(q + t * ldq + lane * 8) = c;
+    if (lane < 4) e[lane * ld_e + t] = (uint8_t)code;
+  } else {
+    const float s = e8_value(code);
+    float f[8];
+    e4m3x8_values(c, f);
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pack_bf16(f[2 * i] * s, f[2 * i + 1] * s);
+    *reinterpret_cast<uint4*>(out + t * ld_out + lane * 8) = make_uint4(p[0], p[1], p[2], p[3]);
+  }
+  if (lane < 8) *reinterpret_cast<uint4*>(out + t * ld_out + (kRaw ? 0 : kLatentDim) + lane * 8) = rope;
+}
+
+}  // namespace
+
+hipError_t launch_latent_write(const uint16_t* kv, int64_t T, int64_t ld_kv, const uint16_t* w, float eps,
+                               const int64_t* slots, const LatentCache& cache, uint8_t* rows, uint8_t* scales,
+                               hipStream_t stream) {
+  hipLaunchKernelGGL(latent_write_kernel, dim3((unsigned)((T + kTokensPerBlock - 1) / kTokensPerBlock)), dim3(256), 0,
+                     stream, kv, ld_kv, w, eps, slots, (int)T, cache, rows, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_latent_read(const LatentCache& cache, const int32_t* cu, int64_t B, int64_t T, uint16_t* out,
+                              int64_t ld_out, hipStream_t stream) {
+  hipLaunchKernelGGL((latent_read_kernel<false>), dim3((unsigned)((T + kTokensPerBlock - 1) / kTokensPerBlock)),
+                     dim3(256), 0, stream, cache, cu, (int)B, (int)T, nullptr, 0, nullptr, 0, out, ld_out);
+  return hipGetLastError();
+}
+
+hipError_t launch_latent_gather(const LatentCache& cache, const int32_t* cu, int64_t B, int64_t T, uint8_t* q,
+                                int64_t ldq, uint8_t* e, int64_t ld_e, uint16_t* rope, int64_t ld_rope,
+                                hipStream_t stream) {
+  hipLaunchKernelGGL((latent_read_kernel<true>), dim3((unsigned)((T + kTokensPerBlock - 1) / kTokensPerBlock)),
+                     dim3(256), 0, stream, cache, cu, (int)B, (int)T, q, ldq, e, ld_e, rope, ld_rope);
+  return hipGetLastError();
+}
+
+}  // namespace bfp8

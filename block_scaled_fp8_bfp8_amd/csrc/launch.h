@@ -70,6 +70,26 @@ hipError_t launch_swiglu_quant(const uint16_t* proj, int64_t M, int64_t I, int64
                                uint8_t* q, int64_t ldq, float* as, int64_t ld_as, hipStream_t stream);
 hipError_t launch_swiglu(const uint16_t* proj, int64_t M, int64_t I, int64_t ldp, const int32_t* layout, uint16_t* h,
                          int64_t ldh, hipStream_t stream);
+// Residual addition + RMS norm + quantization (rmsnorm.hip). x, residual, weight and h have the
+// input's dtype; h is written only with a residual; as holds float32 scales, or UE8M0 codes with e8.
+struct RmsNormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* res;
+  int64_t ld_res;
+  const void* w;
+  float eps;
+  void* h;
+  int64_t ld_h;
+  uint8_t* q;
+  int64_t ldq;
+  void* as;
+  int64_t ld_as;
+  int M, H;
+};
+constexpr int kNormMaxH = 65536;  // a row is held in the registers of one workgroup
+hipError_t launch_rmsnorm_quant(const RmsNormArgs& args, int x_dtype, bool e8, hipStream_t stream);
+
 // NN -> NT conversions (layout.hip): dst[e][n][k] = src[e][k][n] for bytes; dst[e][c][r] =
 // src[e][r][c] for float32 (contiguous).
 hipError_t launch_transpose_u8(const uint8_t* src, int64_t E, int64_t K, int64_t N, int64_t ld_src, uint8_t* dst,

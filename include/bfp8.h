@@ -485,6 +485,71 @@ bfp8_status_t bfp8_expand_act_scales(const float* s, int64_t s_stride, int64_t M
 bfp8_status_t bfp8_expand_weight_scale(const float* s, int64_t N, int64_t K, float* bs, int64_t ld_bs,
                                        void* stream);
 
+/*
+ * bfp8_rmsnorm_quant: the residual addition, the root-mean-square norm and bfp8_quant_act in one
+ * launch. For row m of x [M][ldx]:
+ *   h = round_dtype(x + residual)                      (h = x when residual is NULL)
+ *   y = (h * 1 / sqrt(mean(h^2) + eps)) * weight       in float32, not rounded further
+ * and y is quantized per 1x128 group into q [M][ldq] and as (group-major), as bfp8_quant_act does
+ * (bfp8_rmsnorm_quant_ue8m0: as bfp8_quant_act_ue8m0).
+ *   x, residual, weight [H], h   all of x_dtype (BFP8_IN_F32, BFP8_IN_BF16 or BFP8_IN_F16)
+ *   h [M][ld_h]  written only with a residual, else ignored (may be NULL). h may be the buffer
+ *                of residual or of x (with that buffer's row stride): the stream updated in place
+ *   eps          finite, >= 0
+ *   H            a multiple of 16, at most 65536
+ * Rows, strides and other arguments as for bfp8_quant_act; residual, weight and h are 16-byte
+ * aligned. A NaN in a 128-wide group of y gives a NaN scale and NaN codes for that group.
+ */
+bfp8_status_t bfp8_rmsnorm_quant(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
+                                 int64_t ld_res, const void* weight, float eps, void* h, int64_t ld_h, uint8_t* q,
+                                 int64_t ldq, float* as, int64_t ld_as, void* stream);
+bfp8_status_t bfp8_rmsnorm_quant_ue8m0(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx,
+                                       const void* residual, int64_t ld_res, const void* weight, float eps, void* h,
+                                       int64_t ld_h, uint8_t* q, int64_t ldq, uint8_t* as, int64_t ld_as,
+                                       void* stream);
+
+/*
+ * The paged FP8 latent cache of latent attention. A cached token is a row of 640 bytes: 512
+ * latents as e4m3 codes, then the 64 values of its rotary key in bf16; and one UE8M0 scale code.
+ *   rows    device, row r of page p at rows + p * page_stride + r * 640 (16-byte aligned;
+ *           page_stride a multiple of 128, >= page_size * 640; pages need not touch, so one
+ *           layer's pages may lie between other layers')
+ *   scales  device, the row's scale code at scales + p * scale_stride + r (scale_stride >= page_size)
+ *   pages, page_size   >= 1, any page_size; fewer than 2^31 tokens and 512 GiB in all
+ *
+ * bfp8_latent_cache_write: token t of kv [T][ld_kv] (bf16; 512 latents, then the rotary key) goes
+ * to slot slots[t] = page * page_size + row. With norm_weight (bf16 [512]) the latents are first
+ * RMS-normed in float32. The token's scale is max(amax, 1e-10) / 448 rounded up to a power of
+ * two and held within 2^-42 .. 2^40 (codes saturate past it). A token with a NaN or infinite
+ * latent is stored as zero codes with scale code 255 (NaN). Tokens whose slot is negative
+ * (padding) or past the cache are not written; the slots of one call must differ.
+ *
+ * bfp8_latent_cache_read: the tokens of B sequences back to back as bf16: row t of out [T][ld_out]
+ * holds code * scale of the 512 latents (rounded once), then the rotary key. Sequence b's tokens
+ * are rows cu_tokens[b] .. cu_tokens[b + 1) (int32 [B + 1], rising), its token i lies on page
+ * page_table[b * table_stride + i / page_size]. A token whose entry is not a page of the cache,
+ * or lies past table_width, reads as NaN. Rows at or past cu_tokens[B] are not written.
+ *
+ * bfp8_latent_cache_gather: the same tokens as operands of bfp8_gemm_ue8m0 (K = 512): the codes
+ * into q [T][ldq], the token's scale code as its four 1x128 group scales as[g * ld_as + t], and
+ * the rotary keys into rope [T][ld_rope] (bf16). A token without a page: zero codes, scale codes
+ * 255, NaN rotary key.
+ */
+bfp8_status_t bfp8_latent_cache_write(const uint16_t* kv, int64_t T, int64_t ld_kv, const uint16_t* norm_weight,
+                                      float eps, const int64_t* slots, uint8_t* rows, int64_t page_stride,
+                                      uint8_t* scales, int64_t scale_stride, int64_t pages, int64_t page_size,
+                                      void* stream);
+bfp8_status_t bfp8_latent_cache_read(const uint8_t* rows, int64_t page_stride, const uint8_t* scales,
+                                     int64_t scale_stride, int64_t pages, int64_t page_size,
+                                     const int32_t* page_table, int64_t table_stride, int64_t table_width, int64_t B,
+                                     const int32_t* cu_tokens, int64_t T, uint16_t* out, int64_t ld_out,
+                                     void* stream);
+bfp8_status_t bfp8_latent_cache_gather(const uint8_t* rows, int64_t page_stride, const uint8_t* scales,
+                                       int64_t scale_stride, int64_t pages, int64_t page_size,
+                                       const int32_t* page_table, int64_t table_stride, int64_t table_width,
+                                       int64_t B, const int32_t* cu_tokens, int64_t T, uint8_t* q, int64_t ldq,
+                                       uint8_t* as, int64_t ld_as, uint16_t* rope, int64_t ld_rope, void* stream);
+
 /* Process-wide schedule override for bfp8_gemm (tests and benchmarks):
  * BFP8_SCHED_AUTO restores the automatic choice. Returns BFP8_ERR_INVALID_ARGUMENT
  * for an unknown value. The grouped GEMM always uses the tiled schedule. */

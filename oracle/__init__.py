@@ -37,6 +37,9 @@ What is computed, and where it is defined on the pages:
   (``float8_e8m0fnu`` codes): the quantizer with its scale rounded up to a power of two,
   and the blockwise GEMM of operands carrying such scales.
 
+* residual + RMS norm, the paged FP8 latent cache and latent attention (``latent``): their
+  definitions in float64.
+
 Every function is pinned by tests under ``tests/test_oracle_*.py`` (library
 routines, brute force with exact rationals, closed forms and invariants),
 including the spacing helpers ``bf16.ulp``, ``e4m3.ulp`` and ``f16.ulp`` that
@@ -45,6 +48,6 @@ next value as torch and numpy decode neighbouring bit patterns); none is
 "parity unpinned".
 """
 
-from . import bf16, e4m3, f16, gemm, linear, moe, quant, scales, ue8m0  # noqa: F401
+from . import bf16, e4m3, f16, gemm, latent, linear, moe, quant, scales, ue8m0  # noqa: F401
 
-__all__ = ["bf16", "e4m3", "f16", "gemm", "linear", "moe", "quant", "ue8m0"]
+__all__ = ["bf16", "e4m3", "f16", "gemm", "latent", "linear", "moe", "quant", "ue8m0"]
