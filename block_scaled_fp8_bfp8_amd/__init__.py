@@ -29,6 +29,7 @@ __all__ = [
     "moe_padded_rows", "moe_dispatch", "quant_act_gather", "quant_act_scatter", "swiglu_quant", "swiglu", "moe_combine", "moe_forward",
     "moe_forward_workspace_bytes", "nn_to_nt_weights", "pad_k", "expand_act_scales", "expand_weight_scale", "set_schedule", "get_schedule", "schedule_for",
     "rmsnorm_quant", "rmsnorm_quant_ue8m0", "latent_cache_write", "latent_cache_read", "latent_cache_gather",
+    "latent_attention", "latent_attention_workspace_bytes",
     "abi_version", "BfpError", "LibraryMissing",
 ]
 
@@ -945,6 +946,57 @@ def latent_cache_gather(cache: torch.Tensor, scales: torch.Tensor, page_table: t
                                                 ld, rope.data_ptr(), ROPE_DIM, _stream(dev))
     _check(st, "bfp8_latent_cache_gather")
     return q, e, rope
+
+
+def latent_attention_workspace_bytes(t: int, b: int, heads: int, max_keys: int) -> int:
+    """Workspace bytes of latent_attention (max_keys: page table width * page size)."""
+    return _native.lib().bfp8_latent_attention_workspace_bytes(t, b, heads, max_keys)
+
+
+def latent_attention(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
+                     seq_lens: torch.Tensor, scale: float, cu_q: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of new tokens over the paged FP8 latent cache, absorbed form: q [T, H, 576] bf16
+    against the cached rows [latents, rotary key], values the latents; returns [T, H, 512] bf16.
+
+    The cache already holds the new tokens, which end their sequences: sequence b has seq_lens[b]
+    tokens (int32 [B]) on the pages page_table[b] (int32 [B, width]); its new ones are rows
+    cu_q[b] .. cu_q[b + 1) of q (int32 [B + 1]), or row b alone without cu_q. Each sees its
+    sequence up to itself. Lengths are read on the GPU: nothing here waits for them.
+    workspace: optional caller-owned uint8 buffer (latent_attention_workspace_bytes); by default
+    one buffer per (device, stream) is kept."""
+    _require(q, "q", torch.bfloat16, 3)
+    t, heads, dim = q.shape
+    if dim != LATENT_DIM + ROPE_DIM or q.stride(2) != 1:
+        raise ValueError(f"q must be [T, H, {LATENT_DIM + ROPE_DIM}] with contiguous rows, got {tuple(q.shape)}")
+    rows, ps, sc, ss, pages, page = _latent_cache_args(cache, scales)
+    table, ts, width = _page_table_args(page_table)
+    b = page_table.shape[0]
+    _require(seq_lens, "seq_lens", torch.int32, 1)
+    if seq_lens.shape[0] != b or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens must be a contiguous vector of {b} entries")
+    if cu_q is not None:
+        _starts_arg(cu_q, "cu_q", b)
+    elif t != b:
+        raise ValueError(f"without cu_q every sequence has one query token, got {t} tokens and {b} sequences")
+    if out is None:
+        out = torch.empty((t, heads, LATENT_DIM), dtype=torch.bfloat16, device=q.device)
+    _require(out, "out", torch.bfloat16, 3)
+    if tuple(out.shape) != (t, heads, LATENT_DIM) or out.stride(2) != 1:
+        raise ValueError(f"out must be [{t}, {heads}, {LATENT_DIM}] with contiguous rows")
+    _same_device(q, cache=cache, page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, out=out, workspace=workspace)
+    lib = _native.lib()
+    if workspace is None:
+        ws_ptr, ws_bytes = _workspace(q.device, lib.bfp8_latent_attention_workspace_bytes(t, b, heads, width * page))
+    else:
+        _require(workspace, "workspace", torch.uint8, 1)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    st = lib.bfp8_latent_attention(q.data_ptr(), t, heads, q.stride(0), q.stride(1), rows, ps, sc, ss, pages, page, table,
+                                   ts, width, seq_lens.data_ptr(), b, None if cu_q is None else cu_q.data_ptr(), scale,
+                                   out.data_ptr(), out.stride(0), out.stride(1), ws_ptr or None, ws_bytes,
+                                   _stream(q.device))
+    _check(st, "bfp8_latent_attention")
+    return out
 
 
 def set_schedule(name: str) -> None:

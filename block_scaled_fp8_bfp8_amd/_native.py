@@ -76,6 +76,10 @@ SIGNATURES = [
      [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
     ("bfp8_latent_cache_gather", ctypes.c_int,
      [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    ("bfp8_latent_attention_workspace_bytes", _sz, [_i64, _i64, _i64, _i64]),
+    ("bfp8_latent_attention", ctypes.c_int,
+     [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, ctypes.c_float,
+      _vp, _i64, _i64, _vp, _sz, _vp]),
     ("bfp8_set_schedule", ctypes.c_int, [ctypes.c_int]),
     ("bfp8_get_schedule", ctypes.c_int, []),
     ("bfp8_gemm_schedule_for", ctypes.c_int, [_i64, _i64, _i64]),

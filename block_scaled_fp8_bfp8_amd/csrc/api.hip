@@ -1007,6 +1007,82 @@ bfp8_status_t bfp8_latent_cache_gather(const uint8_t* rows, int64_t page_stride,
                                              (hipStream_t)stream), "latent_cache_gather");
 }
 
+size_t bfp8_latent_attention_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t max_keys) {
+  if (T < 1 || B < 1 || H < 1 || max_keys < 0 || T > kMaxDim || B > kMaxDim || T > kMaxDim / H || max_keys > INT32_MAX)
+    return 0;
+  const bfp8::LatentAttnPlan p = bfp8::plan_latent_attn(T, B, H, max_keys);
+  return p.counts_bytes + p.stats_bytes + p.states_bytes;
+}
+
+bfp8_status_t bfp8_latent_attention(const uint16_t* q, int64_t T, int64_t H, int64_t q_token_stride,
+                                    int64_t q_head_stride, const uint8_t* rows, int64_t page_stride,
+                                    const uint8_t* scales, int64_t scale_stride, int64_t pages, int64_t page_size,
+                                    const int32_t* page_table, int64_t table_stride, int64_t table_width,
+                                    const int32_t* seq_lens, int64_t B, const int32_t* cu_q, float scale,
+                                    uint16_t* out, int64_t out_token_stride, int64_t out_head_stride,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "T = %lld is negative", (long long)T);
+  if (H < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "H = %lld must be >= 1", (long long)H);
+  if (T > kMaxDim || H > kMaxDim || T > kMaxDim / H)
+    return fail(BFP8_ERR_UNSUPPORTED, "T x H = %lld x %lld has more than 2^30 query rows", (long long)T, (long long)H);
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(BFP8_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (T == 0) return ok();
+  bfp8_status_t st = check_latent_cache(rows, scales, pages, page_size, page_stride, scale_stride);
+  if (st == BFP8_OK) st = check_page_table(page_table, B, table_stride, table_width);
+  if (st != BFP8_OK) return st;
+  if (B < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "B must be >= 1 when T > 0");
+  if (table_width > 0 && page_size > INT32_MAX / table_width)
+    return fail(BFP8_ERR_UNSUPPORTED, "a page table reaches 2^31 tokens or more");
+  if (!q || !out || !seq_lens) return fail(BFP8_ERR_INVALID_ARGUMENT, "q, out and seq_lens must not be NULL");
+  if (!cu_q && T != B)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "without cu_q every sequence has one query token: T = %lld, B = %lld",
+                (long long)T, (long long)B);
+  constexpr int kQ = bfp8::kLatentDim + bfp8::kRopeDim;
+  if (q_token_stride < 0 || q_head_stride < 0 || (H > 1 && q_head_stride < kQ) || (T > 1 && q_token_stride < kQ))
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "q strides must be at least %d elements", kQ);
+  if ((H > 1 && out_head_stride < bfp8::kLatentDim) || (T > 1 && out_token_stride < bfp8::kLatentDim))
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "out strides must be at least %d elements", bfp8::kLatentDim);
+  if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 || q_head_stride % 8 || out_token_stride % 8 ||
+      out_head_stride % 8)
+    return fail(BFP8_ERR_MISALIGNED, "q and out rows must be 16-byte aligned");
+  if (!aligned(seq_lens, 4) || !aligned(cu_q, 4))
+    return fail(BFP8_ERR_MISALIGNED, "seq_lens and cu_q must be 4-byte aligned");
+  const bfp8::LatentAttnPlan plan = bfp8::plan_latent_attn(T, B, H, table_width * page_size);
+  const size_t need = plan.counts_bytes + plan.stats_bytes + plan.states_bytes;
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(BFP8_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  if (need > 0 && !aligned(workspace, 256)) return fail(BFP8_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  bfp8::LatentAttnArgs args{};
+  args.q = q;
+  args.q_tok = q_token_stride;
+  args.q_head = q_head_stride;
+  args.out = out;
+  args.o_tok = out_token_stride;
+  args.o_head = out_head_stride;
+  args.cache =
+      latent_cache(rows, page_stride, scales, scale_stride, pages, page_size, page_table, table_stride, table_width);
+  args.lens = seq_lens;
+  args.cu_q = cu_q;
+  args.T = (int)T;
+  args.B = (int)B;
+  args.H = (int)H;
+  args.scale = scale;
+  args.target_parts = plan.target_parts;
+  args.min_tiles = plan.min_tiles;
+  args.max_tiles = plan.max_tiles;
+  args.max_slots = (int)plan.slots;
+  args.max_cuts = (int)plan.cuts;
+  if (need > 0) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    args.counts = reinterpret_cast<int*>(ws);
+    args.stats = reinterpret_cast<float*>(ws + plan.counts_bytes);
+    args.states = reinterpret_cast<float*>(ws + plan.counts_bytes + plan.stats_bytes);
+  }
+  return launched(bfp8::launch_latent_attn(args, plan, (hipStream_t)stream), "latent_attention");
+}
+
 bfp8_status_t bfp8_set_schedule(int schedule) {
   if (schedule < BFP8_SCHED_AUTO || schedule >= BFP8_SCHED_COUNT_)
     return fail(BFP8_ERR_INVALID_ARGUMENT, "unknown schedule %d", schedule);

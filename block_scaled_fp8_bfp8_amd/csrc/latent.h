@@ -32,4 +32,29 @@ hipError_t launch_latent_gather(const LatentCache& cache, const int32_t* cu, int
                                 int64_t ldq, uint8_t* e, int64_t ld_e, uint16_t* rope, int64_t ld_rope,
                                 hipStream_t stream);
 
+// Attention over the cache in the absorbed form. Strides of q and out in elements.
+struct LatentAttnArgs {
+  const uint16_t* q;  // [T][H][576] bf16
+  int64_t q_tok, q_head;
+  uint16_t* out;  // [T][H][512] bf16
+  int64_t o_tok, o_head;
+  LatentCache cache;
+  const int32_t* lens;  // [B] keys of a sequence, its new tokens among them
+  const int32_t* cu_q;  // [B + 1] first query token of a sequence, or NULL: token b is sequence b's
+  int T, B, H;
+  float scale;
+  int target_parts, min_tiles, max_tiles, max_slots, max_cuts;  // how the work is cut (LatentAttnPlan)
+  int* counts;    // workspace: number of cut blocks, then their descriptors from byte 16
+  float* stats;   // running maximum and sum of every row of every part of a cut block
+  float* states;  // its accumulator
+};
+struct LatentAttnPlan {
+  int64_t blocks, parts, slots, cuts;
+  int target_parts, min_tiles, max_tiles;
+  size_t counts_bytes, stats_bytes, states_bytes;
+};
+// max_keys: no sequence's page table reaches further.
+LatentAttnPlan plan_latent_attn(int64_t T, int64_t B, int64_t H, int64_t max_keys);
+hipError_t launch_latent_attn(const LatentAttnArgs& args, const LatentAttnPlan& plan, hipStream_t stream);
+
 }  // namespace bfp8

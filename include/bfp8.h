@@ -550,6 +550,39 @@ bfp8_status_t bfp8_latent_cache_gather(const uint8_t* rows, int64_t page_stride,
                                        int64_t B, const int32_t* cu_tokens, int64_t T, uint8_t* q, int64_t ldq,
                                        uint8_t* as, int64_t ld_as, uint16_t* rope, int64_t ld_rope, void* stream);
 
+/*
+ * bfp8_latent_attention: attention of new tokens over the paged FP8 latent cache, in the absorbed
+ * form (keys and values of every head are the cached row itself):
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . [c_j, r_j]) c_j
+ * with c_j the 512 latents (code * scale) and r_j the rotary key of cached token j. The new tokens
+ * are the last of their sequences, which the cache already holds: token i of the n new ones of a
+ * sequence of length L sees its tokens j <= L - n + i. A token that sees none gives zeros.
+ *   q        bf16 [T][H][576] (512 dimensions against the latents, 64 against the rotary key);
+ *            token and head strides in elements, multiples of 8; heads need not be a power of two
+ *   rows .. table_width  the cache and the page table, as in bfp8_latent_cache_read
+ *   seq_lens int32 [B], the length L of every sequence, new tokens included
+ *   cu_q     int32 [B + 1], rising: sequence b's new tokens are rows cu_q[b] .. cu_q[b + 1) of q;
+ *            or NULL: one new token a sequence (T == B)
+ *   out      bf16 [T][H][512], strides in elements, multiples of 8; rows that no sequence owns
+ *            are not written
+ *   workspace  bfp8_latent_attention_workspace_bytes(T, B, H, table_width * page_size) bytes,
+ *            256-byte aligned (at most about 135 MiB; 0 for short tables). It holds float32
+ *            states of blocks that were cut along their keys, for the call's second launch.
+ * A visible key without a page of the cache, or whose scale code is 255 (NaN), makes its rows NaN;
+ * rows that do not see a key are not affected by a code-255 key. Scale codes of visible keys are
+ * those bfp8_latent_cache_write makes (2^-42 .. 2^40, or 255). Lengths are read on the device: a
+ * captured call follows later changes of seq_lens, cu_q and the table. Weights are kept to 8
+ * significant bits and scores to the FP8 block dot's 13-binade window, everything else in float32.
+ */
+size_t bfp8_latent_attention_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t max_keys);
+bfp8_status_t bfp8_latent_attention(const uint16_t* q, int64_t T, int64_t H, int64_t q_token_stride,
+                                    int64_t q_head_stride, const uint8_t* rows, int64_t page_stride,
+                                    const uint8_t* scales, int64_t scale_stride, int64_t pages, int64_t page_size,
+                                    const int32_t* page_table, int64_t table_stride, int64_t table_width,
+                                    const int32_t* seq_lens, int64_t B, const int32_t* cu_q, float scale,
+                                    uint16_t* out, int64_t out_token_stride, int64_t out_head_stride,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Process-wide schedule override for bfp8_gemm (tests and benchmarks):
  * BFP8_SCHED_AUTO restores the automatic choice. Returns BFP8_ERR_INVALID_ARGUMENT
  * for an unknown value. The grouped GEMM always uses the tiled schedule. */

@@ -114,3 +114,37 @@ def test_gather_rejections(lib, kw, status):
 def test_read_and_gather_t_zero_are_no_ops(lib):
     assert _read(lib, T=0, cu=None, out=None, rows=None, table=None) == OK
     assert _gather(lib, T=0, cu=None, q=None, as_=None, rope=None, rows=None, table=None) == OK
+
+
+def _attend(lib, q=P3, T=3, H=16, qt=16 * 576, qh=576, lens=P4, B=3, cu=None, scale=0.1, out=P5, ot=16 * 512, oh=512, ws=P6,
+            wsb=None, table=P7, ts=8, tw=8, **kw):
+    c = {**CACHE, **kw}
+    if wsb is None:
+        wsb = lib.bfp8_latent_attention_workspace_bytes(max(T, 1), max(B, 1), max(H, 1), max(tw, 0) * max(c["page"], 0))
+    return lib.bfp8_latent_attention(q, T, H, qt, qh, c["rows"], c["ps"], c["sc"], c["ss"], c["pages"], c["page"], table, ts,
+                                     tw, lens, B, cu, scale, out, ot, oh, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHE + [
+    (dict(T=-1), E_INV), (dict(H=0), E_INV), (dict(T=1 << 20, B=1 << 20, H=1 << 11), E_UNS), (dict(q=None), E_INV),
+    (dict(out=None), E_INV), (dict(lens=None), E_INV), (dict(T=4), E_INV), (dict(B=0), E_INV), (dict(qh=575), E_INV),
+    (dict(qt=575), E_INV), (dict(oh=511), E_INV), (dict(ot=511), E_INV), (dict(qh=580), E_MIS), (dict(ot=16 * 512 + 4), E_MIS),
+    (dict(q=P3 + 8), E_MIS), (dict(out=P5 + 8), E_MIS), (dict(lens=P4 + 2), E_MIS), (dict(cu=P4 + 2), E_MIS),
+    (dict(scale=NAN), E_INV), (dict(scale=INF), E_INV), (dict(ws=None), E_WS), (dict(wsb=1024), E_WS), (dict(ws=P6 + 128), E_MIS),
+    (dict(table=None), E_INV), (dict(ts=7), E_INV), (dict(tw=-1), E_INV), (dict(B=1 << 31, T=1 << 31), E_UNS),
+    (dict(tw=1 << 26, ts=1 << 26), E_UNS), (dict(table=P7 + 2), E_MIS), (dict(qt=-8), E_INV),
+])
+def test_attention_rejections(lib, kw, status):
+    assert _attend(lib, **kw) == status, lib.bfp8_last_error_message()
+
+
+def test_attention_t_zero_is_a_no_op_and_workspace_sizes(lib):
+    assert _attend(lib, T=0, q=None, out=None, lens=None, rows=None, ws=None) == OK
+    size = lib.bfp8_latent_attention_workspace_bytes
+    assert size(1, 1, 16, 64) == 0  # one tile: nothing is cut
+    assert size(0, 1, 16, 640) == size(1, 1, 0, 640) == size(1, 1, 1, -1) == size(1 << 20, 1, 1 << 11, 64) == 0
+    last = 0
+    for t in (1, 8, 64, 512, 4096):  # grows with the work up to a bound
+        n = size(t, t, 128, 1 << 20)
+        assert n % 256 == 0 and last <= n <= 136 << 20
+        last = n
