@@ -29,7 +29,7 @@ __all__ = [
     "moe_padded_rows", "moe_dispatch", "quant_act_gather", "quant_act_scatter", "swiglu_quant", "swiglu", "moe_combine", "moe_forward",
     "moe_forward_workspace_bytes", "nn_to_nt_weights", "pad_k", "expand_act_scales", "expand_weight_scale", "set_schedule", "get_schedule", "schedule_for",
     "rmsnorm_quant", "rmsnorm_quant_ue8m0", "latent_cache_write", "latent_cache_read", "latent_cache_gather",
-    "latent_attention", "latent_attention_workspace_bytes",
+    "latent_attention", "latent_attention_workspace_bytes", "latent_attention_expanded",
     "abi_version", "BfpError", "LibraryMissing",
 ]
 
@@ -996,6 +996,46 @@ def latent_attention(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
                                    out.data_ptr(), out.stride(0), out.stride(1), ws_ptr or None, ws_bytes,
                                    _stream(q.device))
     _check(st, "bfp8_latent_attention")
+    return out
+
+
+def latent_attention_expanded(q: torch.Tensor, kv: torch.Tensor, rope: torch.Tensor, cu_q: torch.Tensor,
+                              cu_k: torch.Tensor, scale: float, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Ragged causal attention on expanded keys and values: q [Tq, H, 192], kv [Tk, H, 256] (128 key
+    dimensions, then 128 value dimensions), rope [Tk, 64] (the keys' rotary part, shared by the
+    heads), all bf16 or all fp16; returns [Tq, H, 128] of that dtype.
+
+    Sequence b has query rows cu_q[b] .. cu_q[b + 1) and keys cu_k[b] .. cu_k[b + 1) (int32
+    [B + 1] on the GPU); its last query sees its last key. Queries that see no key give zeros."""
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise NotImplementedError(f"latent_attention_expanded takes bfloat16 or float16, got {q.dtype}")
+    _require(q, "q", q.dtype, 3)
+    _require(kv, "kv", q.dtype, 3)
+    _require(rope, "rope", q.dtype, 2)
+    tq, heads, dim = q.shape
+    tk = kv.shape[0]
+    if dim != 192 or tuple(kv.shape[1:]) != (heads, 256) or tuple(rope.shape) != (tk, ROPE_DIM):
+        raise ValueError(f"expected q [Tq, H, 192], kv [Tk, H, 256] and rope [Tk, 64], got {tuple(q.shape)}, "
+                         f"{tuple(kv.shape)} and {tuple(rope.shape)}")
+    if q.stride(2) != 1 or kv.stride(2) != 1 or rope.stride(1) != 1:
+        raise ValueError("q, kv and rope must have contiguous rows")
+    _require(cu_q, "cu_q", torch.int32, 1)
+    b = cu_q.shape[0] - 1
+    if b < 0:
+        raise ValueError("cu_q must have B + 1 entries")
+    _starts_arg(cu_q, "cu_q", b)
+    _starts_arg(cu_k, "cu_k", b)
+    if out is None:
+        out = torch.empty((tq, heads, 128), dtype=q.dtype, device=q.device)
+    _require(out, "out", q.dtype, 3)
+    if tuple(out.shape) != (tq, heads, 128) or out.stride(2) != 1:
+        raise ValueError(f"out must be [{tq}, {heads}, 128] with contiguous rows")
+    _same_device(q, kv=kv, rope=rope, cu_q=cu_q, cu_k=cu_k, out=out)
+    st = _native.lib().bfp8_latent_attention_expanded(
+        q.data_ptr(), _IN_DTYPES[q.dtype], tq, heads, q.stride(0), q.stride(1), kv.data_ptr(), tk, kv.stride(0),
+        kv.stride(1), rope.data_ptr(), rope.stride(0), cu_q.data_ptr(), cu_k.data_ptr(), b, scale, out.data_ptr(),
+        out.stride(0), out.stride(1), _stream(q.device))
+    _check(st, "bfp8_latent_attention_expanded")
     return out
 
 

@@ -80,6 +80,9 @@ SIGNATURES = [
     ("bfp8_latent_attention", ctypes.c_int,
      [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, ctypes.c_float,
       _vp, _i64, _i64, _vp, _sz, _vp]),
+    ("bfp8_latent_attention_expanded", ctypes.c_int,
+     [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, ctypes.c_float, _vp, _i64,
+      _i64, _vp]),
     ("bfp8_set_schedule", ctypes.c_int, [ctypes.c_int]),
     ("bfp8_get_schedule", ctypes.c_int, []),
     ("bfp8_gemm_schedule_for", ctypes.c_int, [_i64, _i64, _i64]),

@@ -17,7 +17,7 @@ LIB_NAME = "libbfp8.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "quant_act.hip", "gemm_ksplit.hip", "gemm_tiled.hip", "gemm_g64.hip", "gemm_persistent.hip", "moe.hip",
            "layout.hip", "rmsnorm.hip", "latent_cache.hip",
-           "latent_attention.hip"]
+           "latent_attention.hip", "latent_expanded.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1083,6 +1083,61 @@ bfp8_status_t bfp8_latent_attention(const uint16_t* q, int64_t T, int64_t H, int
   return launched(bfp8::launch_latent_attn(args, plan, (hipStream_t)stream), "latent_attention");
 }
 
+bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64_t Tq, int64_t H,
+                                             int64_t q_token_stride, int64_t q_head_stride, const uint16_t* kv,
+                                             int64_t Tk, int64_t kv_token_stride, int64_t kv_head_stride,
+                                             const uint16_t* rope, int64_t ld_rope, const int32_t* cu_q,
+                                             const int32_t* cu_k, int64_t B, float scale, uint16_t* out,
+                                             int64_t out_token_stride, int64_t out_head_stride, void* stream) {
+  if (dtype != BFP8_IN_BF16 && dtype != BFP8_IN_F16)
+    return fail(BFP8_ERR_UNSUPPORTED, "dtype %d is not BFP8_IN_BF16 or BFP8_IN_F16", dtype);
+  if (Tq < 0 || Tk < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "Tq and Tk must not be negative");
+  if (H < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "H = %lld must be >= 1", (long long)H);
+  if (Tq > kMaxDim || Tk > kMaxDim || H > kMaxDim || B > kMaxDim)
+    return fail(BFP8_ERR_UNSUPPORTED, "Tq, Tk, H and B must each be at most 2^30");
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(BFP8_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (Tq == 0) return ok();
+  if (B < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "B must be >= 1 when Tq > 0");
+  if (bfp8::latent_expanded_blocks(Tq, B) > INT32_MAX / H)
+    return fail(BFP8_ERR_UNSUPPORTED, "Tq x H = %lld x %lld has more blocks than one launch grid holds", (long long)Tq,
+                (long long)H);
+  if (!q || !out || !cu_q || !cu_k || (Tk > 0 && (!kv || !rope)))
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "q, kv, rope, out, cu_q and cu_k must not be NULL");
+  if ((H > 1 && q_head_stride < 192) || (Tq > 1 && q_token_stride < 192) || (H > 1 && kv_head_stride < 256) ||
+      (Tk > 1 && kv_token_stride < 256) || (Tk > 1 && ld_rope < 64) || (H > 1 && out_head_stride < 128) ||
+      (Tq > 1 && out_token_stride < 128) || q_head_stride < 0 || q_token_stride < 0 || kv_head_stride < 0 ||
+      kv_token_stride < 0 || ld_rope < 0 || out_head_stride < 0 || out_token_stride < 0)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "rows overlap: strides must be at least 192 (q), 256 (kv), 64 (rope), 128 (out)");
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(rope, 16) || !aligned(out, 16) || q_token_stride % 8 ||
+      q_head_stride % 8 || kv_token_stride % 8 || kv_head_stride % 8 || ld_rope % 8 || out_token_stride % 8 ||
+      out_head_stride % 8)
+    return fail(BFP8_ERR_MISALIGNED, "q, kv, rope and out rows must be 16-byte aligned");
+  if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return fail(BFP8_ERR_MISALIGNED, "cu_q and cu_k must be 4-byte aligned");
+  bfp8_status_t st = check_device();
+  if (st != BFP8_OK) return st;
+  bfp8::LatentExpandedArgs args{};
+  args.q = q;
+  args.q_tok = q_token_stride;
+  args.q_head = q_head_stride;
+  args.kv = kv;
+  args.kv_tok = kv_token_stride;
+  args.kv_head = kv_head_stride;
+  args.rope = rope;
+  args.ld_rope = ld_rope;
+  args.out = out;
+  args.o_tok = out_token_stride;
+  args.o_head = out_head_stride;
+  args.cu_q = cu_q;
+  args.cu_k = cu_k;
+  args.Tq = (int)Tq;
+  args.Tk = (int)Tk;
+  args.B = (int)B;
+  args.H = (int)H;
+  args.scale = scale;
+  return launched(bfp8::launch_latent_expanded(args, dtype == BFP8_IN_F16, (hipStream_t)stream),
+                  "latent_attention_expanded");
+}
+
 bfp8_status_t bfp8_set_schedule(int schedule) {
   if (schedule < BFP8_SCHED_AUTO || schedule >= BFP8_SCHED_COUNT_)
     return fail(BFP8_ERR_INVALID_ARGUMENT, "unknown schedule %d", schedule);

@@ -12,6 +12,10 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 // One 16x16x128 FP8 (e4m3 x e4m3) matrix-core product with a zero accumulator input.
 // Operand layout (gfx950 v_mfma_f32_16x16x128_f8f6f4, both operands e4m3): lane l
@@ -219,6 +223,20 @@ __device__ __forceinline__ void copy4_to_lds(const void* sbase, uint32_t voff, u
       : "s"(sbase), "v"(voff), "s"(lds)
       : "memory");
 }
+// 16 bytes of every lane from its own global address to LDS byte lds + 16 * lane. Awaited with
+// wait_copies(); issued from inline assembly for the reason given at copy16_to_lds.
+__device__ __forceinline__ void copy16_from(const uint8_t* src, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(src), "s"(lds)
+      : "memory");
+}
+
 // The same copies for kernels whose register pressure lets the compiler spill the (wave-uniform)
 // base or LDS address: a value reloaded from a spill lands in a vector register, which the
 // scalar moves above cannot read, so these pass both through readfirstlane (free for values

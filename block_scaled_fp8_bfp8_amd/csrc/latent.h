@@ -57,4 +57,23 @@ struct LatentAttnPlan {
 LatentAttnPlan plan_latent_attn(int64_t T, int64_t B, int64_t H, int64_t max_keys);
 hipError_t launch_latent_attn(const LatentAttnArgs& args, const LatentAttnPlan& plan, hipStream_t stream);
 
+// Attention in the expanded form, ragged and causal. Strides in elements.
+struct LatentExpandedArgs {
+  const uint16_t* q;  // [Tq][H][192]
+  int64_t q_tok, q_head;
+  const uint16_t* kv;  // [Tk][H][256]: 128 key dimensions, 128 value dimensions
+  int64_t kv_tok, kv_head;
+  const uint16_t* rope;  // [Tk][64], shared by the heads
+  int64_t ld_rope;
+  uint16_t* out;  // [Tq][H][128]
+  int64_t o_tok, o_head;
+  const int32_t* cu_q;  // [B + 1]
+  const int32_t* cu_k;  // [B + 1]
+  int Tq, Tk, B, H;
+  float scale;
+};
+// The most blocks of query rows that B sequences of Tq rows in all can have, a head.
+int64_t latent_expanded_blocks(int64_t Tq, int64_t B);
+hipError_t launch_latent_expanded(const LatentExpandedArgs& args, bool f16, hipStream_t stream);
+
 }  // namespace bfp8

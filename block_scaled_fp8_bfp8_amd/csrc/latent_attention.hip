@@ -32,9 +32,6 @@ namespace bfp8 {
 
 namespace {
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef int v2i __attribute__((ext_vector_type(2)));
-
 constexpr int kTile = 64;                  // keys of a tile
 constexpr int kBM = 64;                    // query rows of a block: 16 for each of 4 waves
 constexpr int kSlack = 4;                  // the running maximum may lag by a factor of 2^kSlack ...
@@ -44,20 +41,6 @@ constexpr float kNegInf = -__builtin_inff();
 struct Desc {  // a block that was cut: rows row0 .. of the output, partial states slot .. slot + parts - 1
   int seq, block, slot, parts;
 };
-
-// 16 bytes of every lane from its own global address to LDS byte lds + 16 * lane. Awaited with
-// wait_copies(); issued from inline assembly for the reason given at copy16_to_lds.
-__device__ __forceinline__ void copy16_from(const uint8_t* src, uint32_t lds) {
-  uint32_t saved;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
-      "global_load_lds_dwordx4 %1, off\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
-      : "v"(src), "s"(lds)
-      : "memory");
-}
 
 // XOR of the 16-byte columns of a key's 512-byte row in LDS. Conflict-free both for the score
 // reads (16 lanes: one column of 16 consecutive keys) and for the transposing value reads (32

@@ -583,6 +583,28 @@ bfp8_status_t bfp8_latent_attention(const uint16_t* q, int64_t T, int64_t H, int
                                     uint16_t* out, int64_t out_token_stride, int64_t out_head_stride,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * bfp8_latent_attention_expanded: ragged causal attention on keys and values expanded from the
+ * latents (for prompts and long chunks, where the absorbed form would do 3.4 times the work):
+ *   out[t, h] = sum_j softmax_j(scale * (q[t, h, :128] . kv[j, h, :128] + q[t, h, 128:] . rope[j]))
+ *               kv[j, h, 128:]
+ * q, kv, rope and out all of dtype (BFP8_IN_BF16 or BFP8_IN_F16):
+ *   q     [Tq][H][192]   kv [Tk][H][256] (what bfp8_gemm_ue8m0 makes of bfp8_latent_cache_gather)
+ *   rope  [Tk][64], the rotary key of a token, shared by the heads      out [Tq][H][128]
+ *   strides in elements, multiples of 8
+ *   cu_q, cu_k  int32 [B + 1], rising: sequence b has query rows cu_q[b] .. cu_q[b + 1) and keys
+ *               cu_k[b] .. cu_k[b + 1). Query i of n sees keys j <= L - n + i of its L (the last
+ *               query sees the last key); one that sees none gives zeros. Rows of out that no
+ *               sequence owns are not written.
+ * Scores, softmax and sums are float32, weights are rounded to dtype before the second product.
+ */
+bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64_t Tq, int64_t H,
+                                             int64_t q_token_stride, int64_t q_head_stride, const uint16_t* kv,
+                                             int64_t Tk, int64_t kv_token_stride, int64_t kv_head_stride,
+                                             const uint16_t* rope, int64_t ld_rope, const int32_t* cu_q,
+                                             const int32_t* cu_k, int64_t B, float scale, uint16_t* out,
+                                             int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
 /* Process-wide schedule override for bfp8_gemm (tests and benchmarks):
  * BFP8_SCHED_AUTO restores the automatic choice. Returns BFP8_ERR_INVALID_ARGUMENT
  * for an unknown value. The grouped GEMM always uses the tiled schedule. */

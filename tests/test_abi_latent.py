@@ -148,3 +148,27 @@ def test_attention_t_zero_is_a_no_op_and_workspace_sizes(lib):
         n = size(t, t, 128, 1 << 20)
         assert n % 256 == 0 and last <= n <= 136 << 20
         last = n
+
+
+def _expanded(lib, q=P1, dt=BF16, Tq=10, H=4, qt=768, qh=192, kv=P2, Tk=12, kt=1024, kh=256, rope=P3, ldr=64, cq=P4, ck=P5,
+              B=2, scale=0.1, out=P6, ot=512, oh=128):
+    return lib.bfp8_latent_attention_expanded(q, dt, Tq, H, qt, qh, kv, Tk, kt, kh, rope, ldr, cq, ck, B, scale, out, ot, oh,
+                                              None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dt=F32), E_UNS), (dict(dt=9), E_UNS), (dict(Tq=-1), E_INV), (dict(Tk=-1), E_INV), (dict(H=0), E_INV),
+    (dict(B=0), E_INV), (dict(Tq=1 << 31), E_UNS), (dict(Tk=1 << 31), E_UNS), (dict(Tq=1 << 30, H=1 << 10), E_UNS),
+    (dict(q=None), E_INV), (dict(kv=None), E_INV), (dict(rope=None), E_INV), (dict(out=None), E_INV), (dict(cq=None), E_INV),
+    (dict(ck=None), E_INV), (dict(qt=184), E_INV), (dict(qh=184), E_INV), (dict(kt=248), E_INV), (dict(kh=248), E_INV),
+    (dict(ldr=56), E_INV), (dict(ot=120), E_INV), (dict(oh=120), E_INV), (dict(Tq=1, qt=-8), E_INV), (dict(qt=772), E_MIS),
+    (dict(kh=260), E_MIS), (dict(ldr=68), E_MIS), (dict(oh=132), E_MIS), (dict(q=P1 + 8), E_MIS), (dict(kv=P2 + 8), E_MIS),
+    (dict(rope=P3 + 8), E_MIS), (dict(out=P6 + 8), E_MIS), (dict(cq=P4 + 2), E_MIS), (dict(ck=P5 + 1), E_MIS),
+    (dict(scale=NAN), E_INV), (dict(scale=-INF), E_INV),
+])
+def test_expanded_rejections(lib, kw, status):
+    assert _expanded(lib, **kw) == status, lib.bfp8_last_error_message()
+
+
+def test_expanded_t_zero_is_a_no_op(lib):
+    assert _expanded(lib, Tq=0, q=None, kv=None, rope=None, out=None, cq=None, ck=None) == OK
