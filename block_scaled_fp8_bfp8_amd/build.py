@@ -9,6 +9,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -25,14 +27,12 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # never emit packed-FP32 instructions (v_pk_add/mul/fma_f32)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # MFMA results in ordinary VGPRs: the per-block promotion FMAs read them directly and
     # independent MFMAs do not serialize on one accumulator register quad
     "-mllvm", "-amdgpu-mfma-vgpr-form=1",
-
 ]
 
 
@@ -55,10 +55,7 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     return _compile(SOURCES, LIB_PATH, verbose, extra_flags)
 
 
-def _compile(sources: list[str], lib_path: str, verbose: bool, extra_flags: list[str] | None) -> str:
-    srcs = [os.path.join(CSRC, s) for s in sources]
-    tmp = lib_path + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), *srcs, "-o", tmp]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -68,6 +65,21 @@ def _compile(sources: list[str], lib_path: str, verbose: bool, extra_flags: list
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
+
+
+def _compile(sources: list[str], lib_path: str, verbose: bool, extra_flags: list[str] | None) -> str:
+    """One object a source, up to 8 at a time, then one shared library."""
+    tmp = lib_path + ".tmp"
+    with tempfile.TemporaryDirectory() as objects:
+        def one(src: str) -> str:
+            obj = os.path.join(objects, src + ".o")
+            _run([hipcc(), *HIPCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), "-c",
+                  os.path.join(CSRC, src), "-o", obj], verbose)
+            return obj
+
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            objs = list(pool.map(one, sources))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, lib_path)
     return lib_path
 

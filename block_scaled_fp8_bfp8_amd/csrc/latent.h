@@ -50,7 +50,7 @@ struct LatentAttnArgs {
 };
 struct LatentAttnPlan {
   int64_t blocks, parts, slots, cuts;
-  int target_parts, min_tiles, max_tiles;
+  int pairs, target_parts, min_tiles, max_tiles;
   size_t counts_bytes, stats_bytes, states_bytes;
 };
 // max_keys: no sequence's page table reaches further.
