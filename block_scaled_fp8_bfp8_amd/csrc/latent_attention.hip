@@ -12,9 +12,12 @@
 //     codes need no conversion. The key's scale code is the instruction's row scale. The rotary
 //     part is a bf16 product into the same accumulator.
 //   * values: the weight p_j and the key's scale are one number, p_j 2^(e_j) = 2^(x_j) with
-//     x_j = scale log2(e) s_j + e_j, kept relative to the row's running maximum of x (not of
-//     s), split into hi + lo e4m3 in the same way (at least 8 significant bits, as bf16 would
-//     have). The softmax denominator sums 2^(x_j) 2^(-e_j) in float32.
+//     x_j = scale log2(e) s_j + e_j, split into hi + lo e4m3 in the same way (at least 8
+//     significant bits, as bf16 would have). A row's weights of 32 keys share a power of two, the
+//     least that holds their largest, which the instruction applies: weights far below the largest
+//     of a long sequence keep their bits. The accumulator is kept relative to 2^m, m a whole number
+//     that only moves when a score passes it by 2^kSlack, so it is hardly ever rescaled. The softmax
+//     denominator sums 2^(x_j) 2^(-e_j) in float32.
 // The products are formed transposed (S^T = K Q^T, O^T = V^T P^T) with 32x32x64 instructions: a
 // lane holds 16 scores of one query row, r = lane % 32, for keys 8 q + 4 g + i (g = lane / 32),
 // which are at once its operand of the second product. hi and lo fill the two halves of that
@@ -44,8 +47,9 @@ namespace {
 
 constexpr int kTile = 64;                  // keys of a tile
 constexpr int kTileBytes = kTile * kLatentRow;
-constexpr int kSlack = 4;                  // the running maximum may lag by a factor of 2^kSlack ...
-constexpr float kTop = 8 - kSlack;         // ... so that 2^(x - m + kTop) stays within 2^8 <= 448
+constexpr float kSlack = 32.f;             // weights may pass the accumulator's reference by a factor of 2^kSlack
+constexpr float kTop = 8.f;                // the largest of 32 weights is held at 2^(kTop - 1) .. 2^kTop <= 448
+constexpr float kFar = 100.f;              // weights 2^-kFar below the reference are held relative to that
 constexpr float kNegInf = -__builtin_inff();
 
 struct Desc {  // a block that was cut: rows of block `block`, partial states slot .. slot + parts - 1
@@ -57,17 +61,20 @@ struct Desc {  // a block that was cut: rows of block `block`, partial states sl
 // reads (32 lanes: two neighbouring columns of 8 keys that differ in bits 0, 1 and 3).
 __device__ __forceinline__ int swz(int key) { return ((key & 3) << 1) | (key & 8) | ((key >> 2) & 1); }
 
+// Scale codes: ea's low byte and byte kByte of eb.
+template <int kByte>
 __device__ __forceinline__ v16f mfma_scaled(const v8i& a, const v8i& b, const v16f& c, int ea, int eb) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, ea, 0, eb);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, ea, kByte, eb);
 }
 
 // The same product added to an accumulator in the accumulation registers. Written in assembly so that it
 // stays there: the compiler otherwise moves accumulators between the two register files in bulk. The
 // wait in front covers operands that vector instructions have just written.
-__device__ __forceinline__ void mfma_scaled_acc(const v8i& a, const v8i& b, v16f& c, int ea, int eb) {
-  asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+// Scale codes: byte 0 of `codes` for a, byte 1 for b.
+__device__ __forceinline__ void mfma_scaled_acc(const v8i& a, const v8i& b, v16f& c, int codes) {
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %3 op_sel:[0,1,0] op_sel_hi:[0,0,0]"
       : "+a"(c)
-      : "v"(a), "v"(b), "v"(ea), "v"(eb));
+      : "v"(a), "v"(b), "v"(codes));
 }
 // A value that the compiler takes as new here: what is computed from it is formed where it is used, not
 // kept in registers across a loop.
@@ -96,126 +103,109 @@ __device__ __forceinline__ Seq sequence(const LatentAttnArgs& a, int b) {
   return s;
 }
 
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // 1, 2, 4, 8 lanes up within 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 to the next 16, of the odd rows
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
+  return v;
+}
+
 // What a workgroup computes: part `part` of `parts` of a block, and where its state goes (-1: nowhere).
 struct Work {
-  int seq, block, part, parts, slot;
+  Seq seq;
+  int index, block, part, parts, slot;
 };
 
-// Every workgroup of kThreads threads cuts the work in the same way and picks its own part. False:
-// it has none. `sh`: 64 ints of LDS.
-template <int kThreads, int kBM>
-__device__ __forceinline__ bool find_work(const LatentAttnArgs& a, int* sh, Work& work) {
-  constexpr int kWaves = kThreads / 64;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  // blocks and tiles of this thread's sequences; the first one's are kept
-  auto shape = [&](int b, int& n, int& tiles) {
-    const Seq s = sequence(a, b);
-    n = (int)(((int64_t)s.n * a.H + kBM - 1) / kBM);
-    tiles = min((s.len + kTile - 1) / kTile, a.max_tiles);
-  };
-  int n0 = 0, tiles0 = 0;
-  if (b0 < b1) shape(b0, n0, tiles0);
+// Every wave cuts the work in the same way and picks its workgroup's part. False: there is none.
+template <int kBM>
+__device__ __forceinline__ bool find_work(const LatentAttnArgs& a, Work& work) {
+  constexpr int kHeld = 4;   // sequences of a lane that are read once
+  constexpr int kMany = 1 << 16;  // more parts than ever run at once: sums of 64 such stay in range
+  const int lane = threadIdx.x & 63;
+  const int per = (a.B + 63) / 64;
+  const int b0 = min(lane * per, a.B), count = min(per, a.B - b0);
+  auto blocks_of = [&](const Seq& q) { return (int)(((int64_t)q.n * a.H + kBM - 1) / kBM); };
+  auto tiles_of = [&](const Seq& q) { return min((q.len + kTile - 1) / kTile, a.max_tiles); };
+  Seq held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    held[k] = {0, 0, 0};
+    if (k < count) held[k] = sequence(a, b0 + k);
+  }
   auto each = [&](auto f) {
-    if (b0 < b1) f(b0, n0, tiles0);
-    for (int b = b0 + 1; b < b1; ++b) {
-      int n, tiles;
-      shape(b, n, tiles);
-      f(b, n, tiles);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (k < count) f(b0 + k, held[k], blocks_of(held[k]), tiles_of(held[k]));
+    for (int k = kHeld; k < count; ++k) {
+      const Seq q = sequence(a, b0 + k);
+      f(b0 + k, q, blocks_of(q), tiles_of(q));
     }
   };
-  auto cut = [](int tiles, int quantum) { return max((tiles + quantum - 1) / quantum, 1); };
-  int turn = 0;
-  auto sum = [&](int64_t v) {  // over the workgroup
-#pragma unroll
-    for (int mask = 1; mask < 64; mask <<= 1) v += __shfl_xor(v, mask);
-    int64_t* s = reinterpret_cast<int64_t*>(sh) + 8 * (turn++ & 1);
-    if (lane == 0) s[wave] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += s[w];
-    return v;
+  auto cut = [](int tiles, int quantum) {  // max(ceil(tiles / quantum), 1)
+    int c = (int)((float)(tiles + quantum - 1) * __builtin_amdgcn_rcpf((float)quantum));
+    c += c * quantum < tiles;             // (the quotient by reciprocal is off by one at most)
+    c -= c > 0 && (c - 1) * quantum >= tiles;
+    return max(c, 1);
   };
-  int64_t blocks = 0, units = 0;
-  each([&](int, int n, int tiles) {
-    blocks += n;
-    units += (int64_t)n * tiles;
-  });
-  blocks = sum(blocks);
+  auto total = [](int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); };
   // The quantum: the least number of tiles a part with which the parts do not pass the
   // workgroups that run at once. With as many blocks as that, none is cut.
   int quantum = max(a.max_tiles, 1);
-  if (a.max_slots > 0 && blocks < a.target_parts) {
-    units = sum(units);
-    int lo = (int)max((units + a.target_parts - 1) / a.target_parts, (int64_t)a.min_tiles), hi = max(quantum, lo);
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      int64_t parts = 0;
-      each([&](int, int n, int tiles) { parts += (int64_t)n * cut(tiles, mid); });
-      if (sum(parts) <= a.target_parts) hi = mid;
-      else lo = mid + 1;
+  if (a.max_slots > 0) {
+    int64_t blocks = 0;
+    each([&](int, const Seq&, int n, int) { blocks += n; });
+    if (total((int)min(blocks, (int64_t)kMany)) < a.target_parts) {
+      int lo = a.min_tiles, hi = max(quantum, lo);
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        int64_t parts = 0;
+        each([&](int, const Seq&, int n, int tiles) { parts += (int64_t)n * cut(tiles, mid); });
+        if (total((int)min(parts, (int64_t)kMany)) <= a.target_parts) hi = mid;
+        else lo = mid + 1;
+      }
+      quantum = lo;
     }
-    quantum = lo;
   }
-  int parts = 0, slots = 0, cuts = 0;  // of this thread's sequences
-  each([&](int, int n, int tiles) {
+  int parts = 0, slots = 0, cuts = 0;  // of this lane's sequences
+  each([&](int, const Seq&, int n, int tiles) {
     const int c = cut(tiles, quantum);
     parts += n * c;
     if (c > 1) slots += n * c, cuts += n;
   });
-  // exclusive sums over the threads
-  int p0 = parts, s0 = slots, c0 = cuts;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int x = __shfl_up(p0, d), y = __shfl_up(s0, d), z = __shfl_up(c0, d);
-    if (lane >= d) p0 += x, s0 += y, c0 += z;
-  }
-  __syncthreads();
-  if (lane == 63) sh[wave * 3] = p0, sh[wave * 3 + 1] = s0, sh[wave * 3 + 2] = c0;
-  __syncthreads();
-  int pt = 0, ct = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int x = sh[w * 3], y = sh[w * 3 + 1], z = sh[w * 3 + 2];
-    if (w < wave) p0 += x, s0 += y, c0 += z;
-    pt += x;
-    ct += z;
-  }
+  int p0 = wave_scan(parts), s0 = wave_scan(slots), c0 = wave_scan(cuts);
+  const int cut_blocks = __builtin_amdgcn_readlane(c0, 63);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.counts != nullptr) a.counts[0] = cut_blocks;
   p0 -= parts, s0 -= slots, c0 -= cuts;
-  if (blockIdx.x == 0 && tid == 0 && a.counts != nullptr) a.counts[0] = ct;
-  __syncthreads();
   // pairs of parts (the two blocks of a token's 128 heads, most often) go to one XCD (blockIdx % 8), and
   // share its L2
   const int my = (int)(((blockIdx.x >> 4) * 8 + (blockIdx.x & 7)) * 2 + ((blockIdx.x >> 3) & 1));
-  if (my >= pt) return false;
-  if (my >= p0 && my < p0 + parts) {
+  const bool mine = my >= p0 && my < p0 + parts;
+  const uint64_t who = __ballot(mine);
+  if (who == 0) return false;
+  Work w{};
+  if (mine) {
     bool found = false;
-    each([&](int b, int n, int tiles) {
-      if (found) return;
+    each([&](int b, const Seq& q, int n, int tiles) {
       const int c = cut(tiles, quantum);
-      if (my < p0 + n * c) {
+      if (!found && my < p0 + n * c) {
         const int blk = (my - p0) / c, part = (my - p0) - blk * c;
-        sh[16] = b;
-        sh[17] = blk;
-        sh[18] = part;
-        sh[19] = c;
-        sh[20] = c > 1 ? s0 + blk * c + part : -1;
-        if (c > 1 && part == 0 && c0 + blk < a.max_cuts)
+        w = {q, b, blk, part, c, c > 1 ? s0 + blk * c + part : -1};
+        if (c > 1 && part == 0 && c0 + blk < a.max_cuts && threadIdx.x < 64)
           reinterpret_cast<Desc*>(a.counts + 4)[c0 + blk] = {b, blk, s0 + blk * c, c};
         found = true;
-        return;
       }
       p0 += n * c;
       if (c > 1) s0 += n * c, c0 += n;
     });
   }
-  __syncthreads();
-  work = {__builtin_amdgcn_readfirstlane(sh[16]), __builtin_amdgcn_readfirstlane(sh[17]),
-          __builtin_amdgcn_readfirstlane(sh[18]), __builtin_amdgcn_readfirstlane(sh[19]),
-          __builtin_amdgcn_readfirstlane(sh[20])};
-  __syncthreads();
+  const int src = __builtin_ctzll(who);
+  auto from = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+  work = {{from(w.seq.q0), from(w.seq.n), from(w.seq.len)}, from(w.index), from(w.block), from(w.part), from(w.parts),
+          from(w.slot)};
   // starts that are not rising could ask for more (nothing is promised for them)
   return work.slot < 0 || work.slot - work.part + work.parts <= a.max_slots;
 }
@@ -225,72 +215,108 @@ __device__ __forceinline__ bool find_work(const LatentAttnArgs& a, int* sh, Work
 struct Query {
   v8i hi[8], lo[8];
   v8bf rope[4];
-  int code;
+  int code;  // of hi in byte 0, of lo in byte 1
 };
-__device__ __forceinline__ void load_query(const uint16_t* src, bool row_ok, int g, Query& q) {
-  auto raw = [&](int ks, int j) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row_ok) v = *reinterpret_cast<const uint4*>(src + 64 * ks + 32 * (j >> 1) + 16 * g + 8 * (j & 1));
-    return v;
-  };
-  float amax = 0.f;
+// What a wave reads of its 32 rows: the latents of 4 of the 8 steps (the other wave of its pair reads
+// the rest).
+struct RawQuery {
+  uint4 lat[4][4];
+};
+__device__ __forceinline__ void read_query(const uint16_t* src, bool row_ok, int g, int half, RawQuery& x) {
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
+  for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float f[8];
-      bf16x8_values(raw(ks, j), f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(f[i]));
+      x.lat[ks][j] = make_uint4(0, 0, 0, 0);
+      if (row_ok)
+        x.lat[ks][j] = *reinterpret_cast<const uint4*>(src + 256 * half + 64 * ks + 32 * (j >> 1) + 16 * g + 8 * (j & 1));
     }
+}
+// `box`: 16 KB of LDS a wave, and one int a row and wave behind them.
+template <int kWaves>
+__device__ __forceinline__ void split_query(const RawQuery& x, int lane, int wave, uint8_t* box, Query& q) {
+  typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+  typedef short v2s __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  const int r = lane & 31;
+  // the largest magnitude: without its sign a bf16 pattern grows with its value, NaN last
+  v2us top = {0, 0};
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w[4] = {x.lat[ks][j].x, x.lat[ks][j].y, x.lat[ks][j].z, x.lat[ks][j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(v2us, w[i] & 0x7fff7fffu));
+    }
+  int bits = max((int)top[0], (int)top[1]);
+  const auto swapped = __builtin_amdgcn_permlane32_swap((unsigned)bits, (unsigned)bits, false, false);
+  bits = max((int)swapped[0], (int)swapped[1]);
+  int* tops = reinterpret_cast<int*>(box + kWaves * 16384);
+  if (lane < 32) tops[wave * 32 + r] = bits;
+  __syncthreads();
+  bits = max(bits, tops[(wave ^ 1) * 32 + r]);
+  // the least power of two that holds the row in e4m3 range (kept away from the ends of float32)
+  const float amax = __uint_as_float((uint32_t)bits << 16);
+  const bool finite = bits < 0x7f80;
+  const uint32_t code = finite ? (__float_as_uint(fmaxf(amax, 0x1p-80f) / 448.0f) + 0x7fffffu) >> 23 : 127;
+  const float scale = __uint_as_float(code << 23);
+  q.code = finite ? (int)(code | (code - 4) << 8) : 0xffff;  // a NaN row scores NaN
+  v4i* out = reinterpret_cast<v4i*>(box) + wave * 1024 + lane;
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row_ok) v = *reinterpret_cast<const uint4*>(src + kLatentDim + 16 * ks + 8 * g);
-    q.rope[ks] = __builtin_bit_cast(v8bf, v);
-  }
-  amax = max_nan(amax, __shfl_xor(amax, 32));
-  // the least power of two that holds the row in e4m3 range (kept away from the ends of float32)
-  uint32_t code = (__float_as_uint(max_nan(amax, 0x1p-80f) / 448.0f) + 0x7fffffu) >> 23;
-  const bool finite = amax < __builtin_inff();
-  if (!finite) code = 127;
-  const float inv = finite ? __uint_as_float((254u - code) << 23) : __builtin_nanf("");  // a NaN row scores NaN
-  q.code = (int)code;
-  asm volatile("" ::: "memory");  // the row is read a second time (from L2) rather than held in 128 registers
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
+    v8i hi, lo;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float f[8], back[8], lo[8];
-      bf16x8_values(raw(ks, j), f);
+      const uint32_t w[4] = {x.lat[ks][j].x, x.lat[ks][j].y, x.lat[ks][j].z, x.lat[ks][j].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= inv;
-      const uint2 hi = make_uint2(pack_e4m3(f), pack_e4m3(f + 4));
-      e4m3x8_values(hi, back);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) lo[i] = (f[i] - back[i]) * 16.f;
-      q.hi[ks][2 * j] = (int)hi.x;
-      q.hi[ks][2 * j + 1] = (int)hi.y;
-      q.lo[ks][2 * j] = (int)pack_e4m3(lo);
-      q.lo[ks][2 * j + 1] = (int)pack_e4m3(lo + 4);
+      for (int i = 0; i < 4; i += 2) {
+        v2s h = {0, 0}, l = {0, 0};
+        // (values over the scale, to nearest even; then what is left of them, exactly, over a sixteenth)
+        h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, w[i]), scale, false);
+        h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, w[i + 1]), scale, true);
+        const unsigned hb = __builtin_bit_cast(unsigned, h);
+        const v2f b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hb, scale, false);
+        const v2f b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hb, scale, true);
+        const float tiny = scale * 0.0625f;
+        l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, __uint_as_float(w[i] << 16) - b0[0],
+                                                     __uint_as_float(w[i] & 0xffff0000u) - b0[1], tiny, false);
+        l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, __uint_as_float(w[i + 1] << 16) - b1[0],
+                                                     __uint_as_float(w[i + 1] & 0xffff0000u) - b1[1], tiny, true);
+        hi[2 * j + (i >> 1)] = (int)hb;
+        lo[2 * j + (i >> 1)] = __builtin_bit_cast(int, l);
+      }
     }
+    out[(4 * ks) * 64] = __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
+    out[(4 * ks + 1) * 64] = __builtin_shufflevector(hi, hi, 4, 5, 6, 7);
+    out[(4 * ks + 2) * 64] = __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
+    out[(4 * ks + 3) * 64] = __builtin_shufflevector(lo, lo, 4, 5, 6, 7);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    const v4i* in = reinterpret_cast<const v4i*>(box) + ((wave & ~1) + (ks >> 2)) * 1024 + (ks & 3) * 256 + lane;
+    q.hi[ks] = __builtin_shufflevector(in[0], in[64], 0, 1, 2, 3, 4, 5, 6, 7);
+    q.lo[ks] = __builtin_shufflevector(in[128], in[192], 0, 1, 2, 3, 4, 5, 6, 7);
+  }
 }
 
 // kPairs pairs of waves, 32 query rows each. kAhead: a tile's scores and softmax run while the products of the
 // tile before with its values do, which takes a third tile of LDS.
 template <int kPairs, bool kAhead>
 __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttnArgs a) {
-  constexpr int kThreads = kPairs * 128, kBM = kPairs * 32, kWaves = kPairs * 2;
+  constexpr int kBM = kPairs * 32, kWaves = kPairs * 2;
   constexpr int kBuffers = kAhead ? 3 : 2;
-  __shared__ __align__(1024) uint8_t lds_tiles[kBuffers * kTileBytes];
+  // with room for it, the rotary part of the queries stays in LDS (4 KB a pair)
+  __shared__ __align__(1024) uint8_t lds_tiles[kBuffers * kTileBytes + (kAhead ? kPairs * 4096 : 0)];
   Work work;
-  if (!find_work<kThreads, kBM>(a, reinterpret_cast<int*>(lds_tiles), work)) return;
+  if (!find_work<kBM>(a, work)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;
   const int pair = wave >> 1, half = wave & 1;
-  Seq seq = sequence(a, work.seq);
-  seq = {__builtin_amdgcn_readfirstlane(seq.q0), __builtin_amdgcn_readfirstlane(seq.n),
-         __builtin_amdgcn_readfirstlane(seq.len)};
+  const Seq seq = work.seq;
   const int rows = (int)min((int64_t)seq.n * a.H - (int64_t)work.block * kBM, (int64_t)kBM);
 
   // ---- this lane's query row
@@ -320,13 +346,17 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
   float m = kNegInf, l = 0.f;
 
   if (t_begin < t_end) {
+    RawQuery raw;
+    const uint16_t* q_row = a.q + qtok * a.q_tok + (int64_t)head * a.q_head;
+    read_query(q_row, row_ok, g, half, raw);
     // ---- the page table and the scale codes are read ahead: lane L for key L of a tile
     // (no branches: a column past the table reads its last entry, or where it has none a length, and counts as none)
     const int width = a.cache.table_width;
-    const int32_t* table = width > 0 ? a.cache.table + (int64_t)work.seq * a.cache.table_stride : a.lens;
+    const int32_t* table = width > 0 ? a.cache.table + (int64_t)work.index * a.cache.table_stride : a.lens;
     const int page_size = a.cache.page_size;
-    const int step_col = kTile / page_size, step_off = kTile - step_col * page_size;
-    const int end_col = (keys - 1) / page_size, end_off = (keys - 1) - end_col * page_size;
+    auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    const int step_col = uniform(kTile / page_size), step_off = kTile - step_col * page_size;
+    const int end_col = uniform((keys - 1) / page_size), end_off = (keys - 1) - end_col * page_size;
     int col = (t_begin * kTile + lane) / page_size, off = (t_begin * kTile + lane) - col * page_size;
     // of a tile: the table's entry and the row in its page; keys past the end repeat the last (masked)
     auto look_up = [&](int& page, int& row_in_page) {
@@ -356,18 +386,29 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     constexpr int kCodeCopies = 32 / kWaves, kCopies = 40 / kWaves;
     // Two rows of codes a copy, lanes 32 .. 63 the second; eight rows of rotary keys. The XORs' lane parts
     // are the same for every copy, its own part a constant.
-    auto copy_piece = [&](uint32_t unit, uint32_t at, int j) {
+    struct Lanes {  // formed once a tile
+      int code_from, rope_from, code_at, rope_at;
+    };
+    auto lanes = [&] {
       const int ln = fresh(lane);
-      if (j < kCodeCopies) {
-        const int kk = wave * (2 * kCodeCopies) + 2 * j + (ln >> 5);
-        const uint64_t u = (uint32_t)__builtin_amdgcn_ds_bpermute(kk << 2, (int)unit);
-        copy16_from(a.cache.rows + u * 128 + (((ln & 31) ^ ((ln >> 5) << 1) ^ swz(2 * j)) << 4), at + (wave * kCodeCopies + j) * 1024);
-      } else {
-        const int jr = j - kCodeCopies, kk = wave * (64 / kWaves) + 8 * jr + (ln >> 3);
-        const uint64_t u = (uint32_t)__builtin_amdgcn_ds_bpermute(kk << 2, (int)unit);
-        copy16_from(a.cache.rows + u * 128 + kLatentDim + (((ln & 7) ^ (ln >> 3) ^ (jr & 1)) << 4),
+      Lanes x;
+      x.code_from = fresh((wave * (2 * kCodeCopies) + (ln >> 5)) << 2);
+      x.rope_from = fresh((wave * (64 / kWaves) + (ln >> 3)) << 2);
+      x.code_at = ((ln & 31) ^ ((ln >> 5) << 1)) << 4;
+      x.rope_at = ((ln & 7) ^ (ln >> 3)) << 4;
+      return x;
+    };
+    auto place_of = [&](const Lanes& x, uint32_t unit, int j) {  // the row's place, from the lane that looked it up
+      return (uint32_t)__builtin_amdgcn_ds_bpermute(
+          j < kCodeCopies ? x.code_from + 8 * j : x.rope_from + 32 * (j - kCodeCopies), (int)unit);
+    };
+    auto copy_piece = [&](const Lanes& x, uint32_t u, uint32_t at, int j) {
+      const int jr = j - kCodeCopies;
+      if (j < kCodeCopies)
+        copy16_from(a.cache.rows + (uint64_t)u * 128 + (x.code_at ^ (swz(2 * j) << 4)), at + (wave * kCodeCopies + j) * 1024);
+      else
+        copy16_from(a.cache.rows + (uint64_t)u * 128 + kLatentDim + (x.rope_at ^ ((jr & 1) << 4)),
                     at + kTile * kLatentDim + (wave * (8 / kWaves) + jr) * 1024);
-      }
     };
 
     int page, o, page_next, o_next, page_far, o_far;
@@ -377,16 +418,24 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     int code = code_of(page, o);  // of tile t
     {
       const uint32_t unit = unit_of(page, o);
+      const Lanes x = lanes();
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) copy_piece(unit, lds, j);
+      for (int j = 0; j < kCopies; ++j) copy_piece(x, place_of(x, unit, j), lds, j);
     }
     int code_next = code_of(page_next, o_next);  // of tile t + 1
     uint32_t unit_next = unit_of(page_next, o_next);
     Query q;
-    load_query(a.q + qtok * a.q_tok + (int64_t)head * a.q_head, row_ok, g, q);
-
-    const float c = a.scale * 1.44269504088896341f;
-    const int p_code = g == 0 ? 127 : 123, one = 127;  // slots of hi at 1, of lo at 2^-4
+    split_query<kWaves>(raw, lane, wave, lds_tiles + kTileBytes, q);
+    v4i* rope_box = reinterpret_cast<v4i*>(lds_tiles + kBuffers * kTileBytes) + pair * 256 + lane;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row_ok) v = *reinterpret_cast<const uint4*>(q_row + kLatentDim + 16 * ks + 8 * g);
+      if constexpr (kAhead) rope_box[ks * 64] = __builtin_bit_cast(v4i, v);  // (both waves of a pair write the same)
+      else q.rope[ks] = __builtin_bit_cast(v8bf, v);
+    }
+    const float c = __uint_as_float((uint32_t)uniform((int)__float_as_uint(a.scale * 1.44269504088896341f)));
+    const int p_base = 127 | (g == 0 ? 127 : 123) << 8;  // values at 1; slots of hi at 1, of lo at 2^-4
 
     // ---- scores of this wave's 32 keys of a tile; `between(step)` is called at each of 8 steps
     auto scores = [&](uint32_t tile, int tile_code, auto between) {
@@ -405,47 +454,58 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       auto rope = [&](int ks) {
         return __builtin_bit_cast(v8bf, *reinterpret_cast<lds_v4i*>(rb + ((rsw ^ (ks * 2)) << 4)));
       };
-      v8i k[3];
-      v8bf kr[4];
-      k[0] = key(0);
-      k[1] = key(1);
+      const uint32_t qr = lds + kBuffers * kTileBytes + pair * 4096 + fresh(lane) * 16;
+      auto q_rope = [&](int ks) {
+        if constexpr (kAhead) return __builtin_bit_cast(v8bf, *reinterpret_cast<lds_v4i*>(qr + ks * 1024));
+        else return q.rope[ks];
+      };
+      constexpr int kRing = kAhead ? 3 : 2;
+      v8i k[kRing];
+      v8bf kr[2], qk[2];
+#pragma unroll
+      for (int ks = 0; ks + 1 < kRing; ++ks) k[ks] = key(ks);
       v16f s;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        if (ks + 2 < 8) {
-          k[(ks + 2) % 3] = key(ks + 2);
-        } else {
-          kr[2 * (ks - 6)] = rope(2 * (ks - 6));
-          kr[2 * (ks - 6) + 1] = rope(2 * (ks - 6) + 1);
-        }
-        s = mfma_scaled(k[ks % 3], q.hi[ks], s, kc, q.code);
-        s = mfma_scaled(k[ks % 3], q.lo[ks], s, kc, q.code - 4);
+        if (ks + kRing - 1 < 8) k[(ks + kRing - 1) % kRing] = key(ks + kRing - 1);
+        if (ks >= 6) kr[ks - 6] = rope(ks - 6), qk[ks - 6] = q_rope(ks - 6);
+        s = mfma_scaled<0>(k[ks % kRing], q.hi[ks], s, kc, q.code);
+        s = mfma_scaled<1>(k[ks % kRing], q.lo[ks], s, kc, q.code);
         asm volatile("" : "+v"(s));  // the products stay here
         between(ks);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[ks], q.rope[ks], s, 0, 0, 0);
+      for (int ks = 0; ks < 4; ++ks) {
+        const v8bf x = kr[ks & 1], y = qk[ks & 1];
+        if (ks < 2) kr[ks] = rope(ks + 2), qk[ks] = q_rope(ks + 2);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, s, 0, 0, 0);
+      }
       return s;
     };
-    // ---- x = score in log2 + scale code of the key, its maximum, and the codes of keys 8 q + 4 g .. + 3
+    // ---- softmax of this lane's 16 scores, in pieces that fit between matrix products
     struct Soft {
-      v16f x;
-      uint32_t codes[4];
-      float ref;
+      v16f x;             // score in log2 + scale code of the key
+      uint32_t codes[4];  // of keys 8 q + 4 g .. + 3
+      float ref, sum;
+      int up;  // weights are 2^(x - ref); the accumulator's are 2^up times those
     };
-    // Returns the factor of a new running maximum (1: none).
-    auto soft_begin = [&](const v16f& s, int tile_code, int t, Soft& w) {
-      const int up = __builtin_amdgcn_mov_dpp(tile_code, 0xB1, 0xF, 0xF, true);          // the neighbour's: lanes 1 0 3 2
-      const int two = (lane & 1) ? (up | tile_code << 8) : (tile_code | up << 8);        // both lanes: even, odd
-      const int over = __builtin_amdgcn_mov_dpp(two, 0x4E, 0xF, 0xF, true);              // lanes 2 3 0 1
-      const int four = (lane & 2) ? (over | two << 16) : (two | over << 16);             // the quad's four codes
+    auto soft_codes = [&](int tile_code, Soft& w) {
+      const int up = __builtin_amdgcn_mov_dpp(tile_code, 0xB1, 0xF, 0xF, true);    // the neighbour's: lanes 1 0 3 2
+      const int two = (lane & 1) ? (up | tile_code << 8) : (tile_code | up << 8);  // both lanes: even, odd
+      const int over = __builtin_amdgcn_mov_dpp(two, 0x4E, 0xF, 0xF, true);        // lanes 2 3 0 1
+      const int four = (lane & 2) ? (over | two << 16) : (two | over << 16);       // the quad's four codes
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) w.codes[q4] = (uint32_t)__shfl(four, half * 32 + 8 * q4 + 4 * g);
+      for (int q4 = 0; q4 < 4; ++q4)
+        w.codes[q4] = (uint32_t)__builtin_amdgcn_ds_bpermute(((half * 32 + 4 * g) << 2) + 32 * q4, four);
+    };
+    auto soft_x = [&](const v16f& s, Soft& w) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) w.x[i] = fmaf(s[i], c, (float)((w.codes[i >> 2] >> (8 * (i & 3))) & 0xffu));
+    };
+    auto soft_mask = [&](int t, Soft& w) {
       const int k0 = t * kTile + half * 32;
       if (k0 + 32 > all) {
         const int left = limit - k0 - 4 * g;
@@ -453,36 +513,42 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
         for (int i = 0; i < 16; ++i)
           if (8 * (i >> 2) + (i & 3) >= left) w.x[i] = kNegInf;
       }
+    };
+    // Returns the factor of a new reference (1: none).
+    auto soft_top = [&](Soft& w) {
       float top = w.x[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = fmaxf(top, w.x[i]);
-      top = fmaxf(top, __shfl_xor(top, 32));
-      float f = 1.f;
-      if (__any(top > m + kSlack)) {
-        const float next = fmaxf(m, top);
-        f = m == next ? 1.f : __builtin_amdgcn_exp2f(m - next);  // (m = next = -inf: nothing yet)
-        m = next;
-        l *= f;
-      }
-      w.ref = m == kNegInf ? 0.f : m - kTop;
+      const unsigned bits = __float_as_uint(top);
+      const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+      top = ceilf(fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])));
+      const bool higher = top > m + kSlack;  // also at the first key that the row sees (m = -inf)
+      const float f = higher && m > kNegInf ? __builtin_amdgcn_exp2f(m - top) : 1.f;
+      m = higher ? top : m;
+      l *= f;
+      const float base = m == kNegInf ? 0.f : m;
+      w.ref = fmaxf(top, base - kFar) - kTop;
+      w.up = (int)(w.ref - base);
+      w.sum = 0.f;
       return f;
     };
-    // Weights of four keys (quad q4), into the operand.
-    auto soft_quad = [&](const Soft& w, int q4, v8i& pw) {
-      float p[4], rest[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(w.x[4 * q4 + i] - w.ref);
-        // times 2^-e (a masked key's p is 0, whatever its code)
-        l += __builtin_amdgcn_ldexpf(p[i], 127 - (int)((w.codes[q4] >> (8 * i)) & 0xffu));
+    // Weights of keys 2 k and 2 k + 1, into the operand.
+    auto soft_pair = [&](Soft& w, int k, v8i& pw) {
+      typedef float v2f __attribute__((ext_vector_type(2)));
+      const int q4 = k >> 1;
+      const float p0 = __builtin_amdgcn_exp2f(w.x[2 * k] - w.ref), p1 = __builtin_amdgcn_exp2f(w.x[2 * k + 1] - w.ref);
+      // times 2^-e (a masked key's p is 0, whatever its code)
+      w.sum += __builtin_amdgcn_ldexpf(p0, 127 - (int)((w.codes[q4] >> (16 * (k & 1))) & 0xffu));
+      w.sum += __builtin_amdgcn_ldexpf(p1, 127 - (int)((w.codes[q4] >> (16 * (k & 1) + 8)) & 0xffu));
+      if (k & 1) {
+        pw[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(p0, p1, pw[q4], true);
+        const v2f back = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)pw[q4], 16.f, true);  // 16 times
+        pw[4 + q4] = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(p0, 16.f, -back[0]), fmaf(p1, 16.f, -back[1]), pw[4 + q4], true);
+      } else {
+        pw[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(p0, p1, 0, false);
+        const v2f back = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)pw[q4], 16.f, false);
+        pw[4 + q4] = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(p0, 16.f, -back[0]), fmaf(p1, 16.f, -back[1]), 0, false);
       }
-      const int h = (int)pack_e4m3(p);
-      rest[0] = (p[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 16.f;
-      rest[1] = (p[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 16.f;
-      rest[2] = (p[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 16.f;
-      rest[3] = (p[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 16.f;
-      pw[q4] = h;
-      pw[4 + q4] = (int)pack_e4m3(rest);
     };
     auto rescale = [&](float f) {
       if (__any(f != 1.f)) {
@@ -495,33 +561,34 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
         }
       }
     };
-    // ---- O^T += V^T P^T, 32 value columns at a time; `between(d)` is called at each of 16 steps
-    auto values = [&](uint32_t tile, const v8i& pw, auto between) {
+    // ---- O^T += V^T P^T, 32 value columns at a time: accumulator d is columns 32 (d ^ 8 half) .. + 31, so
+    // that the first 8 are those that the wave joins at the end; `between(d)` is called at each of 16 steps
+    auto values = [&](uint32_t tile, const v8i& pw, int p_code, auto between) {
       typedef __attribute__((address_space(3))) v2i lds_v2i;
       const int ln = fresh(lane);
       const int vk = half * 32 + 8 * ((ln >> 3) & 1) + 4 * g + ((ln >> 1) & 3);  // the row this lane addresses (and vk + 16)
       const uint32_t vb = tile + vk * kLatentDim + 8 * (ln & 1);
-      const int sw = ((ln >> 4) & 1) ^ swz(vk);
-      v2i x[3], y[3];
+      const int sw = ((ln >> 4) & 1) ^ swz(vk) ^ (16 * half);
+      v2i x[2], y[2];
       auto value = [&](int d) {
         const uint32_t at = vb + ((sw ^ (2 * d)) << 4);
-        x[d % 3] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at));
-        y[d % 3] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at + 16 * kLatentDim));
+        x[d % 2] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at));
+        y[d % 2] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at + 16 * kLatentDim));
       };
       value(0);
-      value(1);
 #pragma unroll
       for (int d = 0; d < 16; ++d) {
-        if (d + 2 < 16) value(d + 2);
-        const v2i u = x[d % 3], w = y[d % 3];
+        if (d + 1 < 16) value(d + 1);
+        const v2i u = x[d % 2], w = y[d % 2];
         const v8i v = {u[0], u[1], w[0], w[1], u[0], u[1], w[0], w[1]};
-        mfma_scaled_acc(v, pw, acc[d], one, p_code);
+        mfma_scaled_acc(v, pw, acc[d], p_code);
         between(d);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
 
     v8i pw;
+    int p_code = 127;
     uint32_t tile = lds, tile_before = lds;
     int place = 0;
     // Tile t: everything up to the weights; kFirst: there is no tile before it in this part.
@@ -537,12 +604,21 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       const int tile_code = code;
       code = code_next;
       // (after the last tile the copies bring one that is not used: there always is a key to look up)
-      constexpr int kSteps = 4, kEach = (kCopies + kSteps - 1) / kSteps;
+      constexpr int kSteps = 4, kEach = kCopies / kSteps + (kCopies % kSteps != 0), kFirstPlaces = kEach;
+      uint32_t places[kCopies];
+      const Lanes at = lanes();
+#pragma unroll
+      for (int j = 0; j < kFirstPlaces && j < kCopies; ++j) places[j] = place_of(at, unit, j);
+      Soft w;
+      soft_codes(tile_code, w);
       const v16f s = scores(tile, tile_code, [&](int ks) {
         if (ks < kSteps) {
 #pragma unroll
-          for (int j = 0; j < kEach; ++j)
-            if (ks * kEach + j < kCopies) copy_piece(unit, next_tile, ks * kEach + j);
+          for (int j = 0; j < kEach; ++j) {
+            if (ks * kEach + j < kCopies) copy_piece(at, places[ks * kEach + j], next_tile, ks * kEach + j);
+            const int far = ks * kEach + j + kFirstPlaces;
+            if (far < kCopies) places[far] = place_of(at, unit, far);
+          }
         }
         if (ks == kSteps) {
           unit_next = unit_of(page_far, o_far);
@@ -550,26 +626,28 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
           look_up(page_far, o_far);
         }
       });
-      Soft w;
-      const float f = soft_begin(s, tile_code, t, w);
-      if constexpr (kAhead) {
+      if constexpr (kAhead && !kFirst) {
         v8i next;
-        if constexpr (kFirst) {
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) soft_quad(w, q4, next);
-        } else {
-          values(tile_before, pw, [&](int d) {
-            if ((d & 3) == 3) soft_quad(w, d >> 2, next);
-          });
-          rescale(f);
-        }
+        float f;
+        values(tile_before, pw, p_code, [&](int d) {
+          if (d == 0) soft_x(s, w);
+          if (d == 1) soft_mask(t, w);
+          if (d == 2) f = soft_top(w);
+          if (d >= 3 && d < 11) soft_pair(w, d - 3, next);
+        });
+        rescale(f);
         pw = next;
       } else {
-        rescale(f);
+        soft_x(s, w);
+        soft_mask(t, w);
+        const float f = soft_top(w);
+        if constexpr (!kAhead) rescale(f);  // (the first tile's factor is 1)
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) soft_quad(w, q4, pw);
-        values(tile, pw, [](int) {});
+        for (int k = 0; k < 8; ++k) soft_pair(w, k, pw);
       }
+      p_code = p_base + (w.up << 8);
+      if constexpr (!kAhead) values(tile, pw, p_code, [](int) {});
+      l += __builtin_amdgcn_ldexpf(w.sum, w.up);
       tile_before = tile;
       tile = next_tile;
       place = next_place;
@@ -577,7 +655,7 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     if constexpr (kAhead) {
       step(t_begin, std::true_type{});
       for (int t = t_begin + 1; t < t_end; ++t) step(t, std::false_type{});
-      values(tile_before, pw, [](int) {});
+      values(tile_before, pw, p_code, [](int) {});
     } else {
       for (int t = t_begin; t < t_end; ++t) step(t, std::false_type{});
     }
@@ -600,51 +678,60 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
   const float f0 = m0 == m_all ? 1.f : __builtin_amdgcn_exp2f(m0 - m_all);
   const float f1 = m1 == m_all ? 1.f : __builtin_amdgcn_exp2f(m1 - m_all);
   const float l_all = fmaf(f1, l1, f0 * l0);
-  const float inv = l_all == 0.f ? 0.f : 1.0f / l_all;  // a row that sees no key is zero
-  const float f_own = half ? f1 : f0, f_other = half ? f0 : f1;
   const bool whole = work.slot < 0;
+  const float inv = !whole ? 1.f : l_all == 0.f ? 0.f : 1.0f / l_all;  // a row that sees no key is zero
+  const float f_own = (half ? f1 : f0), f_other = (half ? f0 : f1);
   const int64_t state_row = (int64_t)work.slot * kBM + row;
-  uint16_t* dst = a.out + qtok * a.o_tok + (int64_t)head * a.o_head + 4 * g;
-  float* state = a.states + state_row * kLatentDim + 4 * g;
   if (!whole && half == 0 && g == 0 && row_ok) {
     a.stats[state_row * 2] = m_all;
     a.stats[state_row * 2 + 1] = l_all;
   }
+  uint16_t* dst = a.out + qtok * a.o_tok + (int64_t)head * a.o_head + 256 * half;
+  float* state = a.states + state_row * kLatentDim + 256 * half;
   v4f* box = reinterpret_cast<v4f*>(lds_tiles);  // 16 KB a wave
-  auto send = [&](const v16f& x, int d) {
-#pragma unroll
-    for (int q4 = 0; q4 < 4; ++q4)
-      box[(wave * 16 + d * 4 + q4) * 64 + lane] = v4f{x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]};
-  };
-  auto join = [&](const v16f& x, int d, int column) {
-#pragma unroll
-    for (int q4 = 0; q4 < 4; ++q4) {
-      const v4f y = box[((wave ^ 1) * 16 + d * 4 + q4) * 64 + lane];
-      v4f o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(f_other, y[i], f_own * x[4 * q4 + i]);
-      if (!row_ok) continue;
-      const int at = column + 8 * q4;
-      if (whole)
-        *reinterpret_cast<uint2*>(dst + at) =
-            make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-      else
-        *reinterpret_cast<v4f*>(state + at) = o;
-    }
-  };
 #pragma unroll
   for (int step = 0; step < 2; ++step) {
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      if (half == 0) send(acc[8 + 4 * step + d], d);
-      else send(acc[4 * step + d], d);
+      const v16f x = acc[8 + 4 * step + d];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4)
+        box[(wave * 16 + d * 4 + q4) * 64 + lane] = v4f{x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]};
     }
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      if (half == 0) join(acc[4 * step + d], d, 32 * (4 * step + d));
-      else join(acc[8 + 4 * step + d], d, 32 * (8 + 4 * step + d));
+      const v16f x = acc[4 * step + d];
+      v4f o[4];  // columns 8 q + 4 g .. + 3 of 32
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        const v4f y = box[((wave ^ 1) * 16 + d * 4 + q4) * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[q4][i] = fmaf(f_other, y[i], f_own * x[4 * q4 + i]) * inv;
+      }
+      const int column = 32 * (4 * step + d);
+      if (whole) {
+        // lanes g = 0 and 1 of a row swap quads, so that each stores 16 neighbouring columns
+        uint32_t u[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const auto v = __builtin_amdgcn_permlane32_swap(pack_bf16(o[h][2 * i], o[h][2 * i + 1]),
+                                                            pack_bf16(o[2 + h][2 * i], o[2 + h][2 * i + 1]), false, false);
+            u[h][i] = v[0];
+            u[h][2 + i] = v[1];
+          }
+        if (row_ok) {
+          uint4* p = reinterpret_cast<uint4*>(dst + column + 16 * g);
+          p[0] = make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]);
+          p[1] = make_uint4(u[1][0], u[1][1], u[1][2], u[1][3]);
+        }
+      } else if (row_ok) {
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) *reinterpret_cast<v4f*>(state + column + 8 * q4 + 4 * g) = o[q4];
+      }
     }
   }
 }
