@@ -20,16 +20,17 @@
 //     denominator sums 2^(x_j) 2^(-e_j) in float32.
 // The products are formed transposed (S^T = K Q^T, O^T = V^T P^T) with 32x32x64 instructions: a
 // lane holds 16 scores of one query row, r = lane % 32, for keys 8 q + 4 g + i (g = lane / 32),
-// which are at once its operand of the second product. hi and lo fill the two halves of that
-// product's 64 slots (the lo half under a scale of 2^-4), against the same 16 value bytes twice.
-// Values are read from the key tile with transposing LDS reads.
+// which are at once its operand of the second product. Values are read from the key tile with
+// transposing LDS reads.
 //
-// A workgroup holds 32 query rows a pair of waves; the two waves of a pair take 32 keys each of a
-// 64-key tile with maxima and sums of their own, and join when the block's keys are done. So a
-// wave's 32 rows x 512 columns of float32 accumulator fill its 256 accumulation registers, the
-// queries' two terms 144 of the others, and a key byte read from LDS serves 32 rows: the LDS
-// reads of a tile (36 KB a wave) take about half the clocks of its matrix products (16 rows a wave
-// and 64 keys each, without the pairs, would read 72 KB for half the products).
+// A workgroup holds 32 query rows a pair of waves and walks tiles of 64 keys. Of each tile a wave
+// scores 32 keys; the two waves of a pair then exchange their weights through LDS, and each
+// multiplies all 64 with 256 of the 512 value columns. So the accumulator takes 128 accumulation
+// registers, the queries' two terms 128 others, and both products read a key byte from LDS for 32
+// rows. There is one wave a SIMD, which issues an instruction every 4 clocks at best, so the kernel
+// is bound by its instruction count as much as by the matrix cores: tile t's softmax runs between
+// the value products of tile t - 1 (whose weights crossed at t's only barrier), copies between its
+// score products, and the LDS layout (below) leaves all but a few addresses to constant offsets.
 //
 // Work is cut on the device, where the lengths are: a block is the query rows (tokens x heads)
 // of one sequence that a workgroup holds, and where there are fewer blocks than workgroups fit
@@ -46,20 +47,26 @@ namespace bfp8 {
 namespace {
 
 constexpr int kTile = 64;                  // keys of a tile
-constexpr int kTileBytes = kTile * kLatentRow;
+// A tile in LDS. Codes: pairs of rows, 1024 + 32 bytes apart, the 16-byte columns of the odd row XORed with
+// 5: no bank conflicts for the score reads (16 lanes: one column of 16 consecutive keys) and the transposing
+// value reads (32 lanes: two columns of 8 keys that differ in bits 0, 1 and 3), while the column of a later
+// step lies a constant further on (the XOR's bit 2 swaps neighbouring steps, which takes two addresses).
+// Rotary keys: groups of 8 rows of 128 bytes, 1024 + 64 bytes apart, columns XORed with (row / 2) % 4.
+constexpr int kPairStride = 1024 + 32, kRopeStride = 1024 + 64;
+constexpr int kRopeAt = kTile / 2 * kPairStride;
+constexpr int kTileBytes = kRopeAt + kTile / 8 * kRopeStride;
+constexpr int kBuffers = 3;                // tile t - 1 (values), t, and t + 1 on its way
+constexpr int kWeightBytes = 2 * 2048;     // a wave's weights of 32 keys (two terms), for two tiles in turn
+constexpr int kRefBytes = 2 * 128;         // their exponents
+constexpr int kKeyBytes = 2 * 256;         // a wave's scale codes of a tile as floats, and 2^-e
 constexpr float kSlack = 32.f;             // weights may pass the accumulator's reference by a factor of 2^kSlack
 constexpr float kTop = 8.f;                // the largest of 32 weights is held at 2^(kTop - 1) .. 2^kTop <= 448
-constexpr float kFar = 100.f;              // weights 2^-kFar below the reference are held relative to that
+constexpr float kNone = -1e30f;            // exponent of no weight at all
 constexpr float kNegInf = -__builtin_inff();
 
 struct Desc {  // a block that was cut: rows of block `block`, partial states slot .. slot + parts - 1
   int seq, block, slot, parts;
 };
-
-// XOR of the 16-byte columns of a key's 512-byte row in LDS. Conflict-free both for the score
-// reads (16 lanes: one column of 16 keys that differ in bits 0 .. 3) and for the transposing value
-// reads (32 lanes: two neighbouring columns of 8 keys that differ in bits 0, 1 and 3).
-__device__ __forceinline__ int swz(int key) { return ((key & 3) << 1) | (key & 8) | ((key >> 2) & 1); }
 
 // Scale codes: ea's low byte and byte kByte of eb.
 template <int kByte>
@@ -67,20 +74,24 @@ __device__ __forceinline__ v16f mfma_scaled(const v8i& a, const v8i& b, const v1
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, ea, kByte, eb);
 }
 
-// The same product added to an accumulator in the accumulation registers. Written in assembly so that it
-// stays there: the compiler otherwise moves accumulators between the two register files in bulk. The
-// wait in front covers operands that vector instructions have just written.
-// Scale codes: byte 0 of `codes` for a, byte 1 for b.
+// The same product added to an accumulator in the accumulation registers, written in assembly so that it
+// stays there (the compiler otherwise moves accumulators between the two register files in bulk). The
+// wait in front of the first term's covers operands that vector instructions have just written; the second
+// term's product follows it with the same values. Scale codes: byte 0 of `codes` for a, byte 1 (kLow: 2) for b.
+template <bool kLow>
 __device__ __forceinline__ void mfma_scaled_acc(const v8i& a, const v8i& b, v16f& c, int codes) {
-  asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %3 op_sel:[0,1,0] op_sel_hi:[0,0,0]"
-      : "+a"(c)
-      : "v"(a), "v"(b), "v"(codes));
+  if constexpr (kLow)
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %3 op_sel_hi:[0,1,0]"
+                 : "+a"(c)
+                 : "v"(a), "v"(b), "v"(codes));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %3 op_sel:[0,1,0] op_sel_hi:[0,0,0]"
+                 : "+a"(c)
+                 : "v"(a), "v"(b), "v"(codes));
 }
-// A value that the compiler takes as new here: what is computed from it is formed where it is used, not
-// kept in registers across a loop.
-__device__ __forceinline__ int fresh(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
+// copy16_from without saving M0, which nothing else in this kernel uses (gfx9 LDS instructions do not read it).
+__device__ __forceinline__ void copy16_m0(const uint8_t* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(lds) : "memory");
 }
 // Keeps an accumulator in the accumulation registers at this point.
 __device__ __forceinline__ void keep_acc(v16f& c) { asm volatile("" : "+a"(c)); }
@@ -303,14 +314,13 @@ __device__ __forceinline__ void split_query(const RawQuery& x, int lane, int wav
   }
 }
 
-// kPairs pairs of waves, 32 query rows each. kAhead: a tile's scores and softmax run while the products of the
-// tile before with its values do, which takes a third tile of LDS.
-template <int kPairs, bool kAhead>
+// kPairs pairs of waves, 32 query rows each.
+template <int kPairs>
 __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttnArgs a) {
   constexpr int kBM = kPairs * 32, kWaves = kPairs * 2;
-  constexpr int kBuffers = kAhead ? 3 : 2;
-  // with room for it, the rotary part of the queries stays in LDS (4 KB a pair)
-  __shared__ __align__(1024) uint8_t lds_tiles[kBuffers * kTileBytes + (kAhead ? kPairs * 4096 : 0)];
+  constexpr int kWeightsAt = kBuffers * kTileBytes, kRefsAt = kWeightsAt + kWaves * kWeightBytes;
+  constexpr int kKeysAt = kRefsAt + kWaves * kRefBytes;
+  __shared__ __align__(1024) uint8_t lds_tiles[kKeysAt + kWaves * kKeyBytes];
   Work work;
   if (!find_work<kBM>(a, work)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -328,182 +338,134 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
   // keys the row sees: its sequence up to itself
   const int limit = row_ok ? min(max(seq.len - seq.n + tok + 1, 0), seq.len) : 0;
   // keys the block sees (its last row's), cut into parts of whole tiles
-  const int last_tok = (work.block * kBM + rows - 1) / a.H;
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int last_tok = uniform((work.block * kBM + rows - 1) / a.H);
   const int keys = min(max(seq.len - seq.n + last_tok + 1, 0), seq.len);
   const int tiles = (keys + kTile - 1) / kTile;
-  const int t_begin = (int)((int64_t)tiles * work.part / work.parts);
-  const int t_end = (int)((int64_t)tiles * (work.part + 1) / work.parts);
+  const int t_begin = uniform((int)((int64_t)tiles * work.part / work.parts));
+  const int t_end = uniform((int)((int64_t)tiles * (work.part + 1) / work.parts));
   // keys that every row of the block sees: tiles before need no mask
-  const int all = rows == kBM ? min(max(seq.len - seq.n + work.block * kBM / a.H + 1, 0), seq.len) : 0;
+  const int first_tok = uniform(work.block * kBM / a.H);
+  const int all = rows == kBM ? min(max(seq.len - seq.n + first_tok + 1, 0), seq.len) : 0;
 
-  v16f acc[16];
+  v16f acc[8];  // columns 256 half + 32 d .. + 31
 #pragma unroll
-  for (int d = 0; d < 16; ++d) {
+  for (int d = 0; d < 8; ++d) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
     keep_acc(acc[d]);
   }
-  float m = kNegInf, l = 0.f;
+  // The accumulator's weights are relative to 2^m (the same in both waves of a pair); l sums this wave's keys.
+  float m = kNone, l = 0.f;
+  const uint32_t lds = lds_addr(lds_tiles);
 
   if (t_begin < t_end) {
-    RawQuery raw;
     const uint16_t* q_row = a.q + qtok * a.q_tok + (int64_t)head * a.q_head;
+    RawQuery raw;
     read_query(q_row, row_ok, g, half, raw);
     // ---- the page table and the scale codes are read ahead: lane L for key L of a tile
     // (no branches: a column past the table reads its last entry, or where it has none a length, and counts as none)
     const int width = a.cache.table_width;
     const int32_t* table = width > 0 ? a.cache.table + (int64_t)work.index * a.cache.table_stride : a.lens;
     const int page_size = a.cache.page_size;
-    auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     const int step_col = uniform(kTile / page_size), step_off = kTile - step_col * page_size;
     const int end_col = uniform((keys - 1) / page_size), end_off = (keys - 1) - end_col * page_size;
-    int col = (t_begin * kTile + lane) / page_size, off = (t_begin * kTile + lane) - col * page_size;
-    // of a tile: the table's entry and the row in its page; keys past the end repeat the last (masked)
-    auto look_up = [&](int& page, int& row_in_page) {
-      const bool past = col > end_col || (col == end_col && off > end_off);
+    int key = t_begin * kTile + lane, col = key / page_size, off = key - col * page_size;
+    // Of a tile: the table's entry (valid: whether the table has one) and the row in its page; keys past the end
+    // repeat the last (masked). What is loaded is not touched before the next tile's wait.
+    struct Entry {
+      int page, row, valid;
+    };
+    auto look_up = [&](Entry& x) {
+      const bool past = key >= keys;
       const int at = past ? end_col : col;
-      row_in_page = past ? end_off : off;
-      const int entry = table[min(at, max(width - 1, 0))];
-      page = at < width ? entry : -1;
+      x.row = past ? end_off : off;
+      x.page = table[min(at, max(width - 1, 0))];
+      x.valid = at < width;
+      key += kTile;
       col += step_col;
       off += step_off;
-      if (off >= page_size) off -= page_size, ++col;
+      const bool wrap = off >= page_size;
+      off -= wrap ? page_size : 0;
+      col += wrap ? 1 : 0;
     };
-    auto bad = [&](int page) { return page < 0 || page >= a.cache.pages; };
     const uint32_t page_units = (uint32_t)(a.cache.page_stride / 128);
-    // the row's place in 128-byte units; a page that does not exist reads page 0 ...
-    auto unit_of = [&](int page, int o) {
-      const bool none = bad(page);
-      return (uint32_t)(none ? 0 : page) * page_units + (uint32_t)(none ? 0 : o) * (kLatentRow / 128);
+    // A row's place in 128-byte units, and its scale code as loaded; for a page that does not exist page 0's
+    // first row, under the code of NaN.
+    struct Row {
+      uint32_t unit;
+      int byte, none;
     };
-    auto code_of = [&](int page, int o) {  // ... under the code of NaN
-      const bool none = bad(page);
-      const int byte = a.cache.scales[(int64_t)(none ? 0 : page) * a.cache.scale_stride + (none ? 0 : o)];
-      return none ? 255 : byte;
+    auto row_of = [&](const Entry& x) {
+      const bool none = !x.valid || (unsigned)x.page >= (unsigned)a.cache.pages;
+      const int p = none ? 0 : x.page, o = none ? 0 : x.row;
+      return Row{(uint32_t)p * page_units + (uint32_t)o * (kLatentRow / 128),
+                 a.cache.scales[(int64_t)p * a.cache.scale_stride + o], none ? 255 : 0};
     };
-    // ---- copies of a tile: 64 x 512 bytes of codes, then 64 x 128 bytes of rotary keys
-    const uint32_t lds = lds_addr(lds_tiles);
+    // ---- copies of a tile. Two rows of codes a copy, lanes 32 .. 63 the second; eight rows of rotary keys.
     constexpr int kCodeCopies = 32 / kWaves, kCopies = 40 / kWaves;
-    // Two rows of codes a copy, lanes 32 .. 63 the second; eight rows of rotary keys. The XORs' lane parts
-    // are the same for every copy, its own part a constant.
-    struct Lanes {  // formed once a tile
-      int code_from, rope_from, code_at, rope_at;
-    };
-    auto lanes = [&] {
-      const int ln = fresh(lane);
-      Lanes x;
-      x.code_from = fresh((wave * (2 * kCodeCopies) + (ln >> 5)) << 2);
-      x.rope_from = fresh((wave * (64 / kWaves) + (ln >> 3)) << 2);
-      x.code_at = ((ln & 31) ^ ((ln >> 5) << 1)) << 4;
-      x.rope_at = ((ln & 7) ^ (ln >> 3)) << 4;
-      return x;
-    };
-    auto place_of = [&](const Lanes& x, uint32_t unit, int j) {  // the row's place, from the lane that looked it up
+    const uint8_t* code_src = a.cache.rows + (((lane & 31) ^ ((lane >> 5) * 5)) << 4);
+    const uint8_t* rope_src = a.cache.rows + kLatentDim + (((lane & 7) ^ ((lane >> 4) & 3)) << 4);
+    const int code_from = (wave * (2 * kCodeCopies) + (lane >> 5)) << 2, rope_from = (wave * (64 / kWaves) + (lane >> 3)) << 2;
+    auto place_of = [&](uint32_t unit, int j) {  // the row's place, from the lane that looked it up
       return (uint32_t)__builtin_amdgcn_ds_bpermute(
-          j < kCodeCopies ? x.code_from + 8 * j : x.rope_from + 32 * (j - kCodeCopies), (int)unit);
+          j < kCodeCopies ? code_from + 8 * j : rope_from + 32 * (j - kCodeCopies), (int)unit);
     };
-    auto copy_piece = [&](const Lanes& x, uint32_t u, uint32_t at, int j) {
+    auto copy_piece = [&](uint32_t u, uint32_t at, int j) {
       const int jr = j - kCodeCopies;
-      if (j < kCodeCopies)
-        copy16_from(a.cache.rows + (uint64_t)u * 128 + (x.code_at ^ (swz(2 * j) << 4)), at + (wave * kCodeCopies + j) * 1024);
-      else
-        copy16_from(a.cache.rows + (uint64_t)u * 128 + kLatentDim + (x.rope_at ^ ((jr & 1) << 4)),
-                    at + kTile * kLatentDim + (wave * (8 / kWaves) + jr) * 1024);
+      if (j < kCodeCopies) copy16_m0(code_src + (uint64_t)u * 128, at + (wave * kCodeCopies + j) * kPairStride);
+      else copy16_m0(rope_src + (uint64_t)u * 128, at + kRopeAt + (wave * (8 / kWaves) + jr) * kRopeStride);
     };
 
-    int page, o, page_next, o_next, page_far, o_far;
-    look_up(page, o);
-    look_up(page_next, o_next);
-    look_up(page_far, o_far);
-    int code = code_of(page, o);  // of tile t
+    Entry here, next, far;
+    look_up(here);
+    look_up(next);
+    look_up(far);  // of tile t + 2
+    int code;      // of tile t
     {
-      const uint32_t unit = unit_of(page, o);
-      const Lanes x = lanes();
+      const Row x = row_of(here);
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) copy_piece(x, place_of(x, unit, j), lds, j);
+      for (int j = 0; j < kCopies; ++j) copy_piece(place_of(x.unit, j), lds, j);
+      code = x.byte | x.none;
     }
-    int code_next = code_of(page_next, o_next);  // of tile t + 1
-    uint32_t unit_next = unit_of(page_next, o_next);
+    Row ahead = row_of(next);  // of tile t + 1
     Query q;
     split_query<kWaves>(raw, lane, wave, lds_tiles + kTileBytes, q);
-    v4i* rope_box = reinterpret_cast<v4i*>(lds_tiles + kBuffers * kTileBytes) + pair * 256 + lane;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (row_ok) v = *reinterpret_cast<const uint4*>(q_row + kLatentDim + 16 * ks + 8 * g);
-      if constexpr (kAhead) rope_box[ks * 64] = __builtin_bit_cast(v4i, v);  // (both waves of a pair write the same)
-      else q.rope[ks] = __builtin_bit_cast(v8bf, v);
+      q.rope[ks] = __builtin_bit_cast(v8bf, v);
     }
     const float c = __uint_as_float((uint32_t)uniform((int)__float_as_uint(a.scale * 1.44269504088896341f)));
-    const int p_base = 127 | (g == 0 ? 127 : 123) << 8;  // values at 1; slots of hi at 1, of lo at 2^-4
 
-    // ---- scores of this wave's 32 keys of a tile; `between(step)` is called at each of 8 steps
-    auto scores = [&](uint32_t tile, int tile_code, auto between) {
-      const int kc = __shfl(tile_code, half * 32 + r);
-      const int kk = fresh(half * 32 + r);
-      typedef __attribute__((address_space(3))) const v4i lds_v4i;
-      const uint32_t kb = tile + kk * kLatentDim;
-      const int sw = g ^ swz(kk);
-      auto key = [&](int ks) {
-        const v4i x = *reinterpret_cast<lds_v4i*>(kb + ((sw ^ (ks * 4)) << 4));
-        const v4i y = *reinterpret_cast<lds_v4i*>(kb + ((sw ^ (ks * 4 + 2)) << 4));
-        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-      };
-      const uint32_t rb = tile + kTile * kLatentDim + kk * 128;
-      const int rsw = g ^ lds_swizzle(kk);
-      auto rope = [&](int ks) {
-        return __builtin_bit_cast(v8bf, *reinterpret_cast<lds_v4i*>(rb + ((rsw ^ (ks * 2)) << 4)));
-      };
-      const uint32_t qr = lds + kBuffers * kTileBytes + pair * 4096 + fresh(lane) * 16;
-      auto q_rope = [&](int ks) {
-        if constexpr (kAhead) return __builtin_bit_cast(v8bf, *reinterpret_cast<lds_v4i*>(qr + ks * 1024));
-        else return q.rope[ks];
-      };
-      constexpr int kRing = kAhead ? 3 : 2;
-      v8i k[kRing];
-      v8bf kr[2], qk[2];
-#pragma unroll
-      for (int ks = 0; ks + 1 < kRing; ++ks) k[ks] = key(ks);
-      v16f s;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        if (ks + kRing - 1 < 8) k[(ks + kRing - 1) % kRing] = key(ks + kRing - 1);
-        if (ks >= 6) kr[ks - 6] = rope(ks - 6), qk[ks - 6] = q_rope(ks - 6);
-        s = mfma_scaled<0>(k[ks % kRing], q.hi[ks], s, kc, q.code);
-        s = mfma_scaled<1>(k[ks % kRing], q.lo[ks], s, kc, q.code);
-        asm volatile("" : "+v"(s));  // the products stay here
-        between(ks);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const v8bf x = kr[ks & 1], y = qk[ks & 1];
-        if (ks < 2) kr[ks] = rope(ks + 2), qk[ks] = q_rope(ks + 2);
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, s, 0, 0, 0);
-      }
-      return s;
-    };
+    // ---- LDS addresses within a tile
+    typedef __attribute__((address_space(3))) const v4i lds_v4i;
+    typedef __attribute__((address_space(3))) v4i lds_w4i;
+    typedef __attribute__((address_space(3))) const v4f lds_v4f;
+    typedef __attribute__((address_space(3))) float lds_f;
+    typedef __attribute__((address_space(3))) v2i lds_v2i;
+    const int kk = half * 32 + r, odd = r & 1;
+    const uint32_t key_base = (kk >> 1) * kPairStride + odd * 512 + ((g ^ odd) << 4);
+    const uint32_t key_even = key_base + 64 * odd, key_odd = key_base - 64 * odd;  // steps 0, 2, .. and 1, 3, ..
+    const uint32_t rope_base = kRopeAt + (kk >> 3) * kRopeStride + (kk & 7) * 128;
+    const uint32_t rope_even = rope_base + ((g ^ ((kk >> 1) & 3)) << 4), rope_odd = rope_base + (((2 + g) ^ ((kk >> 1) & 3)) << 4);
+    const int vk = 8 * ((lane >> 3) & 1) + 4 * g + ((lane >> 1) & 3);  // the row this lane addresses (and 16, 32, 48 on)
+    const uint32_t value_base = (vk >> 1) * kPairStride + (vk & 1) * 512 + ((((lane >> 4) & 1) ^ (vk & 1)) << 4) + 8 * (lane & 1) + 256 * half;
+    const uint32_t value_low = value_base + 64 * (vk & 1), value_high = value_base - 64 * (vk & 1);  // d & 2 clear and set
+    const uint32_t weights = lds + kWeightsAt + pair * (2 * kWeightBytes) + lane * 16;  // half, tile in turn, term
+    const uint32_t refs = lds + kRefsAt + pair * (2 * kRefBytes) + r * 4;
+    const uint32_t floats = lds + kKeysAt + wave * kKeyBytes;
+
     // ---- softmax of this lane's 16 scores, in pieces that fit between matrix products
     struct Soft {
-      v16f x;             // score in log2 + scale code of the key
-      uint32_t codes[4];  // of keys 8 q + 4 g .. + 3
-      float ref, sum;
-      int up;  // weights are 2^(x - ref); the accumulator's are 2^up times those
+      v16f x;          // score in log2 + scale code of the key
+      v4f inv[4];      // 2^-e of keys 8 q + 4 g .. + 3
+      float ref, sum;  // weights are 2^(x - ref)
     };
-    auto soft_codes = [&](int tile_code, Soft& w) {
-      const int up = __builtin_amdgcn_mov_dpp(tile_code, 0xB1, 0xF, 0xF, true);    // the neighbour's: lanes 1 0 3 2
-      const int two = (lane & 1) ? (up | tile_code << 8) : (tile_code | up << 8);  // both lanes: even, odd
-      const int over = __builtin_amdgcn_mov_dpp(two, 0x4E, 0xF, 0xF, true);        // lanes 2 3 0 1
-      const int four = (lane & 2) ? (over | two << 16) : (two | over << 16);       // the quad's four codes
+    auto soft_x = [&](const v16f& s, const v4f* e, Soft& w) {
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4)
-        w.codes[q4] = (uint32_t)__builtin_amdgcn_ds_bpermute(((half * 32 + 4 * g) << 2) + 32 * q4, four);
-    };
-    auto soft_x = [&](const v16f& s, Soft& w) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w.x[i] = fmaf(s[i], c, (float)((w.codes[i >> 2] >> (8 * (i & 3))) & 0xffu));
+      for (int i = 0; i < 16; ++i) w.x[i] = fmaf(s[i], c, e[i >> 2][i & 3]);
     };
     auto soft_mask = [&](int t, Soft& w) {
       const int k0 = t * kTile + half * 32;
@@ -514,225 +476,304 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
           if (8 * (i >> 2) + (i & 3) >= left) w.x[i] = kNegInf;
       }
     };
-    // Returns the factor of a new reference (1: none).
     auto soft_top = [&](Soft& w) {
       float top = w.x[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = fmaxf(top, w.x[i]);
       const unsigned bits = __float_as_uint(top);
       const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
-      top = ceilf(fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])));
-      const bool higher = top > m + kSlack;  // also at the first key that the row sees (m = -inf)
-      const float f = higher && m > kNegInf ? __builtin_amdgcn_exp2f(m - top) : 1.f;
-      m = higher ? top : m;
-      l *= f;
-      const float base = m == kNegInf ? 0.f : m;
-      w.ref = fmaxf(top, base - kFar) - kTop;
-      w.up = (int)(w.ref - base);
+      top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
+      w.ref = top == kNegInf ? kNone : ceilf(top) - kTop;
       w.sum = 0.f;
-      return f;
     };
-    // Weights of keys 2 k and 2 k + 1, into the operand.
-    auto soft_pair = [&](Soft& w, int k, v8i& pw) {
+    // Weights of keys 2 k and 2 k + 1; the same into the two terms. Piece 0 .. 15 alternates between them, the
+    // second a piece or two behind.
+    auto soft_weight = [&](Soft& w, float ref, int k) {
+#pragma unroll
+      for (int i = 2 * k; i < 2 * k + 2; ++i) {
+        w.x[i] = __builtin_amdgcn_exp2f(w.x[i] - ref);
+        w.sum = fmaf(w.x[i], w.inv[i >> 2][i & 3], w.sum);  // (a masked key's weight is 0, whatever its scale)
+      }
+    };
+    auto soft_terms = [&](const Soft& w, int k, v4i& hi, v4i& lo) {
       typedef float v2f __attribute__((ext_vector_type(2)));
       const int q4 = k >> 1;
-      const float p0 = __builtin_amdgcn_exp2f(w.x[2 * k] - w.ref), p1 = __builtin_amdgcn_exp2f(w.x[2 * k + 1] - w.ref);
-      // times 2^-e (a masked key's p is 0, whatever its code)
-      w.sum += __builtin_amdgcn_ldexpf(p0, 127 - (int)((w.codes[q4] >> (16 * (k & 1))) & 0xffu));
-      w.sum += __builtin_amdgcn_ldexpf(p1, 127 - (int)((w.codes[q4] >> (16 * (k & 1) + 8)) & 0xffu));
+      const float p0 = w.x[2 * k], p1 = w.x[2 * k + 1];
+      // what the first term leaves, 16 times: exact
       if (k & 1) {
-        pw[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(p0, p1, pw[q4], true);
-        const v2f back = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)pw[q4], 16.f, true);  // 16 times
-        pw[4 + q4] = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(p0, 16.f, -back[0]), fmaf(p1, 16.f, -back[1]), pw[4 + q4], true);
+        hi[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(p0, p1, hi[q4], true);
+        const v2f back = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)hi[q4], 16.f, true);
+        lo[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(p0, 16.f, -back[0]), fmaf(p1, 16.f, -back[1]), lo[q4], true);
       } else {
-        pw[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(p0, p1, 0, false);
-        const v2f back = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)pw[q4], 16.f, false);
-        pw[4 + q4] = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(p0, 16.f, -back[0]), fmaf(p1, 16.f, -back[1]), 0, false);
+        hi[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(p0, p1, 0, false);
+        const v2f back = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)hi[q4], 16.f, false);
+        lo[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(p0, 16.f, -back[0]), fmaf(p1, 16.f, -back[1]), 0, false);
       }
+    };
+    auto soft_piece = [&](Soft& w, float ref, int piece, v4i& hi, v4i& lo) {
+      if (piece == 0 || (piece & 1)) {
+        const int k = (piece + 1) >> 1;  // 0, 1, 2, .. at pieces 0, 1, 3, 5, .., 13; piece 15 is the last terms
+        if (k < 8) {
+          soft_weight(w, ref, k);
+          asm volatile("" : "+v"(w.x[2 * k]), "+v"(w.x[2 * k + 1]), "+v"(w.sum));  // here, not after the products
+          return;
+        }
+      }
+      const int k = piece == 15 ? 7 : (piece >> 1) - 1;
+      soft_terms(w, k, hi, lo);
+      asm volatile("" : "+v"(hi[k >> 1]), "+v"(lo[k >> 1]));
+    };
+    // ---- the weights of a tile, as both waves of the pair wrote them: slots 0 .. 31 of a product are the first
+    // wave's keys, 32 .. 63 the second's, each under its own scale code (lanes g = 0 and 1 hold the two)
+    struct Weights {
+      v8i hi, lo;
+      float r0, r1;
+      int codes;
+    };
+    auto read_weights = [&](int turn, Weights& w) {
+      const uint32_t at = weights + turn * 2048;
+      w.r0 = *reinterpret_cast<lds_f*>(refs + turn * 128), w.r1 = *reinterpret_cast<lds_f*>(refs + turn * 128 + kRefBytes);
+      const v4i h0 = *reinterpret_cast<lds_v4i*>(at), h1 = *reinterpret_cast<lds_v4i*>(at + kWeightBytes);
+      const v4i l0 = *reinterpret_cast<lds_v4i*>(at + 1024), l1 = *reinterpret_cast<lds_v4i*>(at + kWeightBytes + 1024);
+      w.hi = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
+      w.lo = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    // Their scale codes, and a new reference where they pass the old one (no branches but for the accumulator).
+    // Returns its factor.
+    auto refer = [&](Weights& w, float ref_own, float sum_own) {
+      const float top = fmaxf(w.r0, w.r1);
+      const bool higher = top > m + kSlack;  // also at the first key that a row sees (m = kNone; the accumulator is zero)
+      const float f = higher && m > kNone ? __builtin_amdgcn_exp2f(m - top) : 1.f;
+      m = higher ? top : m;
+      // (exponents far below the reference stop at 2^-120 of it)
+      const int up = (int)fmaxf((g ? w.r1 : w.r0) - m, -120.f);
+      w.codes = 127 | (127 + up) << 8 | (123 + up) << 16;
+      l = fmaf(l, f, __builtin_amdgcn_ldexpf(sum_own, (int)(ref_own - m)));
+      return f;
     };
     auto rescale = [&](float f) {
       if (__any(f != 1.f)) {
         asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");  // products in flight
 #pragma unroll
-        for (int d = 0; d < 16; ++d) {
+        for (int d = 0; d < 8; ++d) {
           keep_acc(acc[d]);
           acc[d] *= f;
           keep_acc(acc[d]);
         }
       }
     };
-    // ---- O^T += V^T P^T, 32 value columns at a time: accumulator d is columns 32 (d ^ 8 half) .. + 31, so
-    // that the first 8 are those that the wave joins at the end; `between(d)` is called at each of 16 steps
-    auto values = [&](uint32_t tile, const v8i& pw, int p_code, auto between) {
-      typedef __attribute__((address_space(3))) v2i lds_v2i;
-      const int ln = fresh(lane);
-      const int vk = half * 32 + 8 * ((ln >> 3) & 1) + 4 * g + ((ln >> 1) & 3);  // the row this lane addresses (and vk + 16)
-      const uint32_t vb = tile + vk * kLatentDim + 8 * (ln & 1);
-      const int sw = ((ln >> 4) & 1) ^ swz(vk) ^ (16 * half);
-      v2i x[2], y[2];
-      auto value = [&](int d) {
-        const uint32_t at = vb + ((sw ^ (2 * d)) << 4);
-        x[d % 2] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at));
-        y[d % 2] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at + 16 * kLatentDim));
-      };
-      value(0);
+    // ---- O^T += V^T P^T, 32 value columns at a time; `between(i)` is called after each of 14 products. The first
+    // columns are read by the caller, and the last ones are left to finish(): after the next barrier, while
+    // the first keys are read.
+    auto value_at = [&](uint32_t tile, int d) {
+      const uint32_t at = tile + ((d & 2) ? value_high : value_low) + 32 * d;
+      v2i x[4];
 #pragma unroll
-      for (int d = 0; d < 16; ++d) {
-        if (d + 1 < 16) value(d + 1);
-        const v2i u = x[d % 2], w = y[d % 2];
-        const v8i v = {u[0], u[1], w[0], w[1], u[0], u[1], w[0], w[1]};
-        mfma_scaled_acc(v, pw, acc[d], p_code);
-        between(d);
+      for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at + i * 8 * kPairStride));
+      return v8i{x[0][0], x[0][1], x[1][0], x[1][1], x[2][0], x[2][1], x[3][0], x[3][1]};
+    };
+    Weights late{};  // (nothing is late at the first tile: its products are with zeros)
+    v8i late_v{};
+    late.codes = 127 | 127 << 8 | 127 << 16;
+    auto values = [&](uint32_t tile, const Weights& w, const v8i& v0, auto between) {
+      v8i v[2];
+      v[0] = v0;
+#pragma unroll
+      for (int d = 0; d < 7; ++d) {
+        v[(d + 1) & 1] = value_at(tile, d + 1);
+        mfma_scaled_acc<false>(v[d & 1], w.hi, acc[d], w.codes);
+        between(2 * d);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma_scaled_acc<true>(v[d & 1], w.lo, acc[d], w.codes);
+        between(2 * d + 1);
         __builtin_amdgcn_sched_barrier(0);
       }
+      late = w;
+      late_v = v[1];
+    };
+    auto finish = [&] {
+      mfma_scaled_acc<false>(late_v, late.hi, acc[7], late.codes);
+      mfma_scaled_acc<true>(late_v, late.lo, acc[7], late.codes);
     };
 
-    v8i pw;
-    int p_code = 127;
+    // ---- scores of this wave's 32 keys of a tile; `between(step)` is called at each of 8 steps
+    auto scores = [&](uint32_t tile, int kc, auto between) {
+      auto key_at = [&](int ks) {
+        const uint32_t at = tile + ((ks & 1) ? key_odd : key_even) + 64 * ks;
+        const v4i x = *reinterpret_cast<lds_v4i*>(at), y = *reinterpret_cast<lds_v4i*>(at + 32);
+        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+      };
+      auto rope_at = [&](int ks) {
+        return __builtin_bit_cast(v8bf, *reinterpret_cast<lds_v4i*>(tile + ((ks & 1) ? rope_odd : rope_even) + 64 * (ks >> 1)));
+      };
+      v8i k[3];
+      v8bf kr[4];
+      k[0] = key_at(0);
+      k[1] = key_at(1);
+      finish();
+      v16f s;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        if (ks + 2 < 8) k[(ks + 2) % 3] = key_at(ks + 2);
+        else kr[2 * ks - 12] = rope_at(2 * ks - 12), kr[2 * ks - 11] = rope_at(2 * ks - 11);
+        s = mfma_scaled<0>(k[ks % 3], q.hi[ks], s, kc, q.code);
+        s = mfma_scaled<1>(k[ks % 3], q.lo[ks], s, kc, q.code);
+        asm volatile("" : "+v"(s));  // the products stay here
+        between(ks);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[ks], q.rope[ks], s, 0, 0, 0);
+      return s;
+    };
+    constexpr int kSteps = kPairs == 1 ? 7 : 5, kEach = (kCopies + kSteps - 1) / kSteps;
+    uint32_t places[kCopies];  // where the rows of the next copies lie
+    int kc;                    // scale code of this lane's key of the tile at hand
+    auto prepare = [&](int tile_code, uint32_t unit) {
+      kc = __builtin_amdgcn_ds_bpermute((half * 32 + r) << 2, tile_code);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) places[j] = place_of(unit, j);
+      *reinterpret_cast<lds_f*>(floats + lane * 4) = (float)tile_code;
+      *reinterpret_cast<lds_f*>(floats + 256 + lane * 4) = __builtin_amdgcn_ldexpf(1.f, 127 - tile_code);
+    };
+    prepare(code, ahead.unit);
     uint32_t tile = lds, tile_before = lds;
-    int place = 0;
-    // Tile t: everything up to the weights; kFirst: there is no tile before it in this part.
+    int place = 0, turn = 0;
+    float ref_before = kNone, sum_before = 0.f;
     auto step = [&](int t, auto first) {
       constexpr bool kFirst = decltype(first)::value;
-      // tile t and what was read ahead have landed; every wave is done with the tile whose place is next
+      // tile t and what was read ahead have landed, the weights of tile t - 1 are written, and every wave is
+      // done with the tile whose place is next
       wait_copies();
-      asm volatile("" : "+v"(page_far), "+v"(code_next));
+      asm volatile("" : "+v"(far.page), "+v"(ahead.byte));
       lds_barrier();
       const int next_place = place + 1 == kBuffers ? 0 : place + 1;
       const uint32_t next_tile = lds + next_place * kTileBytes;
-      const uint32_t unit = unit_next;
-      const int tile_code = code;
-      code = code_next;
+      const uint32_t unit = ahead.unit;
+      code = ahead.byte | ahead.none;
       // (after the last tile the copies bring one that is not used: there always is a key to look up)
-      constexpr int kSteps = 4, kEach = kCopies / kSteps + (kCopies % kSteps != 0), kFirstPlaces = kEach;
-      uint32_t places[kCopies];
-      const Lanes at = lanes();
-#pragma unroll
-      for (int j = 0; j < kFirstPlaces && j < kCopies; ++j) places[j] = place_of(at, unit, j);
-      Soft w;
-      soft_codes(tile_code, w);
-      const v16f s = scores(tile, tile_code, [&](int ks) {
+      Weights before;
+      v8i v0;
+      float f = 1.f;
+      const v16f s = scores(tile, kc, [&](int ks) {
         if (ks < kSteps) {
 #pragma unroll
           for (int j = 0; j < kEach; ++j) {
-            if (ks * kEach + j < kCopies) copy_piece(at, places[ks * kEach + j], next_tile, ks * kEach + j);
-            const int far = ks * kEach + j + kFirstPlaces;
-            if (far < kCopies) places[far] = place_of(at, unit, far);
+            if (ks * kEach + j < kCopies) copy_piece(places[ks * kEach + j], next_tile, ks * kEach + j);
+            const int far = ks * kEach + j + kEach;
+            if (far < kCopies) places[far] = place_of(unit, far);
           }
         }
         if (ks == kSteps) {
-          unit_next = unit_of(page_far, o_far);
-          code_next = code_of(page_far, o_far);
-          look_up(page_far, o_far);
+          ahead = row_of(far);
+          look_up(far);
+        }
+        if (!kFirst && ks == 5) read_weights(turn ^ 1, before);
+        if (!kFirst && ks == 7) {
+          f = refer(before, ref_before, sum_before);
+          asm volatile("" : "+v"(f), "+v"(before.codes));
+          v0 = value_at(tile_before, 0);
         }
       });
-      if constexpr (kAhead && !kFirst) {
-        v8i next;
-        float f;
-        values(tile_before, pw, p_code, [&](int d) {
-          if (d == 0) soft_x(s, w);
-          if (d == 1) soft_mask(t, w);
-          if (d == 2) f = soft_top(w);
-          if (d >= 3 && d < 11) soft_pair(w, d - 3, next);
-        });
-        rescale(f);
-        pw = next;
-      } else {
-        soft_x(s, w);
-        soft_mask(t, w);
-        const float f = soft_top(w);
-        if constexpr (!kAhead) rescale(f);  // (the first tile's factor is 1)
+      Soft w;
+      v4f e[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) soft_pair(w, k, pw);
+      for (int q4 = 0; q4 < 4; ++q4) {
+        e[q4] = *reinterpret_cast<lds_v4f*>(floats + (half * 32 + 8 * q4 + 4 * g) * 4);
+        w.inv[q4] = *reinterpret_cast<lds_v4f*>(floats + 256 + (half * 32 + 8 * q4 + 4 * g) * 4);
       }
-      p_code = p_base + (w.up << 8);
-      if constexpr (!kAhead) values(tile, pw, p_code, [](int) {});
-      l += __builtin_amdgcn_ldexpf(w.sum, w.up);
+      v4i hi, lo;
+      float ref;  // (a row that sees none of the keys: its x are -inf, its weights 0)
+      if constexpr (kFirst) {
+        soft_x(s, e, w);
+        soft_mask(t, w);
+        soft_top(w);
+        ref = w.ref == kNone ? 0.f : w.ref;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) soft_piece(w, ref, k, hi, lo);
+      } else {
+        rescale(f);
+        values(tile_before, before, v0, [&](int d) {
+          if (d == 0) soft_x(s, e, w);
+          if (d == 1) soft_mask(t, w);
+          if (d == 2) soft_top(w), ref = w.ref == kNone ? 0.f : w.ref;
+          if (d >= 3) {
+#pragma unroll
+            for (int piece = (d - 3) * 16 / 11; piece < (d - 2) * 16 / 11; ++piece) soft_piece(w, ref, piece, hi, lo);
+          }
+        });
+      }
+      const uint32_t at = weights + half * kWeightBytes + turn * 2048;
+      *reinterpret_cast<lds_w4i*>(at) = hi;
+      *reinterpret_cast<lds_w4i*>(at + 1024) = lo;
+      *reinterpret_cast<lds_f*>(refs + half * kRefBytes + turn * 128) = w.ref;  // (lanes r and r + 32 write the same)
+      prepare(code, ahead.unit);
+      ref_before = w.ref;
+      sum_before = w.sum;
+      turn ^= 1;
       tile_before = tile;
       tile = next_tile;
       place = next_place;
     };
-    if constexpr (kAhead) {
-      step(t_begin, std::true_type{});
-      for (int t = t_begin + 1; t < t_end; ++t) step(t, std::false_type{});
-      values(tile_before, pw, p_code, [](int) {});
-    } else {
-      for (int t = t_begin; t < t_end; ++t) step(t, std::false_type{});
-    }
+    step(t_begin, std::true_type{});
+    for (int t = t_begin + 1; t < t_end; ++t) step(t, std::false_type{});
     wait_copies();
+    lds_barrier();
+    Weights before;
+    read_weights(turn ^ 1, before);
+    finish();
+    rescale(refer(before, ref_before, sum_before));
+    values(tile_before, before, value_at(tile_before, 0), [](int) {});
+    finish();
   }
 
   // the last products' results arrive (the compiler does not know what the assembly above was)
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
-  for (int d = 0; d < 16; ++d) keep_acc(acc[d]);
-  // ---- the two waves of a pair join: each sends the other half its columns
+  for (int d = 0; d < 8; ++d) keep_acc(acc[d]);
+  // ---- the row's sum over its keys, then the wave's columns
   l += __shfl_xor(l, 32);
   __syncthreads();
-  float* sh = reinterpret_cast<float*>(lds_tiles);
-  if (g == 0) sh[(wave * 32 + r) * 2] = m, sh[(wave * 32 + r) * 2 + 1] = l;
+  float* sums = reinterpret_cast<float*>(lds_tiles);
+  if (g == 0) sums[wave * 32 + r] = l;
   __syncthreads();
-  const float m0 = sh[(pair * 64 + r) * 2], l0 = sh[(pair * 64 + r) * 2 + 1];
-  const float m1 = sh[(pair * 64 + 32 + r) * 2], l1 = sh[(pair * 64 + 32 + r) * 2 + 1];
-  const float m_all = fmaxf(m0, m1);
-  const float f0 = m0 == m_all ? 1.f : __builtin_amdgcn_exp2f(m0 - m_all);
-  const float f1 = m1 == m_all ? 1.f : __builtin_amdgcn_exp2f(m1 - m_all);
-  const float l_all = fmaf(f1, l1, f0 * l0);
-  const bool whole = work.slot < 0;
-  const float inv = !whole ? 1.f : l_all == 0.f ? 0.f : 1.0f / l_all;  // a row that sees no key is zero
-  const float f_own = (half ? f1 : f0), f_other = (half ? f0 : f1);
-  const int64_t state_row = (int64_t)work.slot * kBM + row;
-  if (!whole && half == 0 && g == 0 && row_ok) {
-    a.stats[state_row * 2] = m_all;
-    a.stats[state_row * 2 + 1] = l_all;
-  }
-  uint16_t* dst = a.out + qtok * a.o_tok + (int64_t)head * a.o_head + 256 * half;
-  float* state = a.states + state_row * kLatentDim + 256 * half;
-  v4f* box = reinterpret_cast<v4f*>(lds_tiles);  // 16 KB a wave
+  const float l_all = sums[pair * 64 + r] + sums[pair * 64 + 32 + r];
+  if (!row_ok) return;
+  if (work.slot < 0) {
+    const float inv = l_all == 0.f ? 0.f : 1.0f / l_all;  // a row that sees no key is zero
+    uint16_t* dst = a.out + qtok * a.o_tok + (int64_t)head * a.o_head + 256 * half + 16 * g;
 #pragma unroll
-  for (int step = 0; step < 2; ++step) {
-    __syncthreads();
+    for (int d = 0; d < 8; ++d) {
+      // lanes g = 0 and 1 of a row swap quads of columns, so that each stores 16 neighbouring ones
+      uint32_t u[2][4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const v16f x = acc[8 + 4 * step + d];
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const auto v = __builtin_amdgcn_permlane32_swap(
+              pack_bf16(acc[d][4 * h + 2 * i] * inv, acc[d][4 * h + 2 * i + 1] * inv),
+              pack_bf16(acc[d][8 + 4 * h + 2 * i] * inv, acc[d][8 + 4 * h + 2 * i + 1] * inv), false, false);
+          u[h][i] = v[0];
+          u[h][2 + i] = v[1];
+        }
+      uint4* p = reinterpret_cast<uint4*>(dst + 32 * d);
+      p[0] = make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]);
+      p[1] = make_uint4(u[1][0], u[1][1], u[1][2], u[1][3]);
+    }
+  } else {
+    const int64_t state_row = (int64_t)work.slot * kBM + row;
+    if (half == 0 && g == 0) {
+      a.stats[state_row * 2] = m;
+      a.stats[state_row * 2 + 1] = l_all;
+    }
+    float* state = a.states + state_row * kLatentDim + 256 * half + 4 * g;
+#pragma unroll
+    for (int d = 0; d < 8; ++d)
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4)
-        box[(wave * 16 + d * 4 + q4) * 64 + lane] = v4f{x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]};
-    }
-    __syncthreads();
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const v16f x = acc[4 * step + d];
-      v4f o[4];  // columns 8 q + 4 g .. + 3 of 32
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
-        const v4f y = box[((wave ^ 1) * 16 + d * 4 + q4) * 64 + lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[q4][i] = fmaf(f_other, y[i], f_own * x[4 * q4 + i]) * inv;
-      }
-      const int column = 32 * (4 * step + d);
-      if (whole) {
-        // lanes g = 0 and 1 of a row swap quads, so that each stores 16 neighbouring columns
-        uint32_t u[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const auto v = __builtin_amdgcn_permlane32_swap(pack_bf16(o[h][2 * i], o[h][2 * i + 1]),
-                                                            pack_bf16(o[2 + h][2 * i], o[2 + h][2 * i + 1]), false, false);
-            u[h][i] = v[0];
-            u[h][2 + i] = v[1];
-          }
-        if (row_ok) {
-          uint4* p = reinterpret_cast<uint4*>(dst + column + 16 * g);
-          p[0] = make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]);
-          p[1] = make_uint4(u[1][0], u[1][1], u[1][2], u[1][3]);
-        }
-      } else if (row_ok) {
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) *reinterpret_cast<v4f*>(state + column + 8 * q4 + 4 * g) = o[q4];
-      }
-    }
+        *reinterpret_cast<v4f*>(state + 32 * d + 8 * q4) = v4f{acc[d][4 * q4], acc[d][4 * q4 + 1], acc[d][4 * q4 + 2], acc[d][4 * q4 + 3]};
   }
 }
 
@@ -772,14 +813,13 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
 constexpr int kCUs = 256;
 constexpr int kMinTiles = 2;  // fewer tiles a part cost more in states than they save
 
-// Pairs of waves a workgroup: one where a sequence has 32 query rows or fewer on average (then two
-// workgroups share a CU), otherwise two.
+// Pairs of waves a workgroup: one where a sequence has 32 query rows or fewer on average, otherwise two.
 int pairs_for(int64_t T, int64_t B, int64_t H) { return T * H <= 32 * B ? 1 : 2; }
 
 template <int kPairs>
 hipError_t launch(const LatentAttnArgs& args, const LatentAttnPlan& plan, hipStream_t stream) {
   const int64_t grid = (plan.parts + 15) / 16 * 16;
-  hipLaunchKernelGGL((latent_attn_kernel<kPairs, (kPairs > 1)>), dim3((unsigned)grid), dim3(kPairs * 128), 0, stream, args);
+  hipLaunchKernelGGL((latent_attn_kernel<kPairs>), dim3((unsigned)grid), dim3(kPairs * 128), 0, stream, args);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.slots == 0) return e;
   hipLaunchKernelGGL((latent_join_kernel<kPairs * 32>), dim3((unsigned)plan.cuts, kPairs * 8), dim3(256), 0, stream, args);
@@ -796,7 +836,7 @@ LatentAttnPlan plan_latent_attn(int64_t T, int64_t B, int64_t H, int64_t max_key
   p.blocks = T * H / bm + (T < B ? T : B);
   const int64_t max_tiles = (max_keys + kTile - 1) / kTile;
   p.max_tiles = (int)max_tiles;
-  p.target_parts = kCUs * 2 / p.pairs;
+  p.target_parts = kCUs;
   p.min_tiles = kMinTiles;
   // Blocks are cut only into as many parts as run at once in all.
   const int64_t per_block = (max_tiles + kMinTiles - 1) / kMinTiles;
