@@ -56,7 +56,8 @@ def _check(status: int, what: str):
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the current stream's handle, without building the Stream object around it (1.7 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
 
 
 def _require(t: torch.Tensor, name: str, dtype, dims: int):
@@ -88,7 +89,7 @@ def _workspace(device: torch.device, nbytes: int) -> tuple[int, int]:
     ordered on that stream."""
     if nbytes == 0:
         return 0, 0
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    key = (device.index, _stream(device))
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)

@@ -237,6 +237,15 @@ __device__ __forceinline__ void copy16_from(const uint8_t* src, uint32_t lds) {
       : "memory");
 }
 
+// The same for kernels in which nothing else uses M0 (gfx950's LDS instructions do not read it): it is not
+// saved.
+__device__ __forceinline__ void copy16_m0(const uint8_t* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void copy16_m0(const void* sbase, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %1, %0" : : "s"(sbase), "v"(voff), "s"(lds) : "memory");
+}
+
 // The same copies for kernels whose register pressure lets the compiler spill the (wave-uniform)
 // base or LDS address: a value reloaded from a spill lands in a vector register, which the
 // scalar moves above cannot read, so these pass both through readfirstlane (free for values
@@ -273,6 +282,17 @@ __device__ __forceinline__ void map_tile(int bid, int n_tiles, int m_tiles, int 
   const int r = t - (t / band) * band;
   tm = first_m + r % gm;
   tn = r / gm;
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // 1, 2, 4, 8 lanes up within 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 to the next 16, of the odd rows
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
+  return v;
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)p; }

@@ -40,8 +40,6 @@
 #include "latent.h"
 #include "launch.h"
 
-#include <type_traits>
-
 namespace bfp8 {
 
 namespace {
@@ -64,8 +62,8 @@ constexpr float kTop = 8.f;                // the largest of 32 weights is held 
 constexpr float kNone = -1e30f;            // exponent of no weight at all
 constexpr float kNegInf = -__builtin_inff();
 
-struct Desc {  // a block that was cut: rows of block `block`, partial states slot .. slot + parts - 1
-  int seq, block, slot, parts;
+struct Desc {  // a block that was cut: its first query row (token * H + head) and rows, partial states slot .. slot + parts - 1
+  int first, rows, slot, parts;
 };
 
 // Scale codes: ea's low byte and byte kByte of eb.
@@ -89,10 +87,6 @@ __device__ __forceinline__ void mfma_scaled_acc(const v8i& a, const v8i& b, v16f
                  : "+a"(c)
                  : "v"(a), "v"(b), "v"(codes));
 }
-// copy16_from without saving M0, which nothing else in this kernel uses (gfx9 LDS instructions do not read it).
-__device__ __forceinline__ void copy16_m0(const uint8_t* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(lds) : "memory");
-}
 // Keeps an accumulator in the accumulation registers at this point.
 __device__ __forceinline__ void keep_acc(v16f& c) { asm volatile("" : "+a"(c)); }
 
@@ -112,17 +106,6 @@ __device__ __forceinline__ Seq sequence(const LatentAttnArgs& a, int b) {
   }
   s.len = max(a.lens[b], 0);
   return s;
-}
-
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // 1, 2, 4, 8 lanes up within 16
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 to the next 16, of the odd rows
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
-  return v;
 }
 
 // What a workgroup computes: part `part` of `parts` of a block, and where its state goes (-1: nowhere).
@@ -206,7 +189,9 @@ __device__ __forceinline__ bool find_work(const LatentAttnArgs& a, Work& work) {
         const int blk = (my - p0) / c, part = (my - p0) - blk * c;
         w = {q, b, blk, part, c, c > 1 ? s0 + blk * c + part : -1};
         if (c > 1 && part == 0 && c0 + blk < a.max_cuts && threadIdx.x < 64)
-          reinterpret_cast<Desc*>(a.counts + 4)[c0 + blk] = {b, blk, s0 + blk * c, c};
+          reinterpret_cast<Desc*>(a.counts + 4)[c0 + blk] = {
+              (int)((int64_t)q.q0 * a.H + (int64_t)blk * kBM), (int)min((int64_t)q.n * a.H - (int64_t)blk * kBM, (int64_t)kBM),
+              s0 + blk * c, c};
         found = true;
       }
       p0 += n * c;
@@ -642,8 +627,15 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     uint32_t tile = lds, tile_before = lds;
     int place = 0, turn = 0;
     float ref_before = kNone, sum_before = 0.f;
-    auto step = [&](int t, auto first) {
-      constexpr bool kFirst = decltype(first)::value;
+    // Before the first tile there are no weights: its value products are with zeros (one copy of the code, which
+    // every workgroup has to fetch, costs less than a step without them would save).
+    {
+      const uint32_t at = weights + half * kWeightBytes + 2048;
+      *reinterpret_cast<lds_w4i*>(at) = v4i{0, 0, 0, 0};
+      *reinterpret_cast<lds_w4i*>(at + 1024) = v4i{0, 0, 0, 0};
+      *reinterpret_cast<lds_f*>(refs + half * kRefBytes + 128) = kNone;
+    }
+    for (int t = t_begin; t < t_end; ++t) {
       // tile t and what was read ahead have landed, the weights of tile t - 1 are written, and every wave is
       // done with the tile whose place is next
       wait_copies();
@@ -670,8 +662,8 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
           ahead = row_of(far);
           look_up(far);
         }
-        if (!kFirst && ks == 5) read_weights(turn ^ 1, before);
-        if (!kFirst && ks == 7) {
+        if (ks == 5) read_weights(turn ^ 1, before);
+        if (ks == 7) {
           f = refer(before, ref_before, sum_before);
           asm volatile("" : "+v"(f), "+v"(before.codes));
           v0 = value_at(tile_before, 0);
@@ -686,25 +678,16 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       }
       v4i hi, lo;
       float ref;  // (a row that sees none of the keys: its x are -inf, its weights 0)
-      if constexpr (kFirst) {
-        soft_x(s, e, w);
-        soft_mask(t, w);
-        soft_top(w);
-        ref = w.ref == kNone ? 0.f : w.ref;
+      rescale(f);
+      values(tile_before, before, v0, [&](int d) {
+        if (d == 0) soft_x(s, e, w);
+        if (d == 1) soft_mask(t, w);
+        if (d == 2) soft_top(w), ref = w.ref == kNone ? 0.f : w.ref;
+        if (d >= 3) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) soft_piece(w, ref, k, hi, lo);
-      } else {
-        rescale(f);
-        values(tile_before, before, v0, [&](int d) {
-          if (d == 0) soft_x(s, e, w);
-          if (d == 1) soft_mask(t, w);
-          if (d == 2) soft_top(w), ref = w.ref == kNone ? 0.f : w.ref;
-          if (d >= 3) {
-#pragma unroll
-            for (int piece = (d - 3) * 16 / 11; piece < (d - 2) * 16 / 11; ++piece) soft_piece(w, ref, piece, hi, lo);
-          }
-        });
-      }
+          for (int piece = (d - 3) * 16 / 11; piece < (d - 2) * 16 / 11; ++piece) soft_piece(w, ref, piece, hi, lo);
+        }
+      });
       const uint32_t at = weights + half * kWeightBytes + turn * 2048;
       *reinterpret_cast<lds_w4i*>(at) = hi;
       *reinterpret_cast<lds_w4i*>(at + 1024) = lo;
@@ -716,9 +699,7 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       tile_before = tile;
       tile = next_tile;
       place = next_place;
-    };
-    step(t_begin, std::true_type{});
-    for (int t = t_begin + 1; t < t_end; ++t) step(t, std::false_type{});
+    }
     wait_copies();
     lds_barrier();
     Weights before;
@@ -777,40 +758,66 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
   }
 }
 
-// Joins the parts of a cut block, in order: one wave a row.
+constexpr int kMaxParts = 256;  // of a block: no more parts run at once
+
+// Joins the parts of a cut block, in order: one wave a row. The lanes hold the parts' references and sums,
+// then take 8 columns each. Bound by latency (a chain of three loads) where there are few rows, and by HBM and
+// the L2s where every workgroup left a state.
 template <int kBM>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
-  if ((int)blockIdx.x >= a.counts[0]) return;
+  const int cuts = a.counts[0];
   const Desc desc = reinterpret_cast<const Desc*>(a.counts + 4)[blockIdx.x];
+  if ((int)blockIdx.x >= cuts) return;
   const int lane = threadIdx.x & 63;
   const int row = blockIdx.y * 4 + (threadIdx.x >> 6);
-  if (desc.slot + desc.parts > a.max_slots) return;
-  const Seq seq = sequence(a, desc.seq);
-  const int flat = desc.block * kBM + row;
-  if (flat >= seq.n * a.H) return;
-  const int tok = flat / a.H, head = flat - tok * a.H;
+  if (row >= desc.rows || desc.parts > kMaxParts || desc.slot + desc.parts > a.max_slots) return;
+  constexpr int kEach = kMaxParts / 64;
+  float f[kEach], sums[kEach];
   float m = kNegInf;
-  for (int p = 0; p < desc.parts; ++p) m = fmaxf(m, a.stats[((int64_t)(desc.slot + p) * kBM + row) * 2]);
-  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < desc.parts; ++p) {
-    const int64_t at = (int64_t)(desc.slot + p) * kBM + row;
-    const float mp = a.stats[at * 2];
-    const float f = mp == m ? 1.f : __builtin_amdgcn_exp2f(mp - m);
-    l = fmaf(f, a.stats[at * 2 + 1], l);
-    const v4f* src = reinterpret_cast<const v4f*>(a.states + at * kLatentDim + lane * 8);
-    const v4f x = src[0], y = src[1];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fmaf(f, x[i], o[i]), o[4 + i] = fmaf(f, y[i], o[4 + i]);
+  for (int i = 0; i < kEach; ++i) {
+    const int p = 64 * i + lane;
+    f[i] = kNegInf;
+    sums[i] = 0.f;
+    if (p < desc.parts) {
+      const float2 x = reinterpret_cast<const float2*>(a.stats)[(int64_t)(desc.slot + p) * kBM + row];
+      f[i] = x.x;
+      sums[i] = x.y;
+    }
+    m = fmaxf(m, f[i]);
+  }
+#pragma unroll
+  for (int mask = 1; mask < 64; mask <<= 1) m = fmaxf(m, __shfl_xor(m, mask));
+  float l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    f[i] = f[i] == m ? 1.f : __builtin_amdgcn_exp2f(f[i] - m);
+    l = fmaf(f[i], sums[i], l);
+  }
+#pragma unroll
+  for (int mask = 1; mask < 64; mask <<= 1) l += __shfl_xor(l, mask);
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const float* src = a.states + ((int64_t)desc.slot * kBM + row) * kLatentDim + lane * 8;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int n = min(desc.parts - 64 * i, 64);
+    for (int p = 0; p < n; ++p) {
+      const float fp = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f[i]), p));
+      const v4f* at = reinterpret_cast<const v4f*>(src + (int64_t)(64 * i + p) * kBM * kLatentDim);
+      const v4f x = at[0], y = at[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = fmaf(fp, x[j], o[j]), o[4 + j] = fmaf(fp, y[j], o[4 + j]);
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
-  uint16_t* dst = a.out + (seq.q0 + (int64_t)tok) * a.o_tok + (int64_t)head * a.o_head + lane * 8;
+  const int flat = desc.first + row, tok = flat / a.H, head = flat - tok * a.H;
+  uint16_t* dst = a.out + (int64_t)tok * a.o_tok + (int64_t)head * a.o_head + lane * 8;
   *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
                                               pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
 }
 
 constexpr int kCUs = 256;
+static_assert(kCUs <= kMaxParts, "a block's parts fit the join's lanes");
 constexpr int kMinTiles = 2;  // fewer tiles a part cost more in states than they save
 
 // Pairs of waves a workgroup: one where a sequence has 32 query rows or fewer on average, otherwise two.

@@ -6,12 +6,16 @@
 //
 // over the keys j of t's sequence up to t (the last query token sees the last key).
 //
-// One pass with the running maximum and sum of the softmax. A workgroup takes 128 query rows of one
-// head, 32 for each wave, and walks the keys in tiles of 64, copied straight to LDS (a kv row is 512
-// bytes, the rotary key 128). Both products are 32x32x16 matrix-core products, formed transposed
-// (S^T = K Q^T, O^T = V^T P^T): a lane then holds scores of one query row, r = lane % 32, which are
-// its operand of the second product without any exchange, and the running maximum and sum are plain
-// per-lane numbers. V is read from the tile with transposing LDS reads.
+// One pass with the running maximum and sum of the softmax. A workgroup takes 32 query rows of one head
+// a wave and walks the keys in tiles of 64, copied straight to LDS two tiles ahead. Both products are
+// 32x32x16 matrix-core products, formed transposed (S^T = K Q^T, O^T = V^T P^T): a lane then holds
+// scores of one query row, r = lane % 32, which are its operand of the second product without any
+// exchange, and the running maximum and sum are plain per-lane numbers. V is read from the tile with
+// transposing LDS reads.
+//
+// Bound by the matrix cores: with 8 waves a workgroup (256 rows, 2 waves a SIMD) one wave's softmax runs
+// beside another's products. The LDS layout leaves the copies one lane offset for all of a tile's rows, and
+// the reads two addresses each, with constant offsets for everything else.
 #include "device_common.h"
 #include "latent.h"
 #include "launch.h"
@@ -21,19 +25,22 @@ namespace bfp8 {
 namespace {
 
 constexpr int kTile = 64;    // keys of a tile
-constexpr int kBM = 128;     // query rows of a workgroup
 constexpr int kNope = 128;   // key dimensions of a head before the rotary part
 constexpr int kV = 128;      // value dimensions
-constexpr int kKvRow = 2 * (kNope + kV);
 constexpr float kNegInf = -__builtin_inff();
 // The running maximum may lag by a factor of 2^kSlack: weights stay within 2^8, far inside fp16 and
 // bf16, and the accumulator is rescaled only when a tile exceeds that.
 constexpr float kSlack = 8.f;
 
-// XOR of the 16-byte columns of a key's 512-byte row in LDS: conflict-free for the score reads (one
-// column of 16 consecutive keys) and for the transposing value reads (32 lanes: 64 bytes of 4 consecutive
-// keys, so the low two key bits move whole 64-byte pieces).
-__device__ __forceinline__ int swz(int key) { return ((key & 3) << 2) | ((key >> 2) & 3); }
+// A tile in LDS. Rows of kv are 512 bytes; a copy brings two, 2 keys apart, as a pair of 1024 + 16 bytes with the
+// 16-byte columns of the second XORed with 8. Pair p holds keys 16 (p / 8) + 4 (p % 4) + p / 4 % 2 and that + 2:
+// 16 consecutive keys then lie 16 different columns apart modulo 256 bytes (score reads: one column of 16 keys), and
+// 4 consecutive ones 4 columns apart (transposing value reads: 64 bytes of 4 keys). The XOR changes bit 3 of a
+// column alone. Rotary keys: groups of 8 rows of 128 bytes, 1024 + 64 bytes apart, columns XORed with (row / 2) % 4.
+constexpr int kPairStride = 1024 + 16, kRopeStride = 1024 + 64;
+constexpr int kRopeAt = kTile / 2 * kPairStride;
+constexpr int kTileBytes = kRopeAt + kTile / 8 * kRopeStride;
+constexpr int kBuffers = 3;
 
 template <bool kF16>
 __device__ __forceinline__ v16f mfma(const v4i& a, const v4i& b, const v16f& c) {
@@ -49,185 +56,253 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   else return pack_bf16(lo, hi);
 }
 
-template <bool kF16>
-__global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedArgs a) {
-  __shared__ __align__(1024) uint8_t tile[kTile * (kKvRow + 2 * kRopeDim)];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 31, g = lane >> 5;
-  const int head = blockIdx.x % a.H, index = blockIdx.x / a.H;
+__device__ __forceinline__ int clip(int v, int top) { return min(max(v, 0), top); }
 
-  // ---- the index-th block of 128 query rows over all sequences
-  int* sh = reinterpret_cast<int*>(tile);
-  const int per = (a.B + 255) / 256;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  auto clip = [](int v, int top) { return min(max(v, 0), top); };
+// The workgroup's block of kBM query rows, of all sequences' blocks one after the other (of a sequence the last,
+// which has most keys, first). False: there is none. Every wave looks for itself.
+template <int kBM>
+__device__ __forceinline__ bool find_block(const LatentExpandedArgs& a, int index, int& seq, int& block) {
+  const int lane = threadIdx.x & 63;
+  const int per = (a.B + 63) / 64;
+  const int b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
+  auto blocks = [&](int b) { return (max(clip(a.cu_q[b + 1], a.Tq) - clip(a.cu_q[b], a.Tq), 0) + kBM - 1) / kBM; };
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (max(clip(a.cu_q[b + 1], a.Tq) - clip(a.cu_q[b], a.Tq), 0) + kBM - 1) / kBM;
-  int first = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int x = __shfl_up(first, d);
-    if (lane >= d) first += x;
-  }
-  if (lane == 63) sh[wave] = first;
-  __syncthreads();
-  int total = 0;
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) first += sh[w];
-    total += sh[w];
-  }
-  first -= mine;
-  if (index >= total) return;
-  __syncthreads();
+  for (int b = b0; b < b1; ++b) mine += blocks(b);
+  int first = wave_scan(mine) - mine;
+  const uint64_t who = __ballot(index >= first && index < first + mine);
+  if (who == 0) return false;
+  int s = 0, blk = 0;
   if (index >= first && index < first + mine) {
     for (int b = b0; b < b1; ++b) {
-      const int n = (max(clip(a.cu_q[b + 1], a.Tq) - clip(a.cu_q[b], a.Tq), 0) + kBM - 1) / kBM;
+      const int n = blocks(b);
       if (index < first + n) {
-        sh[0] = b;
-        sh[1] = n - 1 - (index - first);  // a sequence's last block, the longest, first
+        s = b;
+        blk = n - 1 - (index - first);
         break;
       }
       first += n;
     }
   }
-  __syncthreads();
-  const int b = sh[0], blk = sh[1];
-  __syncthreads();
-  const int q0 = clip(a.cu_q[b], a.Tq), nq = clip(a.cu_q[b + 1], a.Tq) - q0;
-  const int k0 = clip(a.cu_k[b], a.Tk), nk = max(clip(a.cu_k[b + 1], a.Tk) - k0, 0);
+  seq = __builtin_amdgcn_readlane(s, __builtin_ctzll(who));
+  block = __builtin_amdgcn_readlane(blk, __builtin_ctzll(who));
+  return true;
+}
+
+template <bool kF16, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kernel(LatentExpandedArgs a) {
+  constexpr int kBM = kWaves * 32;
+  __shared__ __align__(1024) uint8_t lds_tiles[kBuffers * kTileBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, g = lane >> 5;
+  const int head = blockIdx.x % a.H, index = blockIdx.x / a.H;
+  int b, blk;
+  if (!find_block<kBM>(a, index, b, blk)) return;
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int q0 = uniform(clip(a.cu_q[b], a.Tq)), nq = uniform(clip(a.cu_q[b + 1], a.Tq)) - q0;
+  const int k0 = uniform(clip(a.cu_k[b], a.Tk)), nk = max(uniform(clip(a.cu_k[b + 1], a.Tk)) - k0, 0);
 
   // ---- this lane's query row
   const int row = blk * kBM + wave * 32 + r;
   const bool row_ok = row < nq;
   const int limit = row_ok ? clip(nk - nq + row + 1, nk) : 0;  // keys it sees
   const int keys = clip(nk - nq + min(blk * kBM + kBM, nq), nk);  // keys the block sees
-  const uint16_t* qs = a.q + (int64_t)(q0 + (row_ok ? row : 0)) * a.q_tok + (int64_t)head * a.q_head;
-  v4i q[12];
+  const int tiles = (keys + kTile - 1) / kTile;
+  // the wave's rows: keys that all of them see (tiles before need no mask), and that any of them sees
+  const int w0 = blk * kBM + wave * 32;
+  const int all = w0 + 32 <= nq ? clip(nk - nq + w0 + 1, nk) : 0;
+  const int any = w0 < nq ? clip(nk - nq + min(w0 + 32, nq), nk) : 0;
+
+  // ---- copies: this wave's share of a tile. In a full tile all rows of a copy lie one lane offset from a
+  // uniform address; in the last tile keys past the block's repeat its last (finite, and masked).
+  constexpr int kKvCopies = 32 / kWaves, kRopeCopies = 8 / kWaves, kCopies = kKvCopies + kRopeCopies;
+  const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.kv + (int64_t)k0 * a.kv_tok + (int64_t)head * a.kv_head);
+  const uint8_t* rope = reinterpret_cast<const uint8_t*>(a.rope + (int64_t)k0 * a.ld_rope);
+  const int64_t kv_step = a.kv_tok * 2, rope_step = a.ld_rope * 2;
+  const bool near = kv_step < (1 << 28) && rope_step < (1 << 27);  // lane offsets fit 32 bits
+  const uint32_t kv_col = ((lane & 31) ^ (g * 8)) << 4, rope_col = ((lane & 7) ^ ((lane >> 4) & 3)) << 4;
+  const uint32_t kv_off = (uint32_t)(2 * g * kv_step) + kv_col, rope_off = (uint32_t)((lane >> 3) * rope_step) + rope_col;
+  const uint32_t lds = lds_addr(lds_tiles);
+  auto copy_tile = [&](int t, int place) {
+    const uint32_t at = lds + place * kTileBytes;
+    const bool full = near && (t + 1) * kTile <= keys;
 #pragma unroll
-  for (int ks = 0; ks < 12; ++ks) {
-    q[ks] = v4i{0, 0, 0, 0};
-    if (row_ok) q[ks] = *reinterpret_cast<const v4i*>(qs + 16 * ks + 8 * g);
-  }
+    for (int j = 0; j < kKvCopies; ++j) {
+      const int p = wave * kKvCopies + j;
+      const int key = t * kTile + 16 * (p >> 3) + 4 * (p & 3) + ((p >> 2) & 1);
+      if (full) copy16_m0(kv + key * kv_step, kv_off, at + p * kPairStride);
+      else copy16_m0(kv + min(key + 2 * g, keys - 1) * kv_step + kv_col, at + p * kPairStride);
+    }
+#pragma unroll
+    for (int j = 0; j < kRopeCopies; ++j) {
+      const int p = wave * kRopeCopies + j;
+      const int key = t * kTile + 8 * p;
+      if (full) copy16_m0(rope + key * rope_step, rope_off, at + kRopeAt + p * kRopeStride);
+      else copy16_m0(rope + min(key + (lane >> 3), keys - 1) * rope_step + rope_col, at + kRopeAt + p * kRopeStride);
+    }
+  };
+
+  v4i q[12];
   v16f acc[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
   float m = kNegInf, l = 0.f;
-  const float c = a.scale * 1.44269504088896341f;
-  const uint32_t lds = lds_addr(tile);
-  const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.kv + (int64_t)k0 * a.kv_tok + (int64_t)head * a.kv_head);
-  const uint8_t* rope = reinterpret_cast<const uint8_t*>(a.rope + (int64_t)k0 * a.ld_rope);
 
-  for (int t0 = 0; t0 < keys; t0 += kTile) {
-    // the tile into LDS; keys past the block's repeat its last (finite, and masked)
+  if (tiles > 0) {
+    const uint16_t* qs = a.q + (int64_t)(q0 + (row_ok ? row : 0)) * a.q_tok + (int64_t)head * a.q_head;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int kk = (wave * 8 + j) * 2 + (lane >> 5);
-      const int64_t key = min(t0 + kk, keys - 1);
-      copy16_from(kv + key * a.kv_tok * 2 + (((lane & 31) ^ swz(kk)) << 4), lds + (wave * 8 + j) * 1024);
+    for (int ks = 0; ks < 12; ++ks) {
+      q[ks] = v4i{0, 0, 0, 0};
+      if (row_ok) q[ks] = *reinterpret_cast<const v4i*>(qs + 16 * ks + 8 * g);
     }
+    // a negative scale is the queries' sign, so that the largest score in log2 is that of the largest product; a
+    // scale of zero is as good as zero (masked products are infinite)
+    const int flip = a.scale < 0.f ? (int)0x80008000 : 0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int kk = (wave * 2 + j) * 8 + (lane >> 3);
-      const int64_t key = min(t0 + kk, keys - 1);
-      copy16_from(rope + key * a.ld_rope * 2 + (((lane & 7) ^ lds_swizzle(kk)) << 4),
-                  lds + kTile * kKvRow + (wave * 2 + j) * 1024);
-    }
-    wait_copies();
-    __syncthreads();
+    for (int ks = 0; ks < 12; ++ks) q[ks] ^= v4i{flip, flip, flip, flip};
+    const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 0x1p-120f);
+#pragma unroll
+    for (int ks = 0; ks < 12; ++ks) asm volatile("" : "+v"(q[ks]));  // loaded before the copies are counted
 
-    // ---- scores of 2 x 32 keys: lane (r, g), register i: key 8 (i / 4) + 4 g + i % 4
-    v16f s[2];
+    copy_tile(0, 0);
+    if (tiles > 1) copy_tile(1, 1);
+
+    // ---- LDS addresses within a tile
+    typedef __attribute__((address_space(3))) const v4i lds_v4i;
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    auto row_at = [](int key) {  // of 16
+      return (((key & 1) << 2) + ((key >> 2) & 3)) * kPairStride + ((key >> 1) & 1) * 512;
+    };
+    const int second = (r >> 1) & 1;
+    const uint32_t key_base = (r >> 4) * 8 * kPairStride + row_at(r & 15) + (g << 4);
+    const uint32_t key_low = key_base + 128 * second, key_high = key_base - 128 * second;  // steps 0 .. 3 and 4 .. 7
+    const uint32_t rope_base = kRopeAt + (r >> 3) * kRopeStride + (r & 7) * 128;
+    const uint32_t rope_even = rope_base + ((g ^ ((r >> 1) & 3)) << 4), rope_odd = rope_base + (((2 + g) ^ ((r >> 1) & 3)) << 4);
+    const int vk = 4 * g + ((lane >> 2) & 3);  // the row this lane addresses (and 8 further on), of 16
+    const uint32_t value_base = row_at(vk) + 256 + (((lane >> 4) & 1) << 5) + (((lane >> 1) & 1) << 4) + 8 * (lane & 1);
+    const uint32_t value_low = value_base + 128 * ((vk >> 1) & 1), value_high = value_base - 128 * ((vk >> 1) & 1);  // d < 2, d >= 2
+
+    int place = 0;
+    for (int t = 0; t < tiles; ++t) {
+      if (t + 1 < tiles) wait_copies_upto<kCopies>();
+      else wait_copies();
+      lds_barrier();  // tile t is there for every wave, and all are done with tile t - 1
+      const int after = place == 0 ? 2 : place - 1;
+      if (t + 2 < tiles) copy_tile(t + 2, after);
+      const uint32_t tile = lds + place * kTileBytes;
+      place = place == 2 ? 0 : place + 1;
+      const int t0 = t * kTile;
+      if (t0 >= any) continue;  // none of the wave's rows sees these keys
+
+      // ---- scores of 2 x 32 keys: lane (r, g), register i: key 8 (i / 4) + 4 g + i % 4
+      v16f s[2];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      const int kk = kt * 32 + r;
+      for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+        for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        const v4i k = *reinterpret_cast<const v4i*>(tile + kk * kKvRow + (((2 * ks + g) ^ swz(kk)) << 4));
-        s[kt] = mfma<kF16>(k, q[ks], s[kt]);
-      }
+        for (int ks = 0; ks < 8; ++ks) {
+          const v4i k = *reinterpret_cast<lds_v4i*>(tile + (ks < 4 ? key_low : key_high) + kt * 16 * kPairStride + 32 * ks);
+          s[kt] = mfma<kF16>(k, q[ks], s[kt]);
+        }
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const v4i k = *reinterpret_cast<const v4i*>(tile + kTile * kKvRow + kk * 128 + (((2 * ks + g) ^ lds_swizzle(kk)) << 4));
-        s[kt] = mfma<kF16>(k, q[8 + ks], s[kt]);
-      }
-    }
-    float top = kNegInf;
-    const bool masked = __any(t0 + kTile > limit);
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[kt][i] *= c;
-        if (masked && t0 + kt * 32 + 8 * (i >> 2) + 4 * g + (i & 3) >= limit) s[kt][i] = kNegInf;
-        top = fmaxf(top, s[kt][i]);
-      }
-    top = fmaxf(top, __shfl_xor(top, 32));
-    if (__any(top > m + kSlack)) {
-      const float next = fmaxf(m, top);
-      const float f = m == next ? 1.f : __builtin_amdgcn_exp2f(m - next);
-      m = next;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) acc[d] *= f;
-    }
-    const float ref = m == kNegInf ? 0.f : m;
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[kt][i] = __builtin_amdgcn_exp2f(s[kt][i] - ref);
-        l += s[kt][i];
-      }
-    // ---- O^T += V^T P^T: 16 keys a step, of which lane g holds 4 g + {0..3} and 8 + 4 g + {0..3}
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        v4i p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = (int)pack16<kF16>(s[kt][8 * u + 2 * i], s[kt][8 * u + 2 * i + 1]);
-        typedef short v4s __attribute__((ext_vector_type(4)));
-        typedef __attribute__((address_space(3))) v4s lds_v4s;
-        // the key row this lane addresses (and the one 8 further on), and its 8 bytes of 32 columns
-        const int vk = kt * 32 + 16 * u + 4 * g + ((lane >> 2) & 3);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const int col = 16 + 4 * d + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-          const uint8_t* x = tile + vk * kKvRow + ((col ^ swz(vk)) << 4) + 8 * (lane & 1);
-          const uint8_t* y = tile + (vk + 8) * kKvRow + ((col ^ swz(vk + 8)) << 4) + 8 * (lane & 1);
-          const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)x));
-          const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)y));
-          acc[d] = mfma<kF16>(v4i{lo[0], lo[1], hi[0], hi[1]}, p, acc[d]);
+        for (int ks = 0; ks < 4; ++ks) {
+          const v4i k = *reinterpret_cast<lds_v4i*>(tile + ((ks & 1) ? rope_odd : rope_even) + kt * 4 * kRopeStride + 64 * (ks >> 1));
+          s[kt] = mfma<kF16>(k, q[8 + ks], s[kt]);
         }
       }
-    __syncthreads();
+      if (t0 + kTile > all) {
+        const int left = limit - t0 - 4 * g;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (kt * 32 + 8 * (i >> 2) + (i & 3) >= left) s[kt][i] = kNegInf;
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i >> 4][i & 15]);
+      const unsigned bits = __float_as_uint(top);
+      const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+      top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * c;
+      if (__any(top > m + kSlack)) {
+        const float next = fmaxf(m, top);
+        const float f = m == next ? 1.f : __builtin_amdgcn_exp2f(m - next);
+        m = next;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[d] *= f;
+      }
+      const float ref = m == kNegInf ? 0.f : m;
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], c, -ref));
+        s[i >> 4][i & 15] = x;
+        sum[i & 1] += x;
+      }
+      l += sum[0] + sum[1];
+      // ---- O^T += V^T P^T: 16 keys a step, of which lane g holds 4 g + {0..3} and 8 + 4 g + {0..3}
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          v4i p;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = (int)pack16<kF16>(s[kt][8 * u + 2 * i], s[kt][8 * u + 2 * i + 1]);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t at = tile + (d < 2 ? value_low : value_high) + (2 * kt + u) * 8 * kPairStride + 64 * d;
+            const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at)));
+            const v2i hi = __builtin_bit_cast(
+                v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at + 2 * kPairStride)));
+            acc[d] = mfma<kF16>(v4i{lo[0], lo[1], hi[0], hi[1]}, p, acc[d]);
+          }
+        }
+    }
   }
 
   l += __shfl_xor(l, 32);
   if (!row_ok) return;
   const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key is zero
-  uint16_t* dst = a.out + (int64_t)(q0 + row) * a.o_tok + (int64_t)head * a.o_head + 4 * g;
+  uint16_t* dst = a.out + (int64_t)(q0 + row) * a.o_tok + (int64_t)head * a.o_head + 16 * g;
 #pragma unroll
-  for (int d = 0; d < 4; ++d)
+  for (int d = 0; d < 4; ++d) {
+    // lanes g = 0 and 1 of a row swap quads of columns, so that each stores 16 neighbouring ones
+    uint32_t u[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint2*>(dst + 32 * d + 8 * i) =
-          make_uint2(pack16<kF16>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv),
-                     pack16<kF16>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv));
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const auto v = __builtin_amdgcn_permlane32_swap(
+            pack16<kF16>(acc[d][4 * h + 2 * i] * inv, acc[d][4 * h + 2 * i + 1] * inv),
+            pack16<kF16>(acc[d][8 + 4 * h + 2 * i] * inv, acc[d][8 + 4 * h + 2 * i + 1] * inv), false, false);
+        u[h][i] = v[0];
+        u[h][2 + i] = v[1];
+      }
+    uint4* p = reinterpret_cast<uint4*>(dst + 32 * d);
+    p[0] = make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]);
+    p[1] = make_uint4(u[1][0], u[1][1], u[1][2], u[1][3]);
+  }
+}
+
+template <bool kF16, int kWaves>
+void launch(const LatentExpandedArgs& args, hipStream_t stream) {
+  const dim3 grid((unsigned)((args.Tq / (kWaves * 32) + (args.Tq < args.B ? args.Tq : args.B)) * (int64_t)args.H));
+  hipLaunchKernelGGL((latent_expanded_kernel<kF16, kWaves>), grid, dim3(kWaves * 64), 0, stream, args);
 }
 
 }  // namespace
 
-int64_t latent_expanded_blocks(int64_t Tq, int64_t B) { return Tq / kBM + (Tq < B ? Tq : B); }
+int64_t latent_expanded_blocks(int64_t Tq, int64_t B) { return Tq / 128 + (Tq < B ? Tq : B); }
 
 hipError_t launch_latent_expanded(const LatentExpandedArgs& args, bool f16, hipStream_t stream) {
-  const dim3 grid((unsigned)(latent_expanded_blocks(args.Tq, args.B) * args.H));
-  if (f16) hipLaunchKernelGGL((latent_expanded_kernel<true>), grid, dim3(256), 0, stream, args);
-  else hipLaunchKernelGGL((latent_expanded_kernel<false>), grid, dim3(256), 0, stream, args);
+  // 256 rows a workgroup where that fills the card and the sequences are long enough on average
+  const bool many = (int64_t)args.Tq * args.H >= 256 * 256 && args.Tq > 128 * (int64_t)args.B;
+  if (f16) many ? launch<true, 8>(args, stream) : launch<true, 4>(args, stream);
+  else many ? launch<false, 8>(args, stream) : launch<false, 4>(args, stream);
   return hipGetLastError();
 }
 
