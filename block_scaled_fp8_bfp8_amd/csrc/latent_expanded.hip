@@ -7,15 +7,16 @@
 // over the keys j of t's sequence up to t (the last query token sees the last key).
 //
 // One pass with the running maximum and sum of the softmax. A workgroup takes 32 query rows of one head
-// a wave and walks the keys in tiles of 64, copied straight to LDS two tiles ahead. Both products are
+// a wave and walks the keys in tiles of 64, copied straight to LDS a tile ahead. Both products are
 // 32x32x16 matrix-core products, formed transposed (S^T = K Q^T, O^T = V^T P^T): a lane then holds
 // scores of one query row, r = lane % 32, which are its operand of the second product without any
 // exchange, and the running maximum and sum are plain per-lane numbers. V is read from the tile with
 // transposing LDS reads.
 //
-// Bound by the matrix cores: with 8 waves a workgroup (256 rows, 2 waves a SIMD) one wave's softmax runs
-// beside another's products. The LDS layout leaves the copies one lane offset for all of a tile's rows, and
-// the reads two addresses each, with constant offsets for everything else.
+// Bound by the matrix cores and by how well their time is shared: with 8 waves a workgroup (256 rows) two
+// waves a SIMD, of which the second multiplies a tile's values one tile later, so that one wave's softmax
+// runs beside the other's products. The LDS layout leaves the copies one lane offset for all of a tile's rows,
+// and the reads two addresses each, with constant offsets for everything else.
 #include "device_common.h"
 #include "latent.h"
 #include "launch.h"
@@ -25,8 +26,6 @@ namespace bfp8 {
 namespace {
 
 constexpr int kTile = 64;    // keys of a tile
-constexpr int kNope = 128;   // key dimensions of a head before the rotary part
-constexpr int kV = 128;      // value dimensions
 constexpr float kNegInf = -__builtin_inff();
 // The running maximum may lag by a factor of 2^kSlack: weights stay within 2^8, far inside fp16 and
 // bf16, and the accumulator is rescaled only when a tile exceeds that.
@@ -114,7 +113,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
 
   // ---- copies: this wave's share of a tile. In a full tile all rows of a copy lie one lane offset from a
   // uniform address; in the last tile keys past the block's repeat its last (finite, and masked).
-  constexpr int kKvCopies = 32 / kWaves, kRopeCopies = 8 / kWaves, kCopies = kKvCopies + kRopeCopies;
+  constexpr int kKvCopies = 32 / kWaves, kRopeCopies = 8 / kWaves;
   const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.kv + (int64_t)k0 * a.kv_tok + (int64_t)head * a.kv_head);
   const uint8_t* rope = reinterpret_cast<const uint8_t*>(a.rope + (int64_t)k0 * a.ld_rope);
   const int64_t kv_step = a.kv_tok * 2, rope_step = a.ld_rope * 2;
@@ -122,23 +121,26 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
   const uint32_t kv_col = ((lane & 31) ^ (g * 8)) << 4, rope_col = ((lane & 7) ^ ((lane >> 4) & 3)) << 4;
   const uint32_t kv_off = (uint32_t)(2 * g * kv_step) + kv_col, rope_off = (uint32_t)((lane >> 3) * rope_step) + rope_col;
   const uint32_t lds = lds_addr(lds_tiles);
-  auto copy_tile = [&](int t, int place) {
-    const uint32_t at = lds + place * kTileBytes;
+  // first key of this wave's pairs and of its rotary groups
+  const int kv_key = kWaves == 8 ? 16 * (wave >> 1) + (wave & 1) : 16 * wave, rope_key = wave * (64 / kWaves);
+  const uint8_t* kv_next = kv + kv_key * kv_step;        // of the next tile to copy
+  const uint8_t* rope_next = rope + rope_key * rope_step;
+  auto copy_tile = [&](int t, uint32_t tile) {  // tiles in order
+    const uint32_t kv_at = tile + wave * kKvCopies * kPairStride, rope_at = tile + kRopeAt + wave * kRopeCopies * kRopeStride;
     const bool full = near && (t + 1) * kTile <= keys;
 #pragma unroll
     for (int j = 0; j < kKvCopies; ++j) {
-      const int p = wave * kKvCopies + j;
-      const int key = t * kTile + 16 * (p >> 3) + 4 * (p & 3) + ((p >> 2) & 1);
-      if (full) copy16_m0(kv + key * kv_step, kv_off, at + p * kPairStride);
-      else copy16_m0(kv + min(key + 2 * g, keys - 1) * kv_step + kv_col, at + p * kPairStride);
+      const int key = 4 * (j & 3) + (j >> 2);
+      if (full) copy16_m0(kv_next + key * kv_step, kv_off, kv_at + j * kPairStride);
+      else copy16_m0(kv + min(t * kTile + kv_key + key + 2 * g, keys - 1) * kv_step + kv_col, kv_at + j * kPairStride);
     }
 #pragma unroll
     for (int j = 0; j < kRopeCopies; ++j) {
-      const int p = wave * kRopeCopies + j;
-      const int key = t * kTile + 8 * p;
-      if (full) copy16_m0(rope + key * rope_step, rope_off, at + kRopeAt + p * kRopeStride);
-      else copy16_m0(rope + min(key + (lane >> 3), keys - 1) * rope_step + rope_col, at + kRopeAt + p * kRopeStride);
+      if (full) copy16_m0(rope_next + 8 * j * rope_step, rope_off, rope_at + j * kRopeStride);
+      else copy16_m0(rope + min(t * kTile + rope_key + 8 * j + (lane >> 3), keys - 1) * rope_step + rope_col, rope_at + j * kRopeStride);
     }
+    kv_next += kTile * kv_step;
+    rope_next += kTile * rope_step;
   };
 
   v4i q[12];
@@ -165,8 +167,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
 #pragma unroll
     for (int ks = 0; ks < 12; ++ks) asm volatile("" : "+v"(q[ks]));  // loaded before the copies are counted
 
-    copy_tile(0, 0);
-    if (tiles > 1) copy_tile(1, 1);
+    copy_tile(0, lds);
 
     // ---- LDS addresses within a tile
     typedef __attribute__((address_space(3))) const v4i lds_v4i;
@@ -184,17 +185,36 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
     const uint32_t value_base = row_at(vk) + 256 + (((lane >> 4) & 1) << 5) + (((lane >> 1) & 1) << 4) + 8 * (lane & 1);
     const uint32_t value_low = value_base + 128 * ((vk >> 1) & 1), value_high = value_base - 128 * ((vk >> 1) & 1);  // d < 2, d >= 2
 
+    // ---- O^T += V^T P^T: 16 keys a step, of which lane g holds 4 g + {0..3} and 8 + 4 g + {0..3}
+    v4i p[4];
+    auto values = [&](uint32_t tile) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const uint32_t at = tile + (d < 2 ? value_low : value_high) + u * 8 * kPairStride + 64 * d;
+          const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at)));
+          const v2i hi = __builtin_bit_cast(
+              v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at + 2 * kPairStride)));
+          acc[d] = mfma<kF16>(v4i{lo[0], lo[1], hi[0], hi[1]}, p[u], acc[d]);
+        }
+    };
+
+    const bool late = kWaves == 8 && wave >= 4;        // the second wave of its SIMD
+    const int mine = (any + kTile - 1) / kTile;        // tiles of which a row of this wave sees a key
+    uint32_t tile = lds, tile_before = lds;
     int place = 0;
     for (int t = 0; t < tiles; ++t) {
-      if (t + 1 < tiles) wait_copies_upto<kCopies>();
-      else wait_copies();
-      lds_barrier();  // tile t is there for every wave, and all are done with tile t - 1
-      const int after = place == 0 ? 2 : place - 1;
-      if (t + 2 < tiles) copy_tile(t + 2, after);
-      const uint32_t tile = lds + place * kTileBytes;
-      place = place == 2 ? 0 : place + 1;
+      wait_copies();
+      lds_barrier();  // tile t is there for every wave, and all are done with tile t - 2
+      place = place == kBuffers - 1 ? 0 : place + 1;
+      const uint32_t next_tile = lds + place * kTileBytes, tile_at_hand = tile;
+      if (t + 1 < tiles) copy_tile(t + 1, next_tile);
+      if (late && t > 0 && t - 1 < mine) values(tile_before);
+      tile_before = tile;
+      tile = next_tile;
+      if (t >= mine) continue;  // none of the wave's rows sees these keys
       const int t0 = t * kTile;
-      if (t0 >= any) continue;  // none of the wave's rows sees these keys
 
       // ---- scores of 2 x 32 keys: lane (r, g), register i: key 8 (i / 4) + 4 g + i % 4
       v16f s[2];
@@ -204,12 +224,12 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
         for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const v4i k = *reinterpret_cast<lds_v4i*>(tile + (ks < 4 ? key_low : key_high) + kt * 16 * kPairStride + 32 * ks);
+          const v4i k = *reinterpret_cast<lds_v4i*>(tile_at_hand + (ks < 4 ? key_low : key_high) + kt * 16 * kPairStride + 32 * ks);
           s[kt] = mfma<kF16>(k, q[ks], s[kt]);
         }
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          const v4i k = *reinterpret_cast<lds_v4i*>(tile + ((ks & 1) ? rope_odd : rope_even) + kt * 4 * kRopeStride + 64 * (ks >> 1));
+          const v4i k = *reinterpret_cast<lds_v4i*>(tile_at_hand + ((ks & 1) ? rope_odd : rope_even) + kt * 4 * kRopeStride + 64 * (ks >> 1));
           s[kt] = mfma<kF16>(k, q[8 + ks], s[kt]);
         }
       }
@@ -244,24 +264,12 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
         sum[i & 1] += x;
       }
       l += sum[0] + sum[1];
-      // ---- O^T += V^T P^T: 16 keys a step, of which lane g holds 4 g + {0..3} and 8 + 4 g + {0..3}
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          v4i p;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = (int)pack16<kF16>(s[kt][8 * u + 2 * i], s[kt][8 * u + 2 * i + 1]);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const uint32_t at = tile + (d < 2 ? value_low : value_high) + (2 * kt + u) * 8 * kPairStride + 64 * d;
-            const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at)));
-            const v2i hi = __builtin_bit_cast(
-                v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at + 2 * kPairStride)));
-            acc[d] = mfma<kF16>(v4i{lo[0], lo[1], hi[0], hi[1]}, p, acc[d]);
-          }
-        }
+      for (int i = 0; i < 16; ++i)
+        p[i >> 2][i & 3] = (int)pack16<kF16>(s[i >> 3][2 * (i & 7)], s[i >> 3][2 * (i & 7) + 1]);
+      if (!late) values(tile_at_hand);
     }
+    if (late && tiles - 1 < mine) values(tile_before);
   }
 
   l += __shfl_xor(l, 32);
