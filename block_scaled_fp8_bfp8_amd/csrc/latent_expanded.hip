@@ -40,6 +40,7 @@ constexpr int kPairStride = 1024 + 16, kRopeStride = 1024 + 64;
 constexpr int kRopeAt = kTile / 2 * kPairStride;
 constexpr int kTileBytes = kRopeAt + kTile / 8 * kRopeStride;
 constexpr int kBuffers = 3;
+constexpr int kRing = 5;  // operands in registers
 
 template <bool kF16>
 __device__ __forceinline__ v16f mfma(const v4i& a, const v4i& b, const v16f& c) {
@@ -127,17 +128,26 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
   const uint8_t* rope_next = rope + rope_key * rope_step;
   auto copy_tile = [&](int t, uint32_t tile) {  // tiles in order
     const uint32_t kv_at = tile + wave * kKvCopies * kPairStride, rope_at = tile + kRopeAt + wave * kRopeCopies * kRopeStride;
-    const bool full = near && (t + 1) * kTile <= keys;
+    if (near && (t + 1) * kTile <= keys) {
+      const uint8_t* src = kv_next;
 #pragma unroll
-    for (int j = 0; j < kKvCopies; ++j) {
-      const int key = 4 * (j & 3) + (j >> 2);
-      if (full) copy16_m0(kv_next + key * kv_step, kv_off, kv_at + j * kPairStride);
-      else copy16_m0(kv + min(t * kTile + kv_key + key + 2 * g, keys - 1) * kv_step + kv_col, kv_at + j * kPairStride);
-    }
+      for (int j = 0; j < kKvCopies; ++j) {  // keys 0, 4, 8, 12 and, of 8 copies, 1, 5, 9, 13
+        copy16_m0(src, kv_off, kv_at + j * kPairStride);
+        src += j == 3 ? kv_step - 12 * kv_step : 4 * kv_step;
+      }
 #pragma unroll
-    for (int j = 0; j < kRopeCopies; ++j) {
-      if (full) copy16_m0(rope_next + 8 * j * rope_step, rope_off, rope_at + j * kRopeStride);
-      else copy16_m0(rope + min(t * kTile + rope_key + 8 * j + (lane >> 3), keys - 1) * rope_step + rope_col, rope_at + j * kRopeStride);
+      for (int j = 0; j < kRopeCopies; ++j) copy16_m0(rope_next + 8 * j * rope_step, rope_off, rope_at + j * kRopeStride);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kKvCopies; ++j) {
+        const int key = t * kTile + kv_key + 4 * (j & 3) + (j >> 2) + 2 * g;
+        copy16_m0(kv + min(key, keys - 1) * kv_step + kv_col, kv_at + j * kPairStride);
+      }
+#pragma unroll
+      for (int j = 0; j < kRopeCopies; ++j) {
+        const int key = t * kTile + rope_key + 8 * j + (lane >> 3);
+        copy16_m0(rope + min(key, keys - 1) * rope_step + rope_col, rope_at + j * kRopeStride);
+      }
     }
     kv_next += kTile * kv_step;
     rope_next += kTile * rope_step;
@@ -188,16 +198,24 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
     // ---- O^T += V^T P^T: 16 keys a step, of which lane g holds 4 g + {0..3} and 8 + 4 g + {0..3}
     v4i p[4];
     auto values = [&](uint32_t tile) {
+      auto value_at = [&](int n) {  // operand of product n
+        const int u = n >> 2, d = n & 3;
+        const uint32_t at = tile + (d < 2 ? value_low : value_high) + u * 8 * kPairStride + 64 * d;
+        const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at)));
+        const v2i hi = __builtin_bit_cast(
+            v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at + 2 * kPairStride)));
+        return v4i{lo[0], lo[1], hi[0], hi[1]};
+      };
+      v4i v[kRing];  // operands are read kRing - 1 products ahead (and kept there: the compiler reads them late)
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int n = 0; n + 1 < kRing; ++n) v[n] = value_at(n);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint32_t at = tile + (d < 2 ? value_low : value_high) + u * 8 * kPairStride + 64 * d;
-          const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at)));
-          const v2i hi = __builtin_bit_cast(
-              v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at + 2 * kPairStride)));
-          acc[d] = mfma<kF16>(v4i{lo[0], lo[1], hi[0], hi[1]}, p[u], acc[d]);
-        }
+      for (int n = 0; n < 16; ++n) {
+        if (n + kRing - 1 < 16) v[(n + kRing - 1) % kRing] = value_at(n + kRing - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        acc[n & 3] = mfma<kF16>(v[n % kRing], p[n >> 2], acc[n & 3]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
 
     const bool late = kWaves == 8 && wave >= 4;        // the second wave of its SIMD
@@ -218,19 +236,26 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
 
       // ---- scores of 2 x 32 keys: lane (r, g), register i: key 8 (i / 4) + 4 g + i % 4
       v16f s[2];
+      {
+        auto key_at = [&](int n) {  // operand of product n
+          const int kt = n & 1, ks = n >> 1;
+          return ks < 8 ? *reinterpret_cast<lds_v4i*>(tile_at_hand + (ks < 4 ? key_low : key_high) + kt * 16 * kPairStride + 32 * ks)
+                        : *reinterpret_cast<lds_v4i*>(tile_at_hand + ((ks & 1) ? rope_odd : rope_even) + kt * 4 * kRopeStride +
+                                                      64 * ((ks - 8) >> 1));
+        };
+        v4i k[kRing];
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
+        for (int n = 0; n + 1 < kRing; ++n) k[n] = key_at(n);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const v4i k = *reinterpret_cast<lds_v4i*>(tile_at_hand + (ks < 4 ? key_low : key_high) + kt * 16 * kPairStride + 32 * ks);
-          s[kt] = mfma<kF16>(k, q[ks], s[kt]);
-        }
+          for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const v4i k = *reinterpret_cast<lds_v4i*>(tile_at_hand + ((ks & 1) ? rope_odd : rope_even) + kt * 4 * kRopeStride + 64 * (ks >> 1));
-          s[kt] = mfma<kF16>(k, q[8 + ks], s[kt]);
+        for (int n = 0; n < 24; ++n) {
+          if (n + kRing - 1 < 24) k[(n + kRing - 1) % kRing] = key_at(n + kRing - 1);
+          __builtin_amdgcn_sched_barrier(0);
+          s[n & 1] = mfma<kF16>(k[n % kRing], q[n >> 1], s[n & 1]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       if (t0 + kTile > all) {
