@@ -295,6 +295,32 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
+template <int kValue>
+struct Const {
+  static constexpr int v = kValue;
+};
+// Sum over the lanes of a wave, and the largest of values >= 0 (NaN if one is NaN), in every lane: the
+// steps of wave_scan, whose last lane then holds the whole.
+template <typename F>
+__device__ __forceinline__ float wave_fold(float v, F f) {
+  auto moved = [](float x, auto ctrl, auto rows) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::v, decltype(rows)::v, 0xf, false));
+  };
+  v = f(v, moved(v, Const<0x111>{}, Const<0xf>{}));
+  v = f(v, moved(v, Const<0x112>{}, Const<0xf>{}));
+  v = f(v, moved(v, Const<0x114>{}, Const<0xf>{}));
+  v = f(v, moved(v, Const<0x118>{}, Const<0xf>{}));
+  v = f(v, moved(v, Const<0x142>{}, Const<0xa>{}));
+  v = f(v, moved(v, Const<0x143>{}, Const<0xc>{}));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_fold(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_fold(v, [](float a, float b) { return max_nan(a, b); });
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)p; }
 
 // XOR swizzle of the 16-byte columns of a 128-byte LDS row. A fragment read has 16 lanes

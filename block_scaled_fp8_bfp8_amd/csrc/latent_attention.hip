@@ -782,6 +782,18 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
   const int lane = threadIdx.x & 63;
   const int row = blockIdx.y * 4 + (threadIdx.x >> 6);
   if (row >= desc.rows || desc.parts > kMaxParts || desc.slot + desc.parts > a.max_slots) return;
+  // the first parts' states are on their way while the statistics are joined
+  constexpr int kTogether = 8;
+  const float* src = a.states + ((int64_t)desc.slot * kBM + row) * kLatentDim + lane * 8;
+  v4f x[kTogether], y[kTogether];
+  auto read_states = [&](int p0, int last) {
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      const v4f* at = reinterpret_cast<const v4f*>(src + (int64_t)min(p0 + k, last) * kBM * kLatentDim);
+      x[k] = at[0], y[k] = at[1];
+    }
+  };
+  read_states(0, desc.parts - 1);
   constexpr int kEach = kMaxParts / 64;
   float f[kEach], sums[kEach];
   float m = kNegInf;
@@ -808,16 +820,19 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
 #pragma unroll
   for (int mask = 1; mask < 64; mask <<= 1) l += __shfl_xor(l, mask);
   float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const float* src = a.states + ((int64_t)desc.slot * kBM + row) * kLatentDim + lane * 8;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int n = min(desc.parts - 64 * i, 64);
-    for (int p = 0; p < n; ++p) {
-      const float fp = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f[i]), p));
-      const v4f* at = reinterpret_cast<const v4f*>(src + (int64_t)(64 * i + p) * kBM * kLatentDim);
-      const v4f x = at[0], y = at[1];
+    for (int p0 = 0; p0 < n; p0 += kTogether) {
+      if (i + p0 > 0) read_states(64 * i + p0, desc.parts - 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fmaf(fp, x[j], o[j]), o[4 + j] = fmaf(fp, y[j], o[4 + j]);
+      for (int k = 0; k < kTogether; ++k) {
+        // (past the last part: its state again, times zero)
+        const float at = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f[i]), min(p0 + k, 63)));
+        const float fp = p0 + k < n ? at : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = fmaf(fp, x[k][j], o[j]), o[4 + j] = fmaf(fp, y[k][j], o[4 + j]);
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
@@ -865,8 +880,7 @@ LatentAttnPlan plan_latent_attn(int64_t T, int64_t B, int64_t H, int64_t max_key
     if (p.blocks * per_block < p.slots) p.slots = p.blocks * per_block;
     p.cuts = p.slots / 2;
   }
-  p.parts = p.blocks;
-  if (p.slots > 0 && p.parts < p.target_parts) p.parts = p.target_parts;
+  p.parts = p.blocks > p.slots ? p.blocks : p.slots;
   p.counts_bytes = p.slots ? ((16 + p.cuts * sizeof(Desc) + 255) / 256) * 256 : 0;
   p.stats_bytes = ((p.slots * bm * 2 * sizeof(float) + 255) / 256) * 256;
   p.states_bytes = p.slots * bm * kLatentDim * sizeof(float);

@@ -45,9 +45,7 @@ __global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* __res
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fmaf(y[i] * f, y[i] * f, sum);
-#pragma unroll
-      for (int mask = 1; mask < 64; mask <<= 1) sum += __shfl_xor(sum, mask);
-      return sum;
+      return wave_sum(sum);
     };
     const float sum = token_sum(1.0f);
     float rstd = 1.0f / sqrtf(sum / (float)kLatentDim + eps);
@@ -61,8 +59,7 @@ __global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* __res
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(y[i]));
-#pragma unroll
-  for (int mask = 1; mask < 64; mask <<= 1) amax = max_nan(amax, __shfl_xor(amax, mask));
+  amax = wave_max(amax);
   uint32_t code = 255;
   uint2 codes = make_uint2(0, 0);
   if (amax < __builtin_inff()) {
