@@ -36,7 +36,7 @@
 // of one sequence that a workgroup holds, and where there are fewer blocks than workgroups fit
 // the card, they are cut along their keys into parts whose float32 states (accumulator, maximum,
 // sum) a second launch joins in order.
-#include "device_common.h"
+#include "device_latent.h"
 #include "latent.h"
 #include "launch.h"
 

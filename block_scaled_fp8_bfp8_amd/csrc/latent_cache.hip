@@ -10,7 +10,7 @@
 // multiply it by a zero weight and stay finite.
 //
 // All three kernels are HBM-bound (a token: 1152 bytes read and 641 written, or the reverse).
-#include "device_common.h"
+#include "device_latent.h"
 #include "latent.h"
 #include "launch.h"
 

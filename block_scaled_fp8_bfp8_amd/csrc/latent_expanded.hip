@@ -17,7 +17,7 @@
 // waves a SIMD, of which the second multiplies a tile's values one tile later, so that one wave's softmax
 // runs beside the other's products. The LDS layout leaves the copies one lane offset for all of a tile's rows,
 // and the reads two addresses each, with constant offsets for everything else.
-#include "device_common.h"
+#include "device_latent.h"
 #include "latent.h"
 #include "launch.h"
 

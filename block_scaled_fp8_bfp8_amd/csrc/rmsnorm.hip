@@ -12,7 +12,7 @@
 // HBM-bound: x and the residual are read once, h, q and s written once (7 bytes an element in
 // bf16). A row lives in the registers of the threads that share it, 8 elements a chunk, so the
 // 16 lanes of a 128-wide group exchange its amax by lane shuffles.
-#include "device_common.h"
+#include "device_latent.h"
 #include "launch.h"
 
 namespace bfp8 {
