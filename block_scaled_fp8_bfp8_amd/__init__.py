@@ -786,9 +786,10 @@ def linear_fuses(m: int, n: int, k: int, ldx: int | None = None) -> bool:
 
 def _same_device(first: torch.Tensor, **others):
     """Every tensor on the first one's device (the launch runs on that device's current stream)."""
+    device = first.device
     for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _rmsnorm_quant(x, weight, residual, eps, out, e8: bool):
@@ -797,15 +798,20 @@ def _rmsnorm_quant(x, weight, residual, eps, out, e8: bool):
     _require(x, "x", x.dtype, 2)
     _require(weight, "weight", x.dtype, 1)
     m, k = x.shape
-    if x.stride(1) != 1 or weight.stride(0) != 1:
+    ldx, inner = x.stride()
+    if inner != 1 or weight.stride(0) != 1:
         raise ValueError("x must be contiguous along its columns, and weight contiguous")
     if weight.shape[0] != k:
         raise ValueError(f"weight has {weight.shape[0]} elements, x has {k} columns")
+    device = x.device
     h = x
     if residual is not None:
         _require(residual, "residual", x.dtype, 2)
-        h = torch.empty((m, k), dtype=x.dtype, device=x.device) if out is None else out
-        _require(h, "out", x.dtype, 2)
+        if out is None:
+            h = torch.empty_strided((m, k), (k, 1), dtype=x.dtype, device=device)
+        else:
+            h = out
+            _require(h, "out", x.dtype, 2)
         if residual.shape != x.shape or h.shape != x.shape:
             raise ValueError(f"residual and out must have x's shape {tuple(x.shape)}")
         if residual.stride(1) != 1 or h.stride(1) != 1:
@@ -813,18 +819,26 @@ def _rmsnorm_quant(x, weight, residual, eps, out, e8: bool):
     elif out is not None:
         raise ValueError("out holds x + residual: it needs a residual")
     _same_device(x, weight=weight, residual=residual, out=out)
-    q = torch.empty((m, -(-k // 128) * 128), dtype=torch.uint8, device=x.device)[:, :k]
+    groups = -(-k // 128)
+    # (whole buffers at their strides where nothing is padded: a view less to build)
+    if k == groups * 128:
+        q = torch.empty_strided((m, k), (k, 1), dtype=torch.uint8, device=device)
+    else:
+        q = torch.empty((m, groups * 128), dtype=torch.uint8, device=device)[:, :k]
     if e8:
         ld = max(-(-m // 4) * 4, 4)
-        scales = torch.empty((-(-k // 128), ld), dtype=torch.uint8, device=x.device)[:, :m].t()
+        if ld == m:
+            scales = torch.empty_strided((m, groups), (1, m), dtype=torch.uint8, device=device)
+        else:
+            scales = torch.empty((groups, ld), dtype=torch.uint8, device=device)[:, :m].t()
     else:
         ld = max(m, 1)
-        scales = torch.empty((-(-k // 128), m), dtype=torch.float32, device=x.device).t()
+        scales = torch.empty_strided((m, groups), (1, ld), dtype=torch.float32, device=device)
     lib = _native.lib()
     entry = lib.bfp8_rmsnorm_quant_ue8m0 if e8 else lib.bfp8_rmsnorm_quant
-    st = entry(x.data_ptr(), dt, m, k, x.stride(0), None if residual is None else residual.data_ptr(),
+    st = entry(x.data_ptr(), dt, m, k, ldx, None if residual is None else residual.data_ptr(),
                k if residual is None else residual.stride(0), weight.data_ptr(), eps, h.data_ptr(), h.stride(0),
-               q.data_ptr(), q.stride(0), scales.data_ptr(), ld, _stream(x.device))
+               q.data_ptr(), groups * 128, scales.data_ptr(), ld, _stream(device))
     _check(st, "bfp8_" + what)
     return q, scales, h
 
@@ -856,23 +870,26 @@ def _latent_cache_args(cache: torch.Tensor, scales: torch.Tensor):
     _require(cache, "cache", torch.uint8, 3)
     _require(scales, "scales", torch.uint8, 2)
     pages, page, row = cache.shape
-    if row != LATENT_ROW or tuple(scales.shape) != (pages, page):
+    if row != LATENT_ROW or scales.shape != (pages, page):
         raise ValueError(f"cache must be [pages, page, {LATENT_ROW}] and scales [pages, page], got "
                          f"{tuple(cache.shape)} and {tuple(scales.shape)}")
-    if cache.stride(2) != 1 or (page > 1 and (cache.stride(1) != LATENT_ROW or scales.stride(1) != 1)):
+    (ps, rs, bs), (ss, cs) = cache.stride(), scales.stride()
+    if bs != 1 or (page > 1 and (rs != LATENT_ROW or cs != 1)):
         raise ValueError("the rows of a page and their scales must be contiguous (pages may be apart)")
-    _same_device(cache, scales=scales)
-    # a single page's stride carries no meaning
-    ps, ss = (cache.stride(0), scales.stride(0)) if pages > 1 else (page * LATENT_ROW, page)
+    if scales.device != cache.device:
+        raise ValueError(f"scales is on {scales.device}, expected {cache.device}")
+    if pages == 1:  # a single page's stride carries no meaning
+        ps, ss = page * LATENT_ROW, page
     return cache.data_ptr(), ps, scales.data_ptr(), ss, pages, page
 
 
 def _page_table_args(table: torch.Tensor):
     _require(table, "page_table", torch.int32, 2)
     b, width = table.shape
-    if width > 1 and table.stride(1) != 1:
+    ts, inner = table.stride()
+    if width > 1 and inner != 1:
         raise ValueError("page_table must be contiguous along its rows")
-    return table.data_ptr(), table.stride(0) if b > 1 else max(width, 1), width
+    return table.data_ptr(), ts if b > 1 else max(width, 1), width
 
 
 def _starts_arg(cu: torch.Tensor, name: str, b: int):
@@ -918,9 +935,10 @@ def latent_cache_read(cache: torch.Tensor, scales: torch.Tensor, page_table: tor
     _starts_arg(cu_tokens, "cu_tokens", page_table.shape[0])
     if out is None:
         out = torch.empty((total, LATENT_DIM + ROPE_DIM), dtype=torch.bfloat16, device=cache.device)
-    _require(out, "out", torch.bfloat16, 2)
-    if tuple(out.shape) != (total, LATENT_DIM + ROPE_DIM) or out.stride(1) != 1:
-        raise ValueError(f"out must be [{total}, {LATENT_DIM + ROPE_DIM}] with contiguous rows")
+    else:
+        _require(out, "out", torch.bfloat16, 2)
+        if out.shape != (total, LATENT_DIM + ROPE_DIM) or out.stride(1) != 1:
+            raise ValueError(f"out must be [{total}, {LATENT_DIM + ROPE_DIM}] with contiguous rows")
     _same_device(cache, page_table=page_table, cu_tokens=cu_tokens, out=out)
     st = _native.lib().bfp8_latent_cache_read(rows, ps, sc, ss, pages, page, table, ts, width, page_table.shape[0],
                                               cu_tokens.data_ptr(), total, out.data_ptr(), out.stride(0),
@@ -982,9 +1000,10 @@ def latent_attention(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
         raise ValueError(f"without cu_q every sequence has one query token, got {t} tokens and {b} sequences")
     if out is None:
         out = torch.empty((t, heads, LATENT_DIM), dtype=torch.bfloat16, device=q.device)
-    _require(out, "out", torch.bfloat16, 3)
-    if tuple(out.shape) != (t, heads, LATENT_DIM) or out.stride(2) != 1:
-        raise ValueError(f"out must be [{t}, {heads}, {LATENT_DIM}] with contiguous rows")
+    else:
+        _require(out, "out", torch.bfloat16, 3)
+        if out.shape != (t, heads, LATENT_DIM) or out.stride(2) != 1:
+            raise ValueError(f"out must be [{t}, {heads}, {LATENT_DIM}] with contiguous rows")
     _same_device(q, cache=cache, page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, out=out, workspace=workspace)
     lib = _native.lib()
     if workspace is None:
@@ -1015,7 +1034,7 @@ def latent_attention_expanded(q: torch.Tensor, kv: torch.Tensor, rope: torch.Ten
     _require(rope, "rope", q.dtype, 2)
     tq, heads, dim = q.shape
     tk = kv.shape[0]
-    if dim != 192 or tuple(kv.shape[1:]) != (heads, 256) or tuple(rope.shape) != (tk, ROPE_DIM):
+    if dim != 192 or kv.shape != (tk, heads, 256) or rope.shape != (tk, ROPE_DIM):
         raise ValueError(f"expected q [Tq, H, 192], kv [Tk, H, 256] and rope [Tk, 64], got {tuple(q.shape)}, "
                          f"{tuple(kv.shape)} and {tuple(rope.shape)}")
     if q.stride(2) != 1 or kv.stride(2) != 1 or rope.stride(1) != 1:
@@ -1028,9 +1047,10 @@ def latent_attention_expanded(q: torch.Tensor, kv: torch.Tensor, rope: torch.Ten
     _starts_arg(cu_k, "cu_k", b)
     if out is None:
         out = torch.empty((tq, heads, 128), dtype=q.dtype, device=q.device)
-    _require(out, "out", q.dtype, 3)
-    if tuple(out.shape) != (tq, heads, 128) or out.stride(2) != 1:
-        raise ValueError(f"out must be [{tq}, {heads}, 128] with contiguous rows")
+    else:
+        _require(out, "out", q.dtype, 3)
+        if out.shape != (tq, heads, 128) or out.stride(2) != 1:
+            raise ValueError(f"out must be [{tq}, {heads}, 128] with contiguous rows")
     _same_device(q, kv=kv, rope=rope, cu_q=cu_q, cu_k=cu_k, out=out)
     st = _native.lib().bfp8_latent_attention_expanded(
         q.data_ptr(), _IN_DTYPES[q.dtype], tq, heads, q.stride(0), q.stride(1), kv.data_ptr(), tk, kv.stride(0),
