@@ -457,7 +457,7 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     struct Soft {
       v16f x;          // score in log2 + scale code of the key
       v4f inv[4];      // 2^-e of keys 8 q + 4 g .. + 3
-      float ref, sum;  // weights are 2^(x - ref)
+      float ref, sum[2];  // weights are 2^(x - ref); two sums, so that no addition waits for the one before
     };
     auto soft_x = [&](const v16f& s, const v4f* e, Soft& w) {
 #pragma unroll
@@ -465,7 +465,7 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     };
     auto soft_mask = [&](int t, Soft& w) {
       const int k0 = t * kTile + half * 32;
-      if (k0 + 32 > all) {
+      if (__builtin_expect(k0 + 32 > all, 0)) {  // (out of the loop's line: a taken branch costs it dear)
         const int left = limit - k0 - 4 * g;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -480,15 +480,15 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
       top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
       w.ref = top == kNegInf ? kNone : ceilf(top) - kTop;
-      w.sum = 0.f;
+      w.sum[0] = w.sum[1] = 0.f;
     };
-    // Weights of keys 2 k and 2 k + 1; the same into the two terms. Piece 0 .. 15 alternates between them, the
-    // second a piece or two behind.
+    // Weights of keys 2 k and 2 k + 1; the same into the two terms.
     auto soft_weight = [&](Soft& w, float ref, int k) {
 #pragma unroll
-      for (int i = 2 * k; i < 2 * k + 2; ++i) {
+      for (int j = 0; j < 2; ++j) {
+        const int i = 2 * k + j;
         w.x[i] = __builtin_amdgcn_exp2f(w.x[i] - ref);
-        w.sum = fmaf(w.x[i], w.inv[i >> 2][i & 3], w.sum);  // (a masked key's weight is 0, whatever its scale)
+        w.sum[j] = fmaf(w.x[i], w.inv[i >> 2][i & 3], w.sum[j]);  // (a masked key's weight is 0, whatever its scale)
       }
     };
     auto soft_terms = [&](const Soft& w, int k, v4i& hi, v4i& lo) {
@@ -506,18 +506,14 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
         lo[q4] = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(p0, 16.f, -back[0]), fmaf(p1, 16.f, -back[1]), 0, false);
       }
     };
+    // Piece 0 .. 9: the weights of pair `piece` and the terms of the pair two before, so that results are not
+    // waited for.
     auto soft_piece = [&](Soft& w, float ref, int piece, v4i& hi, v4i& lo) {
-      if (piece == 0 || (piece & 1)) {
-        const int k = (piece + 1) >> 1;  // 0, 1, 2, .. at pieces 0, 1, 3, 5, .., 13; piece 15 is the last terms
-        if (k < 8) {
-          soft_weight(w, ref, k);
-          asm volatile("" : "+v"(w.x[2 * k]), "+v"(w.x[2 * k + 1]), "+v"(w.sum));  // here, not after the products
-          return;
-        }
-      }
-      const int k = piece == 15 ? 7 : (piece >> 1) - 1;
-      soft_terms(w, k, hi, lo);
-      asm volatile("" : "+v"(hi[k >> 1]), "+v"(lo[k >> 1]));
+      if (piece < 8) soft_weight(w, ref, piece);
+      if (piece >= 2) soft_terms(w, piece - 2, hi, lo);
+      // (here, not after the products)
+      if (piece < 8) asm volatile("" : "+v"(w.x[2 * piece]), "+v"(w.x[2 * piece + 1]), "+v"(w.sum[0]), "+v"(w.sum[1]));
+      if (piece >= 2) asm volatile("" : "+v"(hi[(piece - 2) >> 1]), "+v"(lo[(piece - 2) >> 1]));
     };
     // ---- the weights of a tile, as both waves of the pair wrote them: slots 0 .. 31 of a product are the first
     // wave's keys, 32 .. 63 the second's, each under its own scale code (lanes g = 0 and 1 hold the two)
@@ -548,7 +544,7 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       return f;
     };
     auto rescale = [&](float f) {
-      if (__any(f != 1.f)) {
+      if (__builtin_expect(__any(f != 1.f), 0)) {
         asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");  // products in flight
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
@@ -694,10 +690,7 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
         if (d == 0) soft_x(s, e, w);
         if (d == 1) soft_mask(t, w);
         if (d == 2) soft_top(w), ref = w.ref == kNone ? 0.f : w.ref;
-        if (d >= 3) {
-#pragma unroll
-          for (int piece = (d - 3) * 16 / 11; piece < (d - 2) * 16 / 11; ++piece) soft_piece(w, ref, piece, hi, lo);
-        }
+        if (d >= 3 && d < 13) soft_piece(w, ref, d - 3, hi, lo);
       });
       const uint32_t at = weights + half * kWeightBytes + turn * 2048;
       *reinterpret_cast<lds_w4i*>(at) = hi;
@@ -705,7 +698,7 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       *reinterpret_cast<lds_f*>(refs + half * kRefBytes + turn * 128) = w.ref;  // (lanes r and r + 32 write the same)
       prepare(code, ahead.unit);
       ref_before = w.ref;
-      sum_before = w.sum;
+      sum_before = w.sum[0] + w.sum[1];
       turn ^= 1;
       tile_before = tile;
       tile = next_tile;
