@@ -45,14 +45,13 @@ namespace bfp8 {
 namespace {
 
 constexpr int kTile = 64;                  // keys of a tile
-// A tile in LDS. Codes: pairs of rows, 1024 + 32 bytes apart, the 16-byte columns of the odd row XORed with
-// 5: no bank conflicts for the score reads (16 lanes: one column of 16 consecutive keys) and the transposing
-// value reads (32 lanes: two columns of 8 keys that differ in bits 0, 1 and 3), while the column of a later
-// step lies a constant further on (the XOR's bit 2 swaps neighbouring steps, which takes two addresses).
-// Rotary keys: groups of 8 rows of 128 bytes, 1024 + 64 bytes apart, columns XORed with (row / 2) % 4.
-constexpr int kPairStride = 1024 + 32, kRopeStride = 1024 + 64;
-constexpr int kRopeAt = kTile / 2 * kPairStride;
-constexpr int kTileBytes = kRopeAt + kTile / 8 * kRopeStride;
+// A tile in LDS: groups of 8 rows, each in 5 blocks of 128 bytes of every row (4 of codes, 1 of the rotary key) and
+// 64 bytes of padding; of each 64 bytes the 16-byte columns are XORed with bits 2 and 1 of the row. No bank conflicts
+// for the score reads (16 lanes: one column of 16 rows) and the transposing value reads (32 lanes: two columns of 8
+// rows that differ in bits 0, 1 and 3). A copy brings one block, whole lines of 8 rows, so that a lane keeps to one
+// row of a group, and a column of a later step lies a constant further on.
+constexpr int kBlockBytes = 8 * 128, kGroupBytes = 5 * kBlockBytes + 64;
+constexpr int kTileBytes = 8 * kGroupBytes;
 constexpr int kBuffers = 3;                // tile t - 1 (values), t, and t + 1 on its way
 constexpr int kWeightBytes = 2 * 2048;     // a wave's weights of 32 keys (two terms), for two tiles in turn
 constexpr int kRefBytes = 2 * 128;         // their exponents
@@ -86,6 +85,20 @@ __device__ __forceinline__ void mfma_scaled_acc(const v8i& a, const v8i& b, v16f
     asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %3 op_sel:[0,1,0] op_sel_hi:[0,0,0]"
                  : "+a"(c)
                  : "v"(a), "v"(b), "v"(codes));
+}
+// f(Const<0>) .. f(Const<kCount - 1>).
+template <int kCount, typename F>
+__device__ __forceinline__ void static_for(F f) {
+  if constexpr (kCount > 0) {
+    static_for<kCount - 1>(f);
+    f(Const<kCount - 1>{});
+  }
+}
+// copy16_m0 of the bytes kOffset further on. The instruction's offset counts for both addresses: `lds` lies that
+// much before the destination.
+template <int kOffset>
+__device__ __forceinline__ void copy16_block(const uint8_t* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off offset:%2" : : "v"(src), "s"(lds), "n"(kOffset) : "memory");
 }
 // Keeps an accumulator in the accumulation registers at this point.
 __device__ __forceinline__ void keep_acc(v16f& c) { asm volatile("" : "+a"(c)); }
@@ -398,19 +411,24 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       return Row{(uint32_t)p * page_units + (uint32_t)o * (kLatentRow / 128),
                  a.cache.scales[(int64_t)p * a.cache.scale_stride + o], none ? 255 : 0};
     };
-    // ---- copies of a tile. Two rows of codes a copy, lanes 32 .. 63 the second; eight rows of rotary keys.
-    constexpr int kCodeCopies = 32 / kWaves, kCopies = 40 / kWaves;
-    const uint8_t* code_src = a.cache.rows + (((lane & 31) ^ ((lane >> 5) * 5)) << 4);
-    const uint8_t* rope_src = a.cache.rows + kLatentDim + (((lane & 7) ^ ((lane >> 4) & 3)) << 4);
-    const int code_from = (wave * (2 * kCodeCopies) + (lane >> 5)) << 2, rope_from = (wave * (64 / kWaves) + (lane >> 3)) << 2;
-    auto place_of = [&](uint32_t unit, int j) {  // the row's place, from the lane that looked it up
-      return (uint32_t)__builtin_amdgcn_ds_bpermute(
-          j < kCodeCopies ? code_from + 8 * j : rope_from + 32 * (j - kCodeCopies), (int)unit);
+    // ---- copies of a tile: a wave's groups of 8 rows, lanes 8 r .. 8 r + 7 at row r, five blocks of 128 bytes each
+    constexpr int kGroups = 8 / kWaves, kCopies = 5 * kGroups;
+    auto swizzle = [](int row) { return ((row >> 2) & 1) | (row & 2); };
+    const uint8_t* lane_src = a.cache.rows + (((lane & 7) ^ swizzle(lane >> 3)) << 4);
+    const int row_from = (wave * kGroups * 8 + (lane >> 3)) << 2;
+    auto place_of = [&](uint32_t unit, int group) {  // the row's place, from the lane that looked it up
+      const uint32_t u = (uint32_t)__builtin_amdgcn_ds_bpermute(row_from + 32 * group, (int)unit);
+      return lane_src + (uint64_t)u * 128;
     };
-    auto copy_piece = [&](uint32_t u, uint32_t at, int j) {
-      const int jr = j - kCodeCopies;
-      if (j < kCodeCopies) copy16_m0(code_src + (uint64_t)u * 128, at + (wave * kCodeCopies + j) * kPairStride);
-      else copy16_m0(rope_src + (uint64_t)u * 128, at + kRopeAt + (wave * (8 / kWaves) + jr) * kRopeStride);
+    auto copy_piece = [&](const uint8_t* const* places, uint32_t tile, auto piece) {
+      constexpr int j = decltype(piece)::v, group = j / 5, block = j % 5;
+      copy16_block<128 * block>(places[group], tile + (wave * kGroups + group) * kGroupBytes + (kBlockBytes - 128) * block);
+    };
+    auto copy_pieces = [&](const uint8_t* const* places, uint32_t tile, auto first, auto count) {
+      static_for<decltype(count)::v>([&](auto i) {
+        constexpr int j = decltype(first)::v + decltype(i)::v;
+        if constexpr (j < kCopies) copy_piece(places, tile, Const<j>{});
+      });
     };
 
     Entry here, next, far;
@@ -420,8 +438,10 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     int code;      // of tile t
     {
       const Row x = row_of(here);
+      const uint8_t* from[kGroups];
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) copy_piece(place_of(x.unit, j), lds, j);
+      for (int j = 0; j < kGroups; ++j) from[j] = place_of(x.unit, j);
+      copy_pieces(from, lds, Const<0>{}, Const<kCopies>{});
       code = x.byte | x.none;
     }
     Row ahead = row_of(next);  // of tile t + 1
@@ -441,14 +461,12 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     typedef __attribute__((address_space(3))) const v4f lds_v4f;
     typedef __attribute__((address_space(3))) float lds_f;
     typedef __attribute__((address_space(3))) v2i lds_v2i;
-    const int kk = half * 32 + r, odd = r & 1;
-    const uint32_t key_base = (kk >> 1) * kPairStride + odd * 512 + ((g ^ odd) << 4);
-    const uint32_t key_even = key_base + 64 * odd, key_odd = key_base - 64 * odd;  // steps 0, 2, .. and 1, 3, ..
-    const uint32_t rope_base = kRopeAt + (kk >> 3) * kRopeStride + (kk & 7) * 128;
-    const uint32_t rope_even = rope_base + ((g ^ ((kk >> 1) & 3)) << 4), rope_odd = rope_base + (((2 + g) ^ ((kk >> 1) & 3)) << 4);
-    const int vk = 8 * ((lane >> 3) & 1) + 4 * g + ((lane >> 1) & 3);  // the row this lane addresses (and 16, 32, 48 on)
-    const uint32_t value_base = (vk >> 1) * kPairStride + (vk & 1) * 512 + ((((lane >> 4) & 1) ^ (vk & 1)) << 4) + 8 * (lane & 1) + 256 * half;
-    const uint32_t value_low = value_base + 64 * (vk & 1), value_high = value_base - 64 * (vk & 1);  // d & 2 clear and set
+    const uint32_t key_base = (half * 4 + (r >> 3)) * kGroupBytes + (r & 7) * 128;
+    const uint32_t key_first = key_base + ((g ^ swizzle(r)) << 4), key_second = key_base + (((2 + g) ^ swizzle(r)) << 4);
+    const int vk = 4 * g + ((lane >> 1) & 3);  // the row this lane addresses, of every other group
+    const uint32_t value_base = ((lane >> 3) & 1) * kGroupBytes + vk * 128 + 8 * (lane & 1) + 2 * half * kBlockBytes;
+    const int value_column = ((lane >> 4) & 1) ^ swizzle(vk);
+    const uint32_t value_even = value_base + (value_column << 4), value_odd = value_base + ((2 ^ value_column) << 4);  // d
     const uint32_t weights = lds + kWeightsAt + pair * (2 * kWeightBytes) + lane * 16;  // half, tile in turn, term
     const uint32_t refs = lds + kRefsAt + pair * (2 * kRefBytes) + r * 4;
     const uint32_t floats = lds + kKeysAt + wave * kKeyBytes;
@@ -558,10 +576,10 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     // columns are read by the caller, and the last ones are left to finish(): after the next barrier, while
     // the first keys are read.
     auto value_at = [&](uint32_t tile, int d) {
-      const uint32_t at = tile + ((d & 2) ? value_high : value_low) + 32 * d;
+      const uint32_t at = tile + ((d & 1) ? value_odd : value_even) + (d >> 2) * kBlockBytes + (d & 2) * 32;
       v2i x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at + i * 8 * kPairStride));
+      for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i*>(at + i * 2 * kGroupBytes));
       return v8i{x[0][0], x[0][1], x[1][0], x[1][1], x[2][0], x[2][1], x[3][0], x[3][1]};
     };
     Weights late{};  // (nothing is late at the first tile: its products are with zeros)
@@ -591,12 +609,12 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
     // ---- scores of this wave's 32 keys of a tile; `between(step)` is called at each of 8 steps
     auto scores = [&](uint32_t tile, int kc, auto between) {
       auto key_at = [&](int ks) {
-        const uint32_t at = tile + ((ks & 1) ? key_odd : key_even) + 64 * ks;
-        const v4i x = *reinterpret_cast<lds_v4i*>(at), y = *reinterpret_cast<lds_v4i*>(at + 32);
+        const v4i x = *reinterpret_cast<lds_v4i*>(tile + key_first + (ks >> 1) * kBlockBytes + (ks & 1) * 64);
+        const v4i y = *reinterpret_cast<lds_v4i*>(tile + key_second + (ks >> 1) * kBlockBytes + (ks & 1) * 64);
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
       };
       auto rope_at = [&](int ks) {
-        return __builtin_bit_cast(v8bf, *reinterpret_cast<lds_v4i*>(tile + ((ks & 1) ? rope_odd : rope_even) + 64 * (ks >> 1)));
+        return __builtin_bit_cast(v8bf, *reinterpret_cast<lds_v4i*>(tile + ((ks & 1) ? key_second : key_first) + 4 * kBlockBytes + (ks >> 1) * 64));
       };
       v8i k[3];
       v8bf kr[4];
@@ -606,27 +624,27 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       v16f s;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        if (ks + 2 < 8) k[(ks + 2) % 3] = key_at(ks + 2);
+      static_for<8>([&](auto step) {
+        constexpr int ks = decltype(step)::v;
+        if constexpr (ks + 2 < 8) k[(ks + 2) % 3] = key_at(ks + 2);
         else kr[2 * ks - 12] = rope_at(2 * ks - 12), kr[2 * ks - 11] = rope_at(2 * ks - 11);
         s = mfma_scaled<0>(k[ks % 3], q.hi[ks], s, kc, q.code);
         s = mfma_scaled<1>(k[ks % 3], q.lo[ks], s, kc, q.code);
         asm volatile("" : "+v"(s));  // the products stay here
-        between(ks);
+        between(step);
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[ks], q.rope[ks], s, 0, 0, 0);
       return s;
     };
-    constexpr int kSteps = kPairs == 1 ? 7 : 5, kEach = (kCopies + kSteps - 1) / kSteps;
-    uint32_t places[kCopies];  // where the rows of the next copies lie
+    constexpr int kSteps = 5, kEach = kCopies / kSteps;
+    const uint8_t* places[kGroups];  // where the rows of the next copies lie
     int kc;                    // scale code of this lane's key of the tile at hand
     auto prepare = [&](int tile_code, uint32_t unit) {
       kc = __builtin_amdgcn_ds_bpermute((half * 32 + r) << 2, tile_code);
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) places[j] = place_of(unit, j);
+      for (int j = 0; j < kGroups; ++j) places[j] = place_of(unit, j);
       *reinterpret_cast<lds_f*>(floats + lane * 4) = (float)tile_code;
       *reinterpret_cast<lds_f*>(floats + 256 + lane * 4) = __builtin_amdgcn_ldexpf(1.f, 127 - tile_code);
     };
@@ -650,27 +668,20 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       lds_barrier();
       const int next_place = place + 1 == kBuffers ? 0 : place + 1;
       const uint32_t next_tile = lds + next_place * kTileBytes;
-      const uint32_t unit = ahead.unit;
       code = ahead.byte | ahead.none;
       // (after the last tile the copies bring one that is not used: there always is a key to look up)
       Weights before;
       v8i v0;
       float f = 1.f;
-      const v16f s = scores(tile, kc, [&](int ks) {
-        if (ks < kSteps) {
-#pragma unroll
-          for (int j = 0; j < kEach; ++j) {
-            if (ks * kEach + j < kCopies) copy_piece(places[ks * kEach + j], next_tile, ks * kEach + j);
-            const int far = ks * kEach + j + kEach;
-            if (far < kCopies) places[far] = place_of(unit, far);
-          }
-        }
-        if (ks == kSteps) {
+      const v16f s = scores(tile, kc, [&](auto ks) {
+        constexpr int step = decltype(ks)::v;
+        if constexpr (step < kSteps) copy_pieces(places, next_tile, Const<step * kEach>{}, Const<kEach>{});
+        if (step == kSteps) {
           ahead = row_of(far);
           look_up(far);
         }
-        if (ks == 5) read_weights(turn ^ 1, before);
-        if (ks == 7) {
+        if (step == 5) read_weights(turn ^ 1, before);
+        if (step == 7) {
           f = refer(before, ref_before, sum_before);
           asm volatile("" : "+v"(f), "+v"(before.codes));
           v0 = value_at(tile_before, 0);
