@@ -51,6 +51,7 @@ struct LatentAttnArgs {
 struct LatentAttnPlan {
   int64_t blocks, parts, slots, cuts;
   int pairs, target_parts, min_tiles, max_tiles;
+  bool split_join;  // eight waves join a row
   size_t counts_bytes, stats_bytes, states_bytes;
 };
 // max_keys: no sequence's page table reaches further.

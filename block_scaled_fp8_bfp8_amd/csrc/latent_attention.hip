@@ -775,16 +775,19 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
 
 constexpr int kMaxParts = 256;  // of a block: no more parts run at once
 
-// Joins the parts of a cut block, in order: one wave a row. The lanes hold the parts' references and sums,
-// then take 8 columns each. Bound by latency (a chain of three loads) where there are few rows, and by HBM and
-// the L2s where every workgroup left a state.
-template <int kBM>
-__global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
+// Joins the parts of a cut block, in a fixed order: one wave a row or, where blocks are cut into many parts, eight, which take every 64 parts 8 a wave and add their sums through LDS. The lanes hold the parts'
+// references and sums, then take 8 columns each. Bound by latency (a chain of three loads) where there are few
+// rows, and by HBM and the L2s where every workgroup left a state.
+template <int kBM, int kSplit>
+__global__ __launch_bounds__(kSplit == 1 ? 256 : kSplit * 64) void latent_join_kernel(LatentAttnArgs a) {
   const int cuts = a.counts[0];
   const Desc desc = reinterpret_cast<const Desc*>(a.counts + 4)[blockIdx.x];
   if ((int)blockIdx.x >= cuts) return;
   const int lane = threadIdx.x & 63;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = kSplit == 1 ? blockIdx.y * 4 + wave : blockIdx.y;
+  constexpr int kSpan = 64 / kSplit;  // of every 64 parts, this wave's
+  const int first = kSplit == 1 ? 0 : wave * kSpan;
   if (row >= desc.rows || desc.parts > kMaxParts || desc.slot + desc.parts > a.max_slots) return;
   // the first parts' states are on their way while the statistics are joined
   constexpr int kTogether = 8;
@@ -797,7 +800,7 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
       x[k] = at[0], y[k] = at[1];
     }
   };
-  read_states(0, desc.parts - 1);
+  read_states(first, desc.parts - 1);
   constexpr int kEach = kMaxParts / 64;
   float f[kEach], sums[kEach];
   float m = kNegInf;
@@ -826,9 +829,9 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
   float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int n = min(desc.parts - 64 * i, 64);
-    for (int p0 = 0; p0 < n; p0 += kTogether) {
-      if (i + p0 > 0) read_states(64 * i + p0, desc.parts - 1);
+    const int n = min(desc.parts - 64 * i, first + kSpan);
+    for (int p0 = first; p0 < n; p0 += kTogether) {
+      if (i > 0 || p0 > first) read_states(64 * i + p0, desc.parts - 1);
 #pragma unroll
       for (int k = 0; k < kTogether; ++k) {
         // (past the last part: its state again, times zero)
@@ -839,6 +842,17 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
       }
     }
   }
+  if constexpr (kSplit > 1) {
+    __shared__ float sums_of[kSplit][kLatentDim];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums_of[wave][j * 64 + lane] = o[j];
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 1; w < kSplit; ++w)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += sums_of[w][j * 64 + lane];
+  }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   const int flat = desc.first + row, tok = flat / a.H, head = flat - tok * a.H;
   uint16_t* dst = a.out + (int64_t)tok * a.o_tok + (int64_t)head * a.o_head + lane * 8;
@@ -848,10 +862,26 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnArgs a) {
 
 constexpr int kCUs = 256;
 static_assert(kCUs <= kMaxParts, "a block's parts fit the join's lanes");
-constexpr int kMinTiles = 2;  // fewer tiles a part cost more in states than they save
+// Where no sequence has more tiles, no block is cut and there is no second launch (1 sequence x 128 heads, 200 keys:
+// 17.6 us in two parts, 15.5 whole).
+constexpr int kWhole = 4;
 
-// Pairs of waves a workgroup: one where a sequence has 32 query rows or fewer on average, otherwise two.
-int pairs_for(int64_t T, int64_t B, int64_t H) { return T * H <= 32 * B ? 1 : 2; }
+// Pairs of waves a workgroup: one where a sequence has 32 query rows or fewer on average (64 sequences x 32 heads:
+// 53 us, 59 with two pairs; x 48 heads: 102 and 65), or where blocks of 32 rows leave at most 8 tiles for each
+// compute unit, so that half as large states weigh more than the idle SIMDs (128 heads: 8 sequences of 4000 keys 34.5
+// us, 37.1 with two pairs; 16 of 2000 34.9 and 35.7; 16 of 4000 48.2 and 43.5).
+int pairs_for(int64_t T, int64_t B, int64_t H, int64_t max_tiles) {
+  const int64_t rows = T * H, most = 32 * 8 * kCUs;
+  return rows <= 32 * B || (rows <= most && rows * max_tiles <= most) ? 1 : 2;
+}
+
+// Tiles a part at least: 2, or 3 of long sequences, where more states cost more than they save (1 sequence x 128
+// heads, at least 2 or 3: 1000 keys 19.7 and 19.9 us, 4000 26.7 and 23.6).
+int min_tiles_for(int64_t max_tiles) { return max_tiles > 32 ? 3 : 2; }
+
+// Eight waves a row join more parts than this (1 sequence x 128 heads, one wave and eight: 32 parts 26.6 and 27.3 us,
+// 63 parts 45.6 and 32.9).
+constexpr int kManyParts = 32;
 
 template <int kPairs>
 hipError_t launch(const LatentAttnArgs& args, const LatentAttnPlan& plan, hipStream_t stream) {
@@ -859,7 +889,10 @@ hipError_t launch(const LatentAttnArgs& args, const LatentAttnPlan& plan, hipStr
   hipLaunchKernelGGL((latent_attn_kernel<kPairs>), dim3((unsigned)grid), dim3(kPairs * 128), 0, stream, args);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.slots == 0) return e;
-  hipLaunchKernelGGL((latent_join_kernel<kPairs * 32>), dim3((unsigned)plan.cuts, kPairs * 8), dim3(256), 0, stream, args);
+  if (plan.split_join)
+    hipLaunchKernelGGL((latent_join_kernel<kPairs * 32, 8>), dim3((unsigned)plan.cuts, kPairs * 32), dim3(512), 0, stream, args);
+  else
+    hipLaunchKernelGGL((latent_join_kernel<kPairs * 32, 1>), dim3((unsigned)plan.cuts, kPairs * 8), dim3(256), 0, stream, args);
   return hipGetLastError();
 }
 
@@ -867,22 +900,25 @@ hipError_t launch(const LatentAttnArgs& args, const LatentAttnPlan& plan, hipStr
 
 LatentAttnPlan plan_latent_attn(int64_t T, int64_t B, int64_t H, int64_t max_keys) {
   LatentAttnPlan p;
-  p.pairs = pairs_for(T, B, H);
+  const int64_t max_tiles = (max_keys + kTile - 1) / kTile;
+  p.pairs = pairs_for(T, B, H, max_tiles);
   const int64_t bm = 32 * p.pairs;
   // Blocks: a sequence's last may be partly filled.
   p.blocks = T * H / bm + (T < B ? T : B);
-  const int64_t max_tiles = (max_keys + kTile - 1) / kTile;
   p.max_tiles = (int)max_tiles;
   p.target_parts = kCUs;
-  p.min_tiles = kMinTiles;
+  p.min_tiles = min_tiles_for(max_tiles);
   // Blocks are cut only into as many parts as run at once in all.
-  const int64_t per_block = (max_tiles + kMinTiles - 1) / kMinTiles;
-  if (per_block <= 1) {
+  const int64_t per_block = (max_tiles + p.min_tiles - 1) / p.min_tiles;
+  p.split_join = false;
+  if (max_tiles <= kWhole) {
     p.slots = p.cuts = 0;
   } else {
     p.slots = p.target_parts;
     if (p.blocks * per_block < p.slots) p.slots = p.blocks * per_block;
     p.cuts = p.slots / 2;
+    // (the fewest blocks that hold the rows are cut into the most parts)
+    p.split_join = per_block > kManyParts && p.slots / ((T * H + bm - 1) / bm) > kManyParts;
   }
   p.parts = p.blocks > p.slots ? p.blocks : p.slots;
   p.counts_bytes = p.slots ? ((16 + p.cuts * sizeof(Desc) + 255) / 256) * 256 : 0;
