@@ -10,7 +10,7 @@
 // group makes its scale and codes NaN (maximum() below propagates it).
 //
 // HBM-bound: x and the residual are read once, h, q and s written once (7 bytes an element in
-// bf16). A row lives in the registers of the threads that share it, 8 elements a chunk, so the
+// bf16; 8192 rows of 7168: 5.2 TB/s in a row of calls; 4096: 6.0). A row lives in the registers of the threads that share it, 8 elements a chunk, so the
 // 16 lanes of a 128-wide group exchange its amax by lane shuffles.
 #include "device_latent.h"
 #include "launch.h"
@@ -203,13 +203,19 @@ void run(const RmsNormArgs& a, hipStream_t stream) {
                      a.ld_h, a.q, a.ldq, a.as, a.ld_as, a.M, a.H);
 }
 
+// By the row's length alone, so that a row's result does not depend on how many there are. A wave for every 512
+// elements answers a single row soonest, and long batches are slower where 16 waves wait for each other (bf16 with a
+// residual, us of GPU time for 1 and for 8192 rows): 2048 elements, one wave 5.1 and 22.2, two 3.6 and 21.3, four
+// 3.1 and 21.9; 4096, one 8.3 and 42.0, four 3.8 and 38.5, eight 3.3 and 39.3, sixteen 3.3 and 50.2; 7168, four 5.2
+// and 83, eight 4.0 and 79, sixteen 3.7 and 86.5; 12288, eight 4.8 and 131, sixteen 4.2 and 135.
 template <int kIn, bool kE8>
 void choose(const RmsNormArgs& a, hipStream_t stream) {
   const int pieces = (a.H + 511) / 512;  // 64 lanes of 8 elements
   if (pieces <= 1) run<kIn, kE8, 1, 1>(a, stream);
-  else if (pieces <= 2) run<kIn, kE8, 1, 2>(a, stream);
-  else if (pieces <= 4) run<kIn, kE8, 1, 4>(a, stream);
-  else if (pieces <= 16) run<kIn, kE8, 16, 1>(a, stream);
+  else if (pieces <= 2) run<kIn, kE8, 2, 1>(a, stream);
+  else if (pieces <= 4) run<kIn, kE8, 4, 1>(a, stream);
+  else if (pieces <= 8) run<kIn, kE8, 8, 1>(a, stream);
+  else if (pieces <= 16) run<kIn, kE8, 8, 2>(a, stream);
   else if (pieces <= 32) run<kIn, kE8, 16, 2>(a, stream);
   else if (pieces <= 64) run<kIn, kE8, 16, 4>(a, stream);
   else run<kIn, kE8, 16, 8>(a, stream);
