@@ -72,6 +72,7 @@ struct LatentExpandedArgs {
   const int32_t* cu_k;  // [B + 1]
   int Tq, Tk, B, H;
   float scale;
+  bool longest_first;  // set by the launch
 };
 // The most blocks of query rows that B sequences of Tq rows in all can have, a head.
 int64_t latent_expanded_blocks(int64_t Tq, int64_t B);

@@ -58,14 +58,40 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 
 __device__ __forceinline__ int clip(int v, int top) { return min(max(v, 0), top); }
 
-// The workgroup's block of kBM query rows, of all sequences' blocks one after the other (of a sequence the last,
-// which has most keys, first). False: there is none. Every wave looks for itself.
+// The workgroup's block of kBM query rows: the sequences' blocks one after the other, of each the last, which has
+// most keys, first; or all blocks with most keys first (counted in blocks; of equal ones the first sequence's), so
+// that the last to start are short. False: there is none. Every wave looks for itself.
 template <int kBM>
 __device__ __forceinline__ bool find_block(const LatentExpandedArgs& a, int index, int& seq, int& block) {
   const int lane = threadIdx.x & 63;
   const int per = (a.B + 63) / 64;
   const int b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
   auto blocks = [&](int b) { return (max(clip(a.cu_q[b + 1], a.Tq) - clip(a.cu_q[b], a.Tq), 0) + kBM - 1) / kBM; };
+  if (a.longest_first) {
+    // lane b: sequence b, whose blocks are at the levels top, top - 1, .. top - n + 1 (all at least 1)
+    int n = 0, top = 0;
+    if (lane < a.B) {
+      const int nq = clip(a.cu_q[lane + 1], a.Tq) - clip(a.cu_q[lane], a.Tq);
+      const int nk = max(clip(a.cu_k[lane + 1], a.Tk) - clip(a.cu_k[lane], a.Tk), 0);
+      n = blocks(lane);
+      top = n + max(nk - nq, 0) / kBM;
+    }
+    auto total = [](int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); };
+    auto down_to = [&](int level) { return total(min(max(top - level + 1, 0), n)); };  // blocks at it and above
+    if (index >= total(n)) return false;
+    int lo = 1, hi = (int)wave_max((float)top) + 4;  // the highest level down to which there are more than `index`
+    while (lo < hi) {
+      const int mid = lo + ((hi - lo + 1) >> 1);
+      if (down_to(mid) > index) lo = mid;
+      else hi = mid - 1;
+    }
+    const int above = down_to(lo + 1);
+    const uint64_t at = __ballot(lo <= top && lo > top - n);
+    const bool me = (at >> lane & 1) && __popcll(at & ((1ull << lane) - 1)) == index - above;
+    seq = __builtin_ctzll(__ballot(me));
+    block = __builtin_amdgcn_readlane(n - 1 - (top - lo), seq);
+    return true;
+  }
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += blocks(b);
   int first = wave_scan(mine) - mine;
@@ -321,10 +347,18 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
   }
 }
 
+// The longest blocks first where a compute unit gets no more than about six (4 prompts of 2048 x 16 heads: 132 us in
+// the given order, 105 so; 32 of 50 to 1000 x 16, 1552 workgroups: 145 and 130). Beyond, the tail is short, and
+// blocks of one sequence that run together share its keys in the L2s (4 of 2100 to 4090 x 32, 1664 workgroups: 602
+// and 619; 16 of 100 to 4000 x 32: 1145 and 1262). Where all have a compute unit of their own the search is 0.4 us for
+// nothing (5 of 17 to 300 x 8: 11.9 and 12.3). A wave looks among 64 sequences.
+constexpr int64_t kLongestFirst = 1600;
+
 template <bool kF16, int kWaves>
-void launch(const LatentExpandedArgs& args, hipStream_t stream) {
-  const dim3 grid((unsigned)((args.Tq / (kWaves * 32) + (args.Tq < args.B ? args.Tq : args.B)) * (int64_t)args.H));
-  hipLaunchKernelGGL((latent_expanded_kernel<kF16, kWaves>), grid, dim3(kWaves * 64), 0, stream, args);
+void launch(LatentExpandedArgs args, hipStream_t stream) {
+  const int64_t grid = (args.Tq / (kWaves * 32) + (args.Tq < args.B ? args.Tq : args.B)) * (int64_t)args.H;
+  args.longest_first = grid > 256 && grid <= kLongestFirst && args.B <= 64;
+  hipLaunchKernelGGL((latent_expanded_kernel<kF16, kWaves>), dim3((unsigned)grid), dim3(kWaves * 64), 0, stream, args);
 }
 
 }  // namespace
@@ -332,8 +366,10 @@ void launch(const LatentExpandedArgs& args, hipStream_t stream) {
 int64_t latent_expanded_blocks(int64_t Tq, int64_t B) { return Tq / 128 + (Tq < B ? Tq : B); }
 
 hipError_t launch_latent_expanded(const LatentExpandedArgs& args, bool f16, hipStream_t stream) {
-  // 256 rows a workgroup where that fills the card and the sequences are long enough on average
-  const bool many = (int64_t)args.Tq * args.H >= 256 * 256 && args.Tq > 128 * (int64_t)args.B;
+  // 256 rows a workgroup where that more than fills the card and the sequences are long enough on average (128 and
+  // 256 rows: 1 prompt of 4096 x 16 heads, 256 workgroups of 256 rows, 117 and 139 us; x 20 heads 157 and 146; 64 of
+  // 180 to 200 x 16 74 and 58)
+  const bool many = (int64_t)args.Tq * args.H > 256 * 256 && args.Tq > 128 * (int64_t)args.B;
   if (f16) many ? launch<true, 8>(args, stream) : launch<true, 4>(args, stream);
   else many ? launch<false, 8>(args, stream) : launch<false, 4>(args, stream);
   return hipGetLastError();
