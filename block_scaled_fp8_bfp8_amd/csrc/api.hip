@@ -1072,7 +1072,7 @@ bfp8_status_t bfp8_latent_attention(const uint16_t* q, int64_t T, int64_t H, int
   args.target_parts = plan.target_parts;
   args.min_tiles = plan.min_tiles;
   args.max_tiles = plan.max_tiles;
-  args.max_slots = (int)plan.slots;
+  args.max_slots = plan.join ? (int)plan.slots : 0;
   args.max_cuts = (int)plan.cuts;
   if (need > 0) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -51,6 +51,7 @@ struct LatentAttnArgs {
 struct LatentAttnPlan {
   int64_t blocks, parts, slots, cuts;
   int pairs, target_parts, min_tiles, max_tiles;
+  bool join;        // blocks may be cut: a second launch joins their parts
   bool split_join;  // eight waves join a row
   size_t counts_bytes, stats_bytes, states_bytes;
 };
