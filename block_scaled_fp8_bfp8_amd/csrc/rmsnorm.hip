@@ -10,7 +10,7 @@
 // group makes its scale and codes NaN (maximum() below propagates it).
 //
 // HBM-bound: x and the residual are read once, h, q and s written once (7 bytes an element in
-// bf16; 8192 rows of 7168: 5.2 TB/s in a row of calls; 4096: 6.0). A row lives in the registers of the threads that share it, 8 elements a chunk, so the
+// bf16; 8192 rows of 7168 with UE8M0 scales: 75 us, 5.5 TB/s). A row lives in the registers of the threads that share it, 8 elements a chunk, so the
 // 16 lanes of a 128-wide group exchange its amax by lane shuffles.
 #include "device_latent.h"
 #include "launch.h"
