@@ -81,20 +81,33 @@ def _as_u8(t: torch.Tensor, name: str) -> torch.Tensor:
 _workspaces: dict = {}
 
 
-def _workspace(device: torch.device, nbytes: int) -> tuple[int, int]:
-    """(pointer, size) of a workspace for the current stream, grown on demand.
+def _capturing(device: torch.device) -> bool:
+    """Whether the device's current stream is being captured into a graph."""
+    if device.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _workspace(device: torch.device, nbytes: int) -> tuple[int, int, torch.Tensor | None]:
+    """(pointer, size, owner) of a workspace for the current stream, grown on demand. The owner is held
+    until the call is launched.
 
     Its contents do not persist between calls (the linear layer's quantized activations are
     written and read within one call), so one buffer per (device, stream) serves every call
-    ordered on that stream."""
+    ordered on that stream. A call that is being captured takes its own from the graph's memory
+    instead: the graph keeps that address, and the kept buffer is replaced when a call needs more."""
     if nbytes == 0:
-        return 0, 0
+        return 0, 0, None
+    if _capturing(device):
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return buf.data_ptr(), nbytes, buf
     key = (device.index, _stream(device))
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
         _workspaces[key] = buf
-    return buf.data_ptr(), buf.numel()
+    return buf.data_ptr(), buf.numel(), buf
 
 
 _IN_DTYPES = {torch.float32: _native.BFP8_IN_F32, torch.bfloat16: _native.BFP8_IN_BF16,
@@ -176,7 +189,8 @@ def gemm(a_q: torch.Tensor, a_s: torch.Tensor, b_q: torch.Tensor, b_s: torch.Ten
     row strides of a_q and b_q must be at least ceil(K/128) * 128 (what quant_act and pad_k give).
 
     workspace: optional caller-owned uint8 buffer on the same device (at least
-    bfp8_gemm_workspace_bytes(M, N, K) bytes); by default one buffer per (device, stream) is kept."""
+    bfp8_gemm_workspace_bytes(M, N, K) bytes); by default one buffer per (device, stream) is kept, and
+    a call that is being captured takes one from its graph's memory."""
     return _gemm(a_q, a_s, b_q, b_s, out, workspace, torch.bfloat16)
 
 
@@ -251,7 +265,7 @@ def _gemm(a_q, a_s, b_q, b_s, out, workspace, out_dtype):
         raise ValueError("out must be contiguous along N")
     lib = _native.lib()
     if workspace is None:
-        ws_ptr, ws_bytes = _workspace(a_q.device, lib.bfp8_gemm_workspace_bytes(m, n, k))
+        ws_ptr, ws_bytes, workspace = _workspace(a_q.device, lib.bfp8_gemm_workspace_bytes(m, n, k))
     else:
         _require(workspace, "workspace", torch.uint8, 1)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
@@ -338,7 +352,8 @@ def linear(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, bias: torch.Te
     and bias having x's dtype.
 
     workspace: optional uint8 buffer of at least bfp8_linear_workspace_bytes(M, N, K) bytes
-    (holds the quantized activations); by default one buffer per (device, stream) is kept."""
+    (holds the quantized activations); by default one buffer per (device, stream) is kept, and
+    a call that is being captured takes one from its graph's memory."""
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise NotImplementedError(f"linear takes bfloat16 or float16 activations (the output has their dtype), "
                                   f"got {x.dtype}")
@@ -365,7 +380,7 @@ def linear(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, bias: torch.Te
         raise ValueError("out must be contiguous along N")
     lib = _native.lib()
     if workspace is None:
-        ws_ptr, ws_bytes = _workspace(x.device, lib.bfp8_linear_workspace_bytes(m, n, k))
+        ws_ptr, ws_bytes, workspace = _workspace(x.device, lib.bfp8_linear_workspace_bytes(m, n, k))
     else:
         _require(workspace, "workspace", torch.uint8, 1)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
@@ -497,7 +512,7 @@ def gemm_ue8m0(a_q: torch.Tensor, a_e: torch.Tensor, b_q: torch.Tensor, b_e: tor
         raise ValueError("out must be contiguous along N")
     lib = _native.lib()
     if workspace is None:
-        ws_ptr, ws_bytes = _workspace(a_q.device, lib.bfp8_gemm_workspace_bytes(m, n, k))
+        ws_ptr, ws_bytes, workspace = _workspace(a_q.device, lib.bfp8_gemm_workspace_bytes(m, n, k))
     else:
         _require(workspace, "workspace", torch.uint8, 1)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
@@ -711,7 +726,7 @@ def moe_forward(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
     lib = _native.lib()
     need = lib.bfp8_moe_forward_workspace_bytes(t, topk_ids.shape[1], e, h, i)
     if workspace is None:
-        ws_ptr, ws_bytes = _workspace(hidden.device, need)
+        ws_ptr, ws_bytes, workspace = _workspace(hidden.device, need)
     else:
         _require(workspace, "workspace", torch.uint8, 1)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
@@ -983,7 +998,8 @@ def latent_attention(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
     cu_q[b] .. cu_q[b + 1) of q (int32 [B + 1]), or row b alone without cu_q. Each sees its
     sequence up to itself. Lengths are read on the GPU: nothing here waits for them.
     workspace: optional caller-owned uint8 buffer (latent_attention_workspace_bytes); by default
-    one buffer per (device, stream) is kept."""
+    one buffer per (device, stream) is kept, and a call that is being captured takes one from its
+    graph's memory."""
     _require(q, "q", torch.bfloat16, 3)
     t, heads, dim = q.shape
     if dim != LATENT_DIM + ROPE_DIM or q.stride(2) != 1:
@@ -1007,7 +1023,7 @@ def latent_attention(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
     _same_device(q, cache=cache, page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, out=out, workspace=workspace)
     lib = _native.lib()
     if workspace is None:
-        ws_ptr, ws_bytes = _workspace(q.device, lib.bfp8_latent_attention_workspace_bytes(t, b, heads, width * page))
+        ws_ptr, ws_bytes, workspace = _workspace(q.device, lib.bfp8_latent_attention_workspace_bytes(t, b, heads, width * page))
     else:
         _require(workspace, "workspace", torch.uint8, 1)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
