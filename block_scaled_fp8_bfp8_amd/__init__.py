@@ -16,6 +16,7 @@ there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -78,7 +79,7 @@ def _as_u8(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-_workspaces: dict = {}
+_workspaces = threading.local()  # .kept: {(device index, stream): buffer}
 
 
 def _capturing(device: torch.device) -> bool:
@@ -94,19 +95,22 @@ def _workspace(device: torch.device, nbytes: int) -> tuple[int, int, torch.Tenso
     until the call is launched.
 
     Its contents do not persist between calls (the linear layer's quantized activations are
-    written and read within one call), so one buffer per (device, stream) serves every call
-    ordered on that stream. A call that is being captured takes its own from the graph's memory
-    instead: the graph keeps that address, and the kept buffer is replaced when a call needs more."""
+    written and read within one call), so one buffer per (device, stream) serves every call that
+    a host thread makes on that stream. Another thread's launches may come between those of one
+    call, so each thread has its own (freed with it, in the stream's order). A call that is being
+    captured takes its own from the graph's memory instead: the graph keeps that address, and the
+    kept buffer is replaced when a call needs more."""
     if nbytes == 0:
         return 0, 0, None
     if _capturing(device):
         buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         return buf.data_ptr(), nbytes, buf
     key = (device.index, _stream(device))
-    buf = _workspaces.get(key)
+    kept = _workspaces.__dict__.setdefault("kept", {})
+    buf = kept.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _workspaces[key] = buf
+        kept[key] = buf
     return buf.data_ptr(), buf.numel(), buf
 
 
@@ -189,8 +193,8 @@ def gemm(a_q: torch.Tensor, a_s: torch.Tensor, b_q: torch.Tensor, b_s: torch.Ten
     row strides of a_q and b_q must be at least ceil(K/128) * 128 (what quant_act and pad_k give).
 
     workspace: optional caller-owned uint8 buffer on the same device (at least
-    bfp8_gemm_workspace_bytes(M, N, K) bytes); by default one buffer per (device, stream) is kept, and
-    a call that is being captured takes one from its graph's memory."""
+    bfp8_gemm_workspace_bytes(M, N, K) bytes); by default one buffer per (device, stream, host
+    thread) is kept, and a call that is being captured takes one from its graph's memory."""
     return _gemm(a_q, a_s, b_q, b_s, out, workspace, torch.bfloat16)
 
 
@@ -352,8 +356,8 @@ def linear(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, bias: torch.Te
     and bias having x's dtype.
 
     workspace: optional uint8 buffer of at least bfp8_linear_workspace_bytes(M, N, K) bytes
-    (holds the quantized activations); by default one buffer per (device, stream) is kept, and
-    a call that is being captured takes one from its graph's memory."""
+    (holds the quantized activations); by default one buffer per (device, stream, host
+    thread) is kept, and a call that is being captured takes one from its graph's memory."""
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise NotImplementedError(f"linear takes bfloat16 or float16 activations (the output has their dtype), "
                                   f"got {x.dtype}")
@@ -998,8 +1002,8 @@ def latent_attention(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
     cu_q[b] .. cu_q[b + 1) of q (int32 [B + 1]), or row b alone without cu_q. Each sees its
     sequence up to itself. Lengths are read on the GPU: nothing here waits for them.
     workspace: optional caller-owned uint8 buffer (latent_attention_workspace_bytes); by default
-    one buffer per (device, stream) is kept, and a call that is being captured takes one from its
-    graph's memory."""
+    one buffer per (device, stream, host thread) is kept, and a call that is being captured takes
+    one from its graph's memory."""
     _require(q, "q", torch.bfloat16, 3)
     t, heads, dim = q.shape
     if dim != LATENT_DIM + ROPE_DIM or q.stride(2) != 1:

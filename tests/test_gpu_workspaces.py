@@ -1,6 +1,8 @@
 """GPU tests of the binding's default workspaces: captured calls beside eager ones of other sizes. Every result is
 compared bit for bit with an eager call on the same inputs."""
 
+import threading
+
 import pytest
 import torch
 
@@ -102,3 +104,26 @@ def test_two_graphs_of_one_stream_replayed_on_two(gpu):
         torch.cuda.synchronize()
         for (_, out, _), want in zip(cases, wants):
             assert torch.equal(out, want)
+
+
+def test_two_host_threads_on_one_stream(gpu):
+    """Calls of two launches each, made by two threads on the same stream."""
+    side = torch.cuda.Stream(gpu)
+    cases = [decode(gpu, [5000], 64, seed=58), decode(gpu, [4000, 4500], 64, seed=59)]
+    wants = [attend(c) for c, _, _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    announce("two host threads, one stream")
+
+    def work(i):
+        with torch.cuda.stream(side):
+            outs[i].extend(attend(cases[i][0]) for _ in range(100))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for got, want in zip(outs, wants):
+        assert len(got) == 100 and all(torch.equal(o, want) for o in got)

@@ -1,5 +1,7 @@
 """CPU tests of the binding's default workspaces (no kernel is launched): which buffer a call gets."""
 
+import threading
+
 import pytest
 import torch
 
@@ -36,3 +38,15 @@ def test_a_captured_call_does_not_hold_the_kept_buffer(state):
 def test_nothing_is_made_where_nothing_is_needed(state):
     for state["capturing"] in (False, True):
         assert tuple(bfp8._workspace(HOST, 0))[:2] == (0, 0)
+
+
+def test_host_threads_do_not_share_a_buffer(state):
+    """A call of two launches uses its workspace in both; a second host thread's launches on the same stream may come
+    between them."""
+    mine = bfp8._workspace(HOST, 4096)
+    got = []
+    thread = threading.Thread(target=lambda: got.extend(bfp8._workspace(HOST, 4096) for _ in range(2)))
+    thread.start()
+    thread.join()
+    assert got[0][0] == got[1][0] != mine[0]
+    assert bfp8._workspace(HOST, 4096)[0] == mine[0]
