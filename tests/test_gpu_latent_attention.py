@@ -301,3 +301,30 @@ def test_empty_and_refusals(gpu):
         bfp8.latent_attention(q, *rest[:4], float("nan"))
     with pytest.raises(ValueError):
         bfp8.latent_attention(q.cpu(), *rest)
+
+
+@pytest.mark.parametrize("heads", [2, 40])
+@pytest.mark.parametrize("how", ["no page of the cache", "past the table"])
+def test_missing_page_reaches_only_rows_that_see_it(gpu, heads, how):
+    """A chunk whose last tokens alone lie on a missing page: the rows before them are as they were, whatever bytes
+    the cache's first row holds (here the e4m3 codes of NaN)."""
+    lens, new = [200, 30], [9, 2]
+    c, keys = make(gpu, lens, new, heads, 4, seed=89)
+    nan_page = torch.full_like(c["cache"][:1], 0xFF), torch.full_like(c["scales"][:1], 0xFF)
+    c["cache"] = torch.cat([nan_page[0], c["cache"]])
+    c["scales"] = torch.cat([nan_page[1], c["scales"]])
+    c["table"] = torch.where(c["table"] >= 0, c["table"] + 1, c["table"])
+    want = attend(c)
+    check(want, c["q"], keys, lens, new)
+    if how == "past the table":
+        c["table"] = c["table"][:, :49].contiguous()  # token 196 on (tokens 191 .. 199 are new)
+    else:
+        c["table"][0, 49] = c["cache"].shape[0]
+    announce("latent attention missing page", heads, how)
+    out = attend(c)
+    if how == "past the table":  # (a narrower table may be cut in another way)
+        check(out[:5], c["q"][:5], [keys[0][:196]], [196], [5])
+        check(out[9:], c["q"][9:], keys[1:], lens[1:], new[1:])
+    else:
+        assert torch.equal(out[:5], want[:5]) and torch.equal(out[9:], want[9:])
+    assert out[5:9].isnan().all()
