@@ -57,10 +57,11 @@ __device__ __forceinline__ void widen8(const Raw8<kIn>& r, float* f) {
   }
 }
 
-// kWaves waves share a row (kWaves == 1: four rows a workgroup), kChunks chunks of 8 elements a thread.
+// kWaves waves share a row (kWaves == 1: four rows a workgroup), kChunks chunks of 8 elements a thread. h_out may be
+// x or res: a thread reads its chunks of both before it writes them (a wave that redoes the last row stores nothing of it).
 template <int kIn, bool kE8, int kWaves, int kChunks>
 __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void rmsnorm_quant_kernel(
-    const void* __restrict__ x, int64_t ldx, const void* res, int64_t ld_res, const void* __restrict__ w, float eps,
+    const void* x, int64_t ldx, const void* res, int64_t ld_res, const void* __restrict__ w, float eps,
     void* h_out, int64_t ld_h, uint8_t* __restrict__ q, int64_t ldq, void* __restrict__ as, int64_t ld_as, int M,
     int H) {
   constexpr int kRows = kWaves == 1 ? 4 : 1;

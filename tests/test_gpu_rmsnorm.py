@@ -134,3 +134,21 @@ def test_empty_and_refusals(gpu):
             call(x[:, :200], w[:200])
         with pytest.raises(ValueError):
             call(x.t(), w[:4])
+
+
+@pytest.mark.parametrize("e8", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,h", [(7, 256), (5, 512), (33, 1040), (6, 4096), (3, 7168), (5, 16400), (2, 65536)])
+def test_stream_updated_in_place_of_x(gpu, m, h, dtype, e8):
+    """out = x, with one wave, several waves and several chunks a row."""
+    g = torch.Generator().manual_seed(m * 1009 + h)
+    x, res = torch.randn(m, h, generator=g).to(dtype), (2 * torch.randn(m, h, generator=g)).to(dtype)
+    w = (1 + 0.3 * torch.randn(h, generator=g)).to(dtype)
+    announce("rmsnorm out = x", m, h, dtype, e8)
+    call = bfp8.rmsnorm_quant_ue8m0 if e8 else bfp8.rmsnorm_quant
+    xd = x.to(gpu)
+    q, s, out = call(xd, w.to(gpu), residual=res.to(gpu), out=xd)
+    assert out is xd
+    _check(x, w, res, 1e-6, q, s, out, e8)
+    want = call(x.to(gpu), w.to(gpu), residual=res.to(gpu))
+    assert torch.equal(q, want[0]) and torch.equal(s, want[1]) and torch.equal(out, want[2])
