@@ -124,13 +124,13 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void rmsnorm_quant
   }
 
   __shared__ float part[kWaves > 1 ? 2 : 1][kWaves];
-  // the row's sum of (v * f)^2
-  auto row_sum = [&](float f, int turn) {
+  // the row's sum of v^2
+  auto row_sum = [&](int turn) {
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(v[c][i] * f, v[c][i] * f, sum);
+      for (int i = 0; i < 8; ++i) sum = fmaf(v[c][i], v[c][i], sum);
 #pragma unroll
     for (int mask = 1; mask < 64; mask <<= 1) sum += __shfl_xor(sum, mask);
     if constexpr (kWaves > 1) {
@@ -142,13 +142,20 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void rmsnorm_quant
     }
     return sum;
   };
-  const float sum = row_sum(1.0f, 0);
-  float rstd = 1.0f / sqrtf(sum / (float)H + eps);
-  if (!(sum < __builtin_inff())) {  // (the same in every thread of the row)
-    // The squares pass float32 where |v| reaches 2^60 or so: summed again 2^-64 smaller. An
-    // infinite or NaN element still ends in an infinite or NaN sum.
-    rstd = 0x1p-64f / sqrtf(row_sum(0x1p-64f, kWaves > 1 ? 1 : 0) / (float)H);
+  auto scale_row = [&](float f) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= f;
+  };
+  float mean = row_sum(0) / (float)H + eps;
+  if (!(mean < __builtin_inff())) {  // (the same in every thread of the row)
+    // The squares pass float32 where |v| reaches 2^56 or so: the row again, 2^-80 of it, of which 65536 squares stay
+    // below 2^112. Only an infinite or NaN element still ends in an infinite or NaN sum.
+    scale_row(0x1p-80f);
+    mean = row_sum(kWaves > 1 ? 1 : 0) / (float)H + eps * 0x1p-80f * 0x1p-80f;
   }
+  const float rstd = 1.0f / sqrtf(mean);
 
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {

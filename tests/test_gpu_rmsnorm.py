@@ -152,3 +152,19 @@ def test_stream_updated_in_place_of_x(gpu, m, h, dtype, e8):
     _check(x, w, res, 1e-6, q, s, out, e8)
     want = call(x.to(gpu), w.to(gpu), residual=res.to(gpu))
     assert torch.equal(q, want[0]) and torch.equal(s, want[1]) and torch.equal(out, want[2])
+
+
+@pytest.mark.parametrize("e8", [False, True])
+@pytest.mark.parametrize("dtype,size", [(torch.bfloat16, 2.0 ** 62), (torch.bfloat16, 2.0 ** 110), (torch.bfloat16, 2.0 ** 125),
+                                        (torch.float32, 2.0 ** 125)])
+@pytest.mark.parametrize("m,h", [(3, 128), (2, 1040), (2, 7168), (1, 65536)])
+def test_rows_whose_squares_pass_float32(gpu, m, h, dtype, size, e8):
+    """Finite rows up to the type's range are normed as any other."""
+    g = torch.Generator().manual_seed(h)
+    x = (torch.randn(m, h, generator=g).clamp(-3.9, 3.9) * size).to(dtype)
+    x[0, h // 2] = torch.finfo(dtype).max
+    w = (1 + 0.3 * torch.randn(h, generator=g)).to(dtype)
+    announce("rmsnorm large rows", m, h, dtype, size, e8)
+    call = bfp8.rmsnorm_quant_ue8m0 if e8 else bfp8.rmsnorm_quant
+    q, s, hh = call(x.to(gpu), w.to(gpu))
+    _check(x, w, None, 1e-6, q, s, hh, e8)
