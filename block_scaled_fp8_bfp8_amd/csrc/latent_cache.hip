@@ -42,16 +42,19 @@ __global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* __res
   float y[8];
   bf16x8_values(r, y);
   if (w != nullptr) {
-    auto token_sum = [&](float f) {  // of the (y * f)^2
+    auto token_mean = [&] {  // of the y^2
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(y[i] * f, y[i] * f, sum);
-      return wave_sum(sum);
+      for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+      return wave_sum(sum) / (float)kLatentDim;
     };
-    const float sum = token_sum(1.0f);
-    float rstd = 1.0f / sqrtf(sum / (float)kLatentDim + eps);
-    // squares past float32: summed again 2^-64 smaller
-    if (!(sum < __builtin_inff())) rstd = 0x1p-64f / sqrtf(token_sum(0x1p-64f) / (float)kLatentDim);
+    float mean = token_mean() + eps;
+    if (!(mean < __builtin_inff())) {  // squares past float32: the token again, 2^-80 of it
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= 0x1p-80f;
+      mean = token_mean() + eps * 0x1p-80f * 0x1p-80f;
+    }
+    const float rstd = 1.0f / sqrtf(mean);
     float f[8];
     bf16x8_values(*reinterpret_cast<const uint4*>(w + lane * 8), f);
 #pragma unroll

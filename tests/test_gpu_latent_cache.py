@@ -195,3 +195,22 @@ def test_empty_and_refusals(gpu):
         bfp8.latent_cache_read(cache, sc, table.long(), cu, 3)
     with pytest.raises(ValueError):
         bfp8.latent_cache_read(cache, sc, table, cu, 3, out=torch.empty(2, 576, dtype=torch.bfloat16, device=gpu))
+
+
+@pytest.mark.parametrize("size", [2.0 ** 62, 2.0 ** 110, 2.0 ** 125])
+def test_write_norms_tokens_whose_squares_pass_float32(gpu, size):
+    t = 9
+    kv = torch.randn(t, 576, generator=torch.Generator().manual_seed(31)).clamp(-3.9, 3.9)
+    kv[:, :512] *= size
+    kv = kv.bfloat16()
+    kv[3, 200] = torch.finfo(torch.bfloat16).max
+    w = (1 + 0.3 * torch.randn(512, generator=torch.Generator().manual_seed(32))).bfloat16()
+    announce("latent write large tokens", size)
+    _, _, cache, sc = _empty_cache(gpu, 1, t)
+    bfp8.latent_cache_write(kv.to(gpu), torch.arange(t, device=gpu), cache, sc, norm_weight=w.to(gpu), eps=1e-6)
+    y = latent.rmsnorm_ref(kv[:, :512].double().numpy(), w.double().numpy(), 1e-6)
+    rows, codes = cache.cpu()[0].numpy(), sc.cpu()[0].numpy().astype(np.int64)
+    assert ((codes == latent.token_code_ref(y * (1 - D))) | (codes == latent.token_code_ref(y * (1 + D)))).all()
+    s = latent.e8m0_value(codes)[:, None]
+    bound = np.maximum(np.abs(y) * 2.0 ** -4, s * 2.0 ** -10) + D * np.abs(y)
+    assert (np.abs(e4m3.decode(rows[:, :512].copy()) * s - y) <= bound).all()
