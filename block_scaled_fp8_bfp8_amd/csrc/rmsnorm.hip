@@ -9,9 +9,11 @@
 // norm and y are float32; y is not rounded between the norm and the quantization. A NaN in a
 // group makes its scale and codes NaN (maximum() below propagates it).
 //
-// HBM-bound: x and the residual are read once, h, q and s written once (7 bytes an element in
-// bf16; 8192 rows of 7168 with UE8M0 scales: 75 us, 5.5 TB/s). A row lives in the registers of the threads that share it, 8 elements a chunk, so the
-// 16 lanes of a 128-wide group exchange its amax by lane shuffles.
+// HBM-bound: x and the residual are read once, h, q and s written once (7 bytes an element in bf16;
+// 8192 rows of 7168 with UE8M0 scales: 76 us, 5.4 TB/s). A row lives in the registers of the threads
+// that share it, 8 elements a chunk, so the 16 lanes of a 128-wide group exchange its amax by lane
+// shuffles (beyond 32768 columns a few registers of a thread, in float32 66 of them, go to scratch
+// memory).
 #include "device_latent.h"
 #include "launch.h"
 
@@ -142,18 +144,16 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void rmsnorm_quant
     }
     return sum;
   };
-  auto scale_row = [&](float f) {
+  float mean = row_sum(0) / (float)H + eps;
+  // Squares that pass float32 (|v| of 2^56 or more) or come near its least: the row again, times a power of two
+  // with which 65536 squares stay below 2^120. Only an infinite or NaN element still ends in an infinite or NaN sum.
+  const float f = !(mean < __builtin_inff()) ? 0x1p-80f : mean < 0x1p-96f ? 0x1p100f : 1.0f;
+  if (f != 1.0f) {  // (the same in every thread of the row)
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] *= f;
-  };
-  float mean = row_sum(0) / (float)H + eps;
-  if (!(mean < __builtin_inff())) {  // (the same in every thread of the row)
-    // The squares pass float32 where |v| reaches 2^56 or so: the row again, 2^-80 of it, of which 65536 squares stay
-    // below 2^112. Only an infinite or NaN element still ends in an infinite or NaN sum.
-    scale_row(0x1p-80f);
-    mean = row_sum(kWaves > 1 ? 1 : 0) / (float)H + eps * 0x1p-80f * 0x1p-80f;
+    mean = row_sum(kWaves > 1 ? 1 : 0) / (float)H + eps * f * f;
   }
   const float rstd = 1.0f / sqrtf(mean);
 

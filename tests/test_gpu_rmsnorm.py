@@ -168,3 +168,17 @@ def test_rows_whose_squares_pass_float32(gpu, m, h, dtype, size, e8):
     call = bfp8.rmsnorm_quant_ue8m0 if e8 else bfp8.rmsnorm_quant
     q, s, hh = call(x.to(gpu), w.to(gpu))
     _check(x, w, None, 1e-6, q, s, hh, e8)
+
+
+@pytest.mark.parametrize("e8", [False, True])
+@pytest.mark.parametrize("size,eps", [(2.0 ** -70, 0.0), (2.0 ** -100, 0.0), (2.0 ** -120, 0.0), (2.0 ** -60, 2.0 ** -121)])
+@pytest.mark.parametrize("m,h", [(3, 128), (2, 1040), (2, 7168), (1, 65536)])
+def test_rows_whose_squares_vanish_in_float32(gpu, m, h, size, eps, e8):
+    """With an eps as small as the rows' mean square, or none, tiny rows are normed as any other."""
+    g = torch.Generator().manual_seed(h + 1)
+    x = (torch.randn(m, h, generator=g) * size).bfloat16()
+    w = (1 + 0.3 * torch.randn(h, generator=g)).bfloat16()
+    announce("rmsnorm tiny rows", m, h, size, eps, e8)
+    call = bfp8.rmsnorm_quant_ue8m0 if e8 else bfp8.rmsnorm_quant
+    q, s, hh = call(x.to(gpu), w.to(gpu), eps=eps)
+    _check(x, w, None, eps, q, s, hh, e8)
