@@ -49,10 +49,12 @@ __global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* __res
       return wave_sum(sum) / (float)kLatentDim;
     };
     float mean = token_mean() + eps;
-    if (!(mean < __builtin_inff())) {  // squares past float32: the token again, 2^-80 of it
+    // squares that pass float32 or come near its least: the token again, times a power of two
+    const float by = !(mean < __builtin_inff()) ? 0x1p-80f : mean < 0x1p-96f ? 0x1p100f : 1.0f;
+    if (by != 1.0f) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= 0x1p-80f;
-      mean = token_mean() + eps * 0x1p-80f * 0x1p-80f;
+      for (int i = 0; i < 8; ++i) y[i] *= by;
+      mean = token_mean() + eps * by * by;
     }
     const float rstd = 1.0f / sqrtf(mean);
     float f[8];

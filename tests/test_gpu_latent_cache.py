@@ -214,3 +214,21 @@ def test_write_norms_tokens_whose_squares_pass_float32(gpu, size):
     s = latent.e8m0_value(codes)[:, None]
     bound = np.maximum(np.abs(y) * 2.0 ** -4, s * 2.0 ** -10) + D * np.abs(y)
     assert (np.abs(e4m3.decode(rows[:, :512].copy()) * s - y) <= bound).all()
+
+
+@pytest.mark.parametrize("size", [2.0 ** -70, 2.0 ** -100, 2.0 ** -120])
+def test_write_norms_tokens_whose_squares_vanish_in_float32(gpu, size):
+    t = 9
+    kv = torch.randn(t, 576, generator=torch.Generator().manual_seed(33))
+    kv[:, :512] *= size
+    kv = kv.bfloat16()
+    w = (1 + 0.3 * torch.randn(512, generator=torch.Generator().manual_seed(34))).bfloat16()
+    announce("latent write tiny tokens", size)
+    _, _, cache, sc = _empty_cache(gpu, 1, t)
+    bfp8.latent_cache_write(kv.to(gpu), torch.arange(t, device=gpu), cache, sc, norm_weight=w.to(gpu), eps=0.0)
+    y = latent.rmsnorm_ref(kv[:, :512].double().numpy(), w.double().numpy(), 0.0)
+    rows, codes = cache.cpu()[0].numpy(), sc.cpu()[0].numpy().astype(np.int64)
+    assert ((codes == latent.token_code_ref(y * (1 - D))) | (codes == latent.token_code_ref(y * (1 + D)))).all()
+    s = latent.e8m0_value(codes)[:, None]
+    bound = np.maximum(np.abs(y) * 2.0 ** -4, s * 2.0 ** -10) + D * np.abs(y)
+    assert (np.abs(e4m3.decode(rows[:, :512].copy()) * s - y) <= bound).all()
