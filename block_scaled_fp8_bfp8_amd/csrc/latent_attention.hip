@@ -123,7 +123,9 @@ __device__ __forceinline__ Seq sequence(const LatentAttnArgs& a, int b) {
     s.q0 = b;
     s.n = 1;
   }
-  s.len = max(a.lens[b], 0);
+  // A length far past the table is as good as one of which every new token sees a key past it (its row is NaN).
+  const unsigned reach = (unsigned)a.cache.table_width * (unsigned)a.cache.page_size;  // below 2^31
+  s.len = min(max(a.lens[b], 0), (int)min(reach + (unsigned)s.n + 1u, (unsigned)INT32_MAX - kTile));
   return s;
 }
 

@@ -328,3 +328,21 @@ def test_missing_page_reaches_only_rows_that_see_it(gpu, heads, how):
     else:
         assert torch.equal(out[:5], want[:5]) and torch.equal(out[9:], want[9:])
     assert out[5:9].isnan().all()
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 64, 2 ** 30, 65, 96])
+@pytest.mark.parametrize("heads", [2, 128])
+def test_lengths_past_the_table(gpu, length, heads):
+    """A length that the page table does not hold makes the rows that see past it NaN, soon and whatever the length,
+    and leaves the other sequences as they were."""
+    lens, new = [64, 30], [3, 2]
+    c, keys = make(gpu, lens, new, heads, 16, seed=90)
+    want = attend(c)
+    c["lens"][0] = length
+    announce("latent attention length past the table", length, heads)
+    out = attend(c)
+    assert torch.equal(out[3:], want[3:])
+    past = [min(length, 1000) - 3 + i + 1 > 64 for i in range(3)]
+    assert out[:3][torch.tensor(past)].isnan().all()
+    if not all(past):
+        check(out[:2], c["q"][:2], [keys[0]], [64], [2])
