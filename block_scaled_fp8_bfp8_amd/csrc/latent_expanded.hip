@@ -57,6 +57,130 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   else return pack_bf16(lo, hi);
 }
 
+// Of two 16-bit values, those that are infinite or NaN: all ones in their place.
+template <bool kF16>
+__device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
+  constexpr uint32_t kInf = kF16 ? 0x7c00u : 0x7f80u;
+  return ((pair & 0x7fffu) >= kInf ? 0xffffu : 0u) | ((pair >> 16 & 0x7fffu) >= kInf ? 0xffff0000u : 0u);
+}
+
+// A wave's 32 rows again, for values that may be infinite or NaN, of which a weight of zero does not make nothing: the
+// products leave them out, and each is added in the end to the rows that see it (any weight makes the same of it).
+// Everything else has the bits of the first time, so the steps are the kernel's (which has them in place: calling one
+// function for both cost it 6 % on 5 short prompts x 8 heads). Operands come from memory as they are needed: this is
+// rare.
+template <bool kF16>
+__device__ __forceinline__ void attend_not_finite(const uint16_t* q_row, bool row_ok, const uint8_t* kv, int64_t kv_step,
+                                                  const uint8_t* rope, int64_t rope_step, int limit, int any, int flip,
+                                                  float c, v16f* acc, float& l) {
+  const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+  float m = kNegInf;
+  l = 0.f;
+#pragma unroll 1
+  for (int t0 = 0; t0 < any; t0 += kTile) {
+    v16f s[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < 24; ++n) {
+      const int kt = n & 1, ks = n >> 1, key = min(t0 + 32 * kt + r, any - 1);
+      const uint8_t* at = ks < 8 ? kv + key * kv_step + 32 * ks : rope + key * rope_step + 32 * (ks - 8);
+      v4i q = {0, 0, 0, 0};
+      if (row_ok) q = *reinterpret_cast<const v4i*>(q_row + 16 * ks + 8 * g) ^ v4i{flip, flip, flip, flip};
+      s[kt] = mfma<kF16>(*reinterpret_cast<const v4i*>(at + 16 * g), q, s[kt]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    v4i p[4];
+    const int left = limit - t0 - 4 * g;
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (kt * 32 + 8 * (i >> 2) + (i & 3) >= left) s[kt][i] = kNegInf;
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i >> 4][i & 15]);
+    const unsigned bits = __float_as_uint(top);
+    const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+    top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * c;
+    if (__any(top > m + kSlack)) {
+      const float next = fmaxf(m, top);
+      const float f = m == next ? 1.f : __builtin_amdgcn_exp2f(m - next);
+      m = next;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc[d] *= f;
+    }
+    const float ref = m == kNegInf ? 0.f : m;
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float x = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], c, -ref));
+      s[i >> 4][i & 15] = x;
+      sum[i & 1] += x;
+    }
+    l += sum[0] + sum[1];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      p[i >> 2][i & 3] = (int)pack16<kF16>(s[i >> 3][2 * (i & 7)], s[i >> 3][2 * (i & 7) + 1]);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      const int u = n >> 2, d = n & 3;
+      v4i v;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t pair = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int key = min(t0 + 16 * u + 8 * (w >> 1) + 4 * g + 2 * (w & 1) + e, any - 1);
+          pair |= (uint32_t)*reinterpret_cast<const uint16_t*>(kv + key * kv_step + 256 + 2 * (32 * d + r)) << (16 * e);
+        }
+        v[w] = (int)(pair & ~not_finite<kF16>(pair));
+      }
+      acc[d] = mfma<kF16>(v, p[u], acc[d]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll 1
+  for (int t0 = 0; t0 < any; t0 += 64) {
+    // lane k: whether key t0 + k has such values
+    const uint4* row = reinterpret_cast<const uint4*>(kv + min(t0 + lane, any - 1) * kv_step + 256);
+    uint32_t bad = 0;
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+      const uint4 x = row[j];
+      bad |= not_finite<kF16>(x.x) | not_finite<kF16>(x.y) | not_finite<kF16>(x.z) | not_finite<kF16>(x.w);
+    }
+#pragma unroll 1
+    for (uint64_t which = __ballot(bad != 0 && t0 + lane < any); which != 0; which &= which - 1) {
+      const int key = t0 + __builtin_ctzll(which);
+      const bool seen = key < limit;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        v16f add;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {  // columns 32 d + 2 i + 4 g .. + 3
+          const uint2 x = *reinterpret_cast<const uint2*>(kv + key * kv_step + 256 + 8 * g + 64 * d + 4 * i);
+          const uint32_t y[2] = {x.x & not_finite<kF16>(x.x), x.y & not_finite<kF16>(x.y)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t half = y[k >> 1] >> (16 * (k & 1)) & 0xffffu;
+            add[i + k] = !seen ? 0.f : kF16 ? f16_value(half) : __uint_as_float(half << 16);
+          }
+        }
+        acc[d] += add;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ int clip(int v, int top) { return min(max(v, 0), top); }
 
 // The workgroup's block of kBM query rows: the sequences' blocks one after the other, of each the last, which has
@@ -140,7 +264,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
   const int any = w0 < nq ? clip(nk - nq + min(w0 + 32, nq), nk) : 0;
 
   // ---- copies: this wave's share of a tile. In a full tile all rows of a copy lie one lane offset from a
-  // uniform address; in the last tile keys past the block's repeat its last (finite, and masked).
+  // uniform address; in the last tile keys past the block's repeat its last (masked).
   constexpr int kKvCopies = 32 / kWaves, kRopeCopies = 8 / kWaves;
   const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.kv + (int64_t)k0 * a.kv_tok + (int64_t)head * a.kv_head);
   const uint8_t* rope = reinterpret_cast<const uint8_t*>(a.rope + (int64_t)k0 * a.ld_rope);
@@ -180,6 +304,11 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
     rope_next += kTile * rope_step;
   };
 
+  const uint16_t* qs = a.q + (int64_t)(q0 + (row_ok ? row : 0)) * a.q_tok + (int64_t)head * a.q_head;
+  // a negative scale is the queries' sign, so that the largest score in log2 is that of the largest product; a
+  // scale of zero is as good as zero (masked products are infinite)
+  const int flip = a.scale < 0.f ? (int)0x80008000 : 0;
+  const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 0x1p-120f);
   v4i q[12];
   v16f acc[4];
 #pragma unroll
@@ -189,18 +318,13 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
   float m = kNegInf, l = 0.f;
 
   if (tiles > 0) {
-    const uint16_t* qs = a.q + (int64_t)(q0 + (row_ok ? row : 0)) * a.q_tok + (int64_t)head * a.q_head;
 #pragma unroll
     for (int ks = 0; ks < 12; ++ks) {
       q[ks] = v4i{0, 0, 0, 0};
       if (row_ok) q[ks] = *reinterpret_cast<const v4i*>(qs + 16 * ks + 8 * g);
     }
-    // a negative scale is the queries' sign, so that the largest score in log2 is that of the largest product; a
-    // scale of zero is as good as zero (masked products are infinite)
-    const int flip = a.scale < 0.f ? (int)0x80008000 : 0;
 #pragma unroll
     for (int ks = 0; ks < 12; ++ks) q[ks] ^= v4i{flip, flip, flip, flip};
-    const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 0x1p-120f);
 #pragma unroll
     for (int ks = 0; ks < 12; ++ks) asm volatile("" : "+v"(q[ks]));  // loaded before the copies are counted
 
@@ -323,6 +447,16 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
     }
     if (late && tiles - 1 < mine) values(tile_before);
   }
+
+  // Values that are not finite make an output not finite, that of a row that does not see them included (0.1 us of 12
+  // to find out).
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 64; i += 2)
+    top[(i >> 1) & 3] = max_nan(max_nan(top[(i >> 1) & 3], fabsf(acc[i >> 4][i & 15])), fabsf(acc[i >> 4][(i & 15) + 1]));
+  const float largest = max_nan(max_nan(top[0], top[1]), max_nan(top[2], top[3]));
+  if (__builtin_expect(__any(!(largest < __builtin_inff())), 0))
+    attend_not_finite<kF16>(qs, row_ok, kv, kv_step, rope, rope_step, limit, any, flip, c, acc, l);
 
   l += __shfl_xor(l, 32);
   if (!row_ok) return;

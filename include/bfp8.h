@@ -597,6 +597,7 @@ bfp8_status_t bfp8_latent_attention(const uint16_t* q, int64_t T, int64_t H, int
  *               query sees the last key); one that sees none gives zeros. Rows of out that no
  *               sequence owns are not written.
  * Scores, softmax and sums are float32, weights are rounded to dtype before the second product.
+ * Keys and values that are infinite or NaN reach the rows that see them and no others.
  */
 bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64_t Tq, int64_t H,
                                              int64_t q_token_stride, int64_t q_head_stride, const uint16_t* kv,

@@ -172,3 +172,44 @@ def test_empty_and_refusals(gpu):
                 dict(out=torch.empty(4, 2, 64, dtype=torch.bfloat16, device=gpu)), dict(q=c["q"].cpu())]:
         with pytest.raises(ValueError):
             call(**bad)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("nq,nk,heads", [([100], [100], 2), ([40, 90], [77, 90], 3), ([700], [700], 2), ([300] * 9, [300] * 9, 30),
+                                         ([130], [99], 2)])
+def test_infinite_and_nan_values_reach_only_rows_that_see_them(gpu, nq, nk, heads, dtype):
+    """A row that does not see a key keeps its bits whatever the key's values are; one that does has in each column
+    what the sum of the formula gives: the infinity, or NaN for a NaN or infinities of both signs."""
+    c = make(nq, nk, heads, dtype, seed=9)
+    want = run(c, gpu)
+    at = np.concatenate([[0], np.cumsum(nk)])[:-1]
+    inf = float("inf")
+    first = [(3 * n) // 5 for n in nk]  # no key before it is touched
+    for a, f, n in zip(at, first, nk):
+        v = c["kv"][a + f:a + n, :, 128:]
+        v[0, :, 3] = inf
+        v[1, :, 7] = -inf
+        v[2, :, 5] = float("nan")
+        v[4, :, 3] = -inf
+        v[4, :, 64] = inf
+        v[-1, :, 127] = inf  # the last key, which a partly filled tile repeats
+    announce("expanded values not finite", nq[:3], nk[:3], heads, dtype)
+    got = run(c, gpu).cpu()
+    want = want.cpu()
+    q, kv, rope = (c[n].double().numpy() for n in ("q", "kv", "rope"))
+    aq = 0
+    for a, f, n, length in zip(at, first, nq, nk):
+        sees = length - n + 1 + np.arange(n)
+        before = torch.from_numpy(sees <= f)
+        assert torch.equal(got[aq:aq + n][before], want[aq:aq + n][before])
+        for h in sorted({0, heads - 1}):
+            k = np.concatenate([kv[a:a + length, h, :128], rope[a:a + length]], axis=1)
+            with np.errstate(invalid="ignore"):
+                o, _, _ = latent.attention_ref(q[aq:aq + n, h], k, kv[a:a + length, h, 128:], sees, SCALE)
+            g = got[aq:aq + n, h].double().numpy()
+            assert (np.isnan(g) == np.isnan(o)).all()
+            assert (np.where(np.isinf(o), o, 0) == np.where(np.isinf(g), g, 0)).all()
+            same = np.isfinite(o)
+            assert (np.isfinite(g) == same).all()
+            assert (g[same] == want[aq:aq + n, h].double().numpy()[same]).all()
+        aq += n
