@@ -7,7 +7,8 @@
 //
 // Both products run on the FP8 matrix cores, on the cached codes as they are:
 //   * scores: a bf16 query has 8 significant bits, so it is the sum of two e4m3 values
-//     (hi: its top 4 bits; lo: the rest, scaled 2^4), both under one power-of-two scale a row.
+//     (hi: its top 4 bits; lo: the rest, scaled 2^4), both under one power-of-two scale a row:
+//     exactly, down to 2^-13 of the row's largest element; below, to 2^-21 of that.
 //     Two scaled FP8 products cost as many matrix-core clocks as one bf16 product, and the
 //     codes need no conversion. The key's scale code is the instruction's row scale. The rotary
 //     part is a bf16 product into the same accumulator.

@@ -566,13 +566,17 @@ bfp8_status_t bfp8_latent_cache_gather(const uint8_t* rows, int64_t page_stride,
  *   out      bf16 [T][H][512], strides in elements, multiples of 8; rows that no sequence owns
  *            are not written
  *   workspace  bfp8_latent_attention_workspace_bytes(T, B, H, table_width * page_size) bytes,
- *            256-byte aligned (at most about 135 MiB; 0 for short tables). It holds float32
+ *            256-byte aligned (at most 33.7 MB, whatever the sizes; 0 for tables of at most 256
+ *            keys; needed whether or not the lengths then have blocks cut). It holds float32
  *            states of blocks that were cut along their keys, for the call's second launch.
  * A visible key without a page of the cache, or whose scale code is 255 (NaN), makes its rows NaN;
  * rows that do not see a key are not affected by a code-255 key. Scale codes of visible keys are
  * those bfp8_latent_cache_write makes (2^-42 .. 2^40, or 255). Lengths are read on the device: a
- * captured call follows later changes of seq_lens, cu_q and the table. Weights are kept to 8
- * significant bits and scores to the FP8 block dot's 13-binade window, everything else in float32.
+ * captured call follows later changes of seq_lens, cu_q and the table. Below float32 are: weights
+ * times their keys' scales, kept to 8 significant bits down to 2^-13 of the largest of their 32 keys
+ * (smaller ones are off by at most 2^-21 of that); a query's latent dimensions, kept whole down to
+ * 2^-13 of its row's largest (smaller ones likewise); and the scores' products of FP8 codes, summed
+ * in the FP8 block dot's 13-binade window.
  */
 size_t bfp8_latent_attention_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t max_keys);
 bfp8_status_t bfp8_latent_attention(const uint16_t* q, int64_t T, int64_t H, int64_t q_token_stride,

@@ -2,6 +2,8 @@
 rejections, each before any device call, and the documented no-ops (fake pointers are never
 dereferenced, nothing is launched)."""
 
+import random
+
 import pytest
 
 from block_scaled_fp8_bfp8_amd import _native
@@ -172,3 +174,18 @@ def test_expanded_rejections(lib, kw, status):
 
 def test_expanded_t_zero_is_a_no_op(lib):
     assert _expanded(lib, Tq=0, q=None, kv=None, rope=None, out=None, cq=None, ck=None) == OK
+
+
+def test_attention_workspace_stays_below_its_stated_bound(lib):
+    """256 parts of 64 rows: their float32 states, statistics and descriptors, whatever the sizes."""
+    size = lib.bfp8_latent_attention_workspace_bytes
+    bound = 256 * 64 * (512 + 2) * 4 + 2304
+    rng = random.Random(5)
+    most = 0
+    for _ in range(20000):
+        t, h, keys = (int(2 ** rng.uniform(0, top)) for top in (22, 8, 31))
+        b = rng.choice([t, max(1, t // rng.randint(1, 64)), 1])
+        n = size(t, b, h, min(keys, 2 ** 31 - 1))
+        assert n <= bound, (t, b, h, keys)
+        most = max(most, n)
+    assert most == bound < 33 << 20
