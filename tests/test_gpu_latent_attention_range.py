@@ -86,3 +86,53 @@ def test_one_sequence_cut_into_many_parts(gpu):
     announce("latent attention many parts")
     c, keys = make(gpu, [20000], [1], 8, 64, seed=95)
     check(attend(c), c["q"], keys, [20000], [1])
+
+
+@pytest.mark.parametrize("q_by,c_by", [(32.0, 1.0), (1.0, 32.0), (6.0, 6.0), (4096.0, 0.0)])
+def test_outlier_channels(gpu, q_by, c_by):
+    """A few channels of the queries, of the latents or of both far larger than the rest, and queries 2^12 larger where
+    the latents are zero. The root mean square is held as ever; an element's scores to what the two windows can
+    cost: products are off by 2^-13 of the largest of their group of 8 (of each of the query's two terms, together
+    1.125 of it; 64 groups, so the 64 largest products of a key bound the sum), query elements by 2^-21 of their row's
+    largest, and float32 sums by 2^-16 of their terms."""
+    n, heads, channels = 400, 16, [5, 200, 511]
+    announce("latent attention outliers", q_by, c_by)
+    c, _ = make(gpu, [n], [1], heads, 16, seed=98)
+    g = torch.Generator().manual_seed(99)
+    kv = torch.randn(n, 576, generator=g)
+    kv[:, channels] *= c_by
+    kv = kv.bfloat16()
+    i = torch.arange(n)
+    slots = c["table"].cpu()[0, i // 16].long() * 16 + i % 16
+    bfp8.latent_cache_write(kv.to(gpu), slots.to(gpu), c["cache"], c["scales"])
+    rows = c["cache"].cpu()[slots // 16, slots % 16].numpy()
+    codes = c["scales"].cpu()[slots // 16, slots % 16].numpy()
+    lat = e4m3.decode(rows[:, :512].copy()) * latent.e8m0_value(codes)[:, None]
+    keys = np.concatenate([lat, kv[:, 512:].double().numpy()], axis=1)
+    c["q"][:, :, channels] *= q_by
+    out = attend(c)
+    check(out, c["q"], [keys], [n], [1])
+    q, got = c["q"][0].double().cpu().numpy(), out[0].double().cpu().numpy()
+    o, mag, _ = latent.attention_ref(q, keys, lat, np.full(heads, n), SCALE)
+    for h in range(heads):
+        terms = np.abs(q[h] * keys)
+        windows = 2.0 ** -10 * 1.125 * np.sort(terms[:, :512], axis=1)[:, -64:].sum(axis=1)
+        d = SCALE * (windows + 2.0 ** -21 * np.abs(q[h, :512]).max() * np.abs(lat).sum(axis=1) + 2.0 ** -16 * terms.sum(axis=1)).max()
+        bound = 2.0 ** -8 * np.abs(o[h]) + (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -14 + 2 * np.expm1(d)) * mag[h]
+        assert (np.abs(got[h] - o[h]) <= bound).all()
+
+
+@pytest.mark.parametrize("lens,heads", [([5000] + [7 + 3 * i % 90 for i in range(259)], 16), ([70] * 129, 128), ([2000] + [100] * 140, 128)])
+def test_many_blocks_of_uneven_lengths(gpu, lens, heads):
+    """As many blocks as run at once or more, one sequence much longer than the rest, and one block too many."""
+    announce("latent attention many uneven", len(lens), max(lens), heads)
+    c, keys = make(gpu, lens, [1] * len(lens), heads, 64, seed=100)
+    out = attend(c)
+    check(out, c["q"], keys, lens, [1] * len(lens))
+    assert torch.equal(out.view(torch.int16), attend(c).view(torch.int16))
+
+
+def test_long_context(gpu):
+    announce("latent attention long context")
+    c, keys = make(gpu, [70001, 40], [1, 1], 8, 64, seed=101)
+    check(attend(c), c["q"], keys, [70001, 40], [1, 1])
