@@ -483,10 +483,11 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void latent_expanded_kerne
 }
 
 // The longest blocks first where a compute unit gets no more than about six (4 prompts of 2048 x 16 heads: 132 us in
-// the given order, 105 so; 32 of 50 to 1000 x 16, 1552 workgroups: 145 and 130). Beyond, the tail is short, and
-// blocks of one sequence that run together share its keys in the L2s (4 of 2100 to 4090 x 32, 1664 workgroups: 602
-// and 619; 16 of 100 to 4000 x 32: 1145 and 1262). Where all have a compute unit of their own the search is 0.4 us for
-// nothing (5 of 17 to 300 x 8: 11.9 and 12.3). A wave looks among 64 sequences.
+// the given order, 105 so; 32 of 50 to 1000 x 16, 1552 workgroups: 145 and 130). Beyond, the tail is short, and the
+// given order is the faster one (4 of 2100 to 4090 x 32, 1664 workgroups: 602 and 619; 16 of 100 to 4000 x 32: 1145 and
+// 1262), it is thought because blocks of one sequence run together and share its keys in the L2s: the limit stands
+// between these sizes, the cause was not measured by itself. Where all have a compute unit of their own the search is
+// 0.4 us for nothing (5 of 17 to 300 x 8: 11.9 and 12.3). A wave looks among 64 sequences.
 constexpr int64_t kLongestFirst = 1600;
 
 template <bool kF16, int kWaves>
