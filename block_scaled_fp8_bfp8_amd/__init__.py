@@ -102,11 +102,15 @@ def _workspace(device: torch.device, nbytes: int) -> tuple[int, int, torch.Tenso
     kept buffer is replaced when a call needs more."""
     if nbytes == 0:
         return 0, 0, None
-    if _capturing(device):
+    stream = _stream(device)
+    if stream != 0 and _capturing(device):  # (the default stream cannot be captured)
         buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         return buf.data_ptr(), nbytes, buf
-    key = (device.index, _stream(device))
-    kept = _workspaces.__dict__.setdefault("kept", {})
+    key = (device.index, stream)
+    try:
+        kept = _workspaces.kept
+    except AttributeError:  # the thread's first call
+        kept = _workspaces.kept = {}
     buf = kept.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
