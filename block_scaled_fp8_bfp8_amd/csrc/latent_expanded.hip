@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
 // products leave them out, and each is added in the end to the rows that see it (any weight makes the same of it).
 // Everything else has the bits of the first time, so the steps are the kernel's (which has them in place: calling one
 // function for both cost it 6 % on 5 short prompts x 8 heads). Operands come from memory as they are needed: this is
-// rare.
+// rare (4 prompts of 4000 x 32 heads: 0.7 ms; with a NaN at the first key of one 2.1, of all four 6.0).
 template <bool kF16>
 __device__ __forceinline__ void attend_not_finite(const uint16_t* q_row, bool row_ok, const uint8_t* kv, int64_t kv_step,
                                                   const uint8_t* rope, int64_t rope_step, int limit, int any, int flip,
