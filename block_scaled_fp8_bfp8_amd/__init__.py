@@ -31,6 +31,7 @@ __all__ = [
     "moe_forward_workspace_bytes", "nn_to_nt_weights", "pad_k", "expand_act_scales", "expand_weight_scale", "set_schedule", "get_schedule", "schedule_for",
     "rmsnorm_quant", "rmsnorm_quant_ue8m0", "latent_cache_write", "latent_cache_read", "latent_cache_gather",
     "latent_attention", "latent_attention_workspace_bytes", "latent_attention_expanded",
+    "quant_act_int8", "gemm_int8", "linear_int8", "linear_int8_workspace_bytes",
     "abi_version", "BfpError", "LibraryMissing",
 ]
 
@@ -1081,6 +1082,138 @@ def latent_attention_expanded(q: torch.Tensor, kv: torch.Tensor, rope: torch.Ten
         kv.stride(1), rope.data_ptr(), rope.stride(0), cu_q.data_ptr(), cu_k.data_ptr(), b, scale, out.data_ptr(),
         out.stride(0), out.stride(1), _stream(q.device))
     _check(st, "bfp8_latent_attention_expanded")
+    return out
+
+
+def _call(device: torch.device, name: str, *args):
+    """The C entry `name` on the device of its tensors and that device's current stream (its last argument)."""
+    entry = getattr(_native.lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = entry(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = entry(*args, _stream(device))
+    _check(st, name)
+
+
+def _int8_scales(s: torch.Tensor, name: str, n: int):
+    _require(s, name, torch.float32, 1)
+    if s.shape[0] != n or (n > 1 and s.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} scales, got shape {tuple(s.shape)}")
+
+
+def _int8_weight(w_q: torch.Tensor, w_s: torch.Tensor, bias: torch.Tensor | None, k: int, dtype) -> int:
+    """Checks a weight [N, K] of int8 codes, its channel scales and its bias; returns N."""
+    _require(w_q, "w_q", torch.int8, 2)
+    n = w_q.shape[0]
+    if w_q.shape[1] != k:
+        raise ValueError(f"the activations and w_q disagree on K: {k} vs {w_q.shape[1]}")
+    if w_q.stride(1) != 1:
+        raise ValueError("w_q must be K-contiguous")
+    _int8_scales(w_s, "w_s", n)
+    if bias is not None:
+        _require(bias, "bias", dtype, 1)
+        if bias.shape[0] != n or (n > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias must be a contiguous vector of length {n}")
+    return n
+
+
+def _row_stride(t: torch.Tensor, step: int) -> int:
+    """Row stride of a matrix; a single row's carries no meaning (its length, rounded up to `step`)."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // step) * step
+
+
+def quant_act_int8(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """Quantization to 8-bit integers, one scale a token: for x [M, K] (fp32, bf16 or fp16; K a
+    multiple of 16, at most 65536; rows may be apart) returns (q int8 [M, K], s float32 [M]) with
+    s = max(max |x|, 1e-10) / 127 and q = 127 x / max |x| to the nearest integer, ties to even. A token with
+    an infinite or NaN element has a NaN scale and zero codes. A weight [N, K] is quantized alike, one
+    scale a channel."""
+    dt = _in_dtype(x, "quant_act_int8")
+    _require(x, "x", x.dtype, 2)
+    if x.stride(1) != 1:
+        raise ValueError("x must be K-contiguous")
+    m, k = x.shape
+    if q is None:
+        q = torch.empty((m, k), dtype=torch.int8, device=x.device)
+    else:
+        _require(q, "q", torch.int8, 2)
+        if q.shape != (m, k) or q.stride(1) != 1:
+            raise ValueError(f"q must be [{m}, {k}] and K-contiguous")
+    if scales is None:
+        scales = torch.empty((m,), dtype=torch.float32, device=x.device)
+    else:
+        _int8_scales(scales, "scales", m)
+    _same_device(x, q=q, scales=scales)
+    _call(x.device, "bfp8_quant_act_int8", x.data_ptr(), dt, m, k, _row_stride(x, 8), q.data_ptr(), _row_stride(q, 16),
+          scales.data_ptr())
+    return q, scales
+
+
+def gemm_int8(a_q: torch.Tensor, a_s: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor,
+              bias: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """C[M, N] = (a_q . w_q^T) * a_s[:, None] * w_s + bias, for int8 codes a_q [M, K] and w_q [N, K] (K a
+    multiple of 16, at most 65536; rows may be apart by multiples of 16), float32 scales a_s [M] of
+    the tokens and w_s [N] of the channels, and an optional bias [N]. The sums are exact; C and the bias are
+    bfloat16 or float16 (dtype)."""
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise NotImplementedError(f"gemm_int8 gives bfloat16 or float16, not {dtype}")
+    _require(a_q, "a_q", torch.int8, 2)
+    m, k = a_q.shape
+    if a_q.stride(1) != 1:
+        raise ValueError("a_q must be K-contiguous")
+    _int8_scales(a_s, "a_s", m)
+    n = _int8_weight(w_q, w_s, bias, k, dtype)
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=a_q.device)
+    else:
+        _require(out, "out", dtype, 2)
+        if out.shape != (m, n) or (n > 1 and out.stride(1) != 1):
+            raise ValueError(f"out must be [{m}, {n}] with contiguous rows")
+    _same_device(a_q, a_s=a_s, w_q=w_q, w_s=w_s, bias=bias, out=out)
+    _call(a_q.device, "bfp8_gemm_int8", a_q.data_ptr(), _row_stride(a_q, 16), a_s.data_ptr(), w_q.data_ptr(),
+          _row_stride(w_q, 16), w_s.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
+          _IN_DTYPES[dtype], _row_stride(out, 1), m, n, k)
+    return out
+
+
+def linear_int8_workspace_bytes(m: int, k: int) -> int:
+    """Workspace bytes of linear_int8 (codes and scales of the activations)."""
+    return _native.lib().bfp8_linear_int8_workspace_bytes(m, k)
+
+
+def linear_int8(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, bias: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Linear layer on 8-bit integers: quant_act_int8 of x [M, K] (bf16 or fp16), gemm_int8 with w_q
+    [N, K] and w_s [N], and the bias; the output and the bias have x's dtype.
+
+    workspace: optional uint8 buffer of at least linear_int8_workspace_bytes(M, K) bytes; by default one
+    buffer per (device, stream, host thread) is kept, and a call that is being captured takes one
+    from its graph's memory."""
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise NotImplementedError(f"linear_int8 takes bfloat16 or float16 activations (the output has their dtype), "
+                                  f"got {x.dtype}")
+    _require(x, "x", x.dtype, 2)
+    if x.stride(1) != 1:
+        raise ValueError("x must be K-contiguous")
+    m, k = x.shape
+    n = _int8_weight(w_q, w_s, bias, k, x.dtype)
+    if out is None:
+        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    else:
+        _require(out, "out", x.dtype, 2)
+        if out.shape != (m, n) or (n > 1 and out.stride(1) != 1):
+            raise ValueError(f"out must be [{m}, {n}] with contiguous rows")
+    _same_device(x, w_q=w_q, w_s=w_s, bias=bias, out=out, workspace=workspace)
+    if workspace is None:
+        ws_ptr, ws_bytes, workspace = _workspace(x.device, linear_int8_workspace_bytes(m, k))
+    else:
+        _require(workspace, "workspace", torch.uint8, 1)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _call(x.device, "bfp8_linear_int8", x.data_ptr(), _IN_DTYPES[x.dtype], m, k, _row_stride(x, 8), w_q.data_ptr(),
+          _row_stride(w_q, 16), w_s.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
+          _row_stride(out, 1), n, ws_ptr or None, ws_bytes)
     return out
 
 

@@ -15,6 +15,7 @@
 #include <string>
 
 #include "bfp8.h"
+#include "int8.h"
 #include "latent.h"
 #include "launch.h"
 
@@ -1136,6 +1137,124 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
   args.scale = scale;
   return launched(bfp8::launch_latent_expanded(args, dtype == BFP8_IN_F16, (hipStream_t)stream),
                   "latent_attention_expanded");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes of the integer products.
+bfp8_status_t check_int8_sizes(int64_t M, int64_t N, int64_t K) {
+  if (M < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "M = %lld is negative", (long long)M);
+  if (N < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "N = %lld must be >= 1", (long long)N);
+  if (K < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "K = %lld must be >= 1", (long long)K);
+  if (K % 16 != 0) return fail(BFP8_ERR_UNSUPPORTED, "K = %lld is not a multiple of 16", (long long)K);
+  if (K > bfp8::kInt8MaxK) return fail(BFP8_ERR_UNSUPPORTED, "K = %lld is more than %d", (long long)K, bfp8::kInt8MaxK);
+  if (M > kMaxDim || N > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "M and N must each be at most 2^30");
+  if (((M + 63) / 64) * ((N + 127) / 128) > (int64_t)INT32_MAX)
+    return fail(BFP8_ERR_UNSUPPORTED, "M x N = %lld x %lld has more output tiles than one launch grid holds",
+                (long long)M, (long long)N);
+  return BFP8_OK;
+}
+
+bfp8_status_t check_quant_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, const int8_t* q, int64_t ldq,
+                               const float* s) {
+  if (x_dtype != BFP8_IN_F32 && x_dtype != BFP8_IN_BF16 && x_dtype != BFP8_IN_F16)
+    return fail(BFP8_ERR_UNSUPPORTED, "x_dtype %d is not BFP8_IN_F32, BFP8_IN_BF16 or BFP8_IN_F16", x_dtype);
+  const bfp8_status_t st = check_int8_sizes(M, 1, K);
+  if (st != BFP8_OK || M == 0) return st;
+  if (!x || !q || !s) return fail(BFP8_ERR_INVALID_ARGUMENT, "x, q and s must not be NULL");
+  if (ldx < K) return fail(BFP8_ERR_INVALID_ARGUMENT, "ldx = %lld < K = %lld", (long long)ldx, (long long)K);
+  if (ldq < K) return fail(BFP8_ERR_INVALID_ARGUMENT, "ldq = %lld < K = %lld", (long long)ldq, (long long)K);
+  const int64_t esize = x_dtype == BFP8_IN_F32 ? 4 : 2;
+  if (ldx > kMaxDim || ldq > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "row strides must be at most 2^30");
+  if ((ldx * esize) % 16 || ldq % 16) return fail(BFP8_ERR_MISALIGNED, "row strides must be multiples of 16 bytes");
+  if (!aligned(x, 16) || !aligned(q, 16)) return fail(BFP8_ERR_MISALIGNED, "x and q must be 16-byte aligned");
+  if (!aligned(s, 4)) return fail(BFP8_ERR_MISALIGNED, "s must be 4-byte aligned");
+  return BFP8_OK;
+}
+
+bfp8_status_t check_gemm_int8(const int8_t* a, int64_t lda, const float* as, const int8_t* b, int64_t ldb, const float* bs,
+                              const uint16_t* bias, const uint16_t* c, int out_dtype, int64_t ldc, int64_t M, int64_t N,
+                              int64_t K) {
+  if (out_dtype != BFP8_IN_BF16 && out_dtype != BFP8_IN_F16)
+    return fail(BFP8_ERR_UNSUPPORTED, "out_dtype %d is not BFP8_IN_BF16 or BFP8_IN_F16", out_dtype);
+  const bfp8_status_t st = check_int8_sizes(M, N, K);
+  if (st != BFP8_OK) return st;
+  if (!b || !bs) return fail(BFP8_ERR_INVALID_ARGUMENT, "b and bs must not be NULL");
+  if (M > 0 && (!a || !as || !c)) return fail(BFP8_ERR_INVALID_ARGUMENT, "a, as and c must not be NULL when M > 0");
+  if (lda < K) return fail(BFP8_ERR_INVALID_ARGUMENT, "lda = %lld < K = %lld", (long long)lda, (long long)K);
+  if (ldb < K) return fail(BFP8_ERR_INVALID_ARGUMENT, "ldb = %lld < K = %lld", (long long)ldb, (long long)K);
+  if (ldc < N) return fail(BFP8_ERR_INVALID_ARGUMENT, "ldc = %lld < N = %lld", (long long)ldc, (long long)N);
+  if (lda % 16 || ldb % 16) return fail(BFP8_ERR_MISALIGNED, "lda and ldb must be multiples of 16 bytes");
+  // a tile's rows are addressed with 32-bit offsets from its first
+  if (lda >= (int64_t)1 << 23 || ldb >= (int64_t)1 << 23) return fail(BFP8_ERR_UNSUPPORTED, "lda and ldb must be below 2^23");
+  if (ldc > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "ldc must be at most 2^30");
+  if (!aligned(a, 16) || !aligned(b, 16)) return fail(BFP8_ERR_MISALIGNED, "a and b must be 16-byte aligned");
+  if (!aligned(as, 4) || !aligned(bs, 4)) return fail(BFP8_ERR_MISALIGNED, "as and bs must be 4-byte aligned");
+  if (!aligned(c, 2) || !aligned(bias, 2)) return fail(BFP8_ERR_MISALIGNED, "c and bias must be 2-byte aligned");
+  return BFP8_OK;
+}
+
+// Workspace of the integer linear layer: codes in rows of K bytes, then the scales.
+size_t int8_scales_at(int64_t M, int64_t K) { return ((size_t)M * (size_t)K + 255) / 256 * 256; }
+
+}  // namespace
+
+extern "C" {
+
+bfp8_status_t bfp8_quant_act_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ldq,
+                                  float* s, void* stream) {
+  bfp8_status_t st = check_quant_int8(x, x_dtype, M, K, ldx, q, ldq, s);
+  if (st != BFP8_OK) return st;
+  if (M == 0) return ok();
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  return launched(bfp8::launch_quant_act_int8(x, x_dtype, M, K, ldx, q, ldq, s, (hipStream_t)stream), "quant_act_int8");
+}
+
+bfp8_status_t bfp8_gemm_int8(const int8_t* a, int64_t lda, const float* as, const int8_t* b, int64_t ldb, const float* bs,
+                             const uint16_t* bias, uint16_t* c, int out_dtype, int64_t ldc, int64_t M, int64_t N,
+                             int64_t K, void* stream) {
+  bfp8_status_t st = check_gemm_int8(a, lda, as, b, ldb, bs, bias, c, out_dtype, ldc, M, N, K);
+  if (st != BFP8_OK) return st;
+  if (M == 0) return ok();
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  const bfp8::Int8GemmArgs args{a, lda, as, b, ldb, bs, bias, c, ldc, (int)M, (int)N, (int)K, out_dtype == BFP8_IN_F16};
+  return launched(bfp8::launch_gemm_int8(args, (hipStream_t)stream), "gemm_int8");
+}
+
+size_t bfp8_linear_int8_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 1 || K < 1 || M > kMaxDim || K > bfp8::kInt8MaxK) return 0;
+  return int8_scales_at(M, K) + ((size_t)M * 4 + 255) / 256 * 256;
+}
+
+bfp8_status_t bfp8_linear_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, const int8_t* b, int64_t ldb,
+                               const float* bs, const uint16_t* bias, uint16_t* c, int64_t ldc, int64_t N,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (x_dtype != BFP8_IN_BF16 && x_dtype != BFP8_IN_F16)
+    return fail(BFP8_ERR_UNSUPPORTED,
+                "the linear layer takes bf16 or fp16 activations (its output has their dtype), got x_dtype %d", x_dtype);
+  bfp8_status_t st = check_int8_sizes(M, N, K);
+  if (st != BFP8_OK) return st;
+  if (!aligned(workspace, 256)) return fail(BFP8_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  const size_t need = bfp8_linear_int8_workspace_bytes(M, K);
+  if (M > 0 && (!workspace || workspace_bytes < need))
+    return fail(BFP8_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  int8_t* q = static_cast<int8_t*>(workspace);
+  float* s = M > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + int8_scales_at(M, K)) : nullptr;
+  st = check_quant_int8(x, x_dtype, M, K, ldx, q, K, s);
+  if (st != BFP8_OK) return st;
+  st = check_gemm_int8(q, K, s, b, ldb, bs, bias, c, x_dtype, ldc, M, N, K);
+  if (st != BFP8_OK) return st;
+  if (M == 0) return ok();
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  st = launched(bfp8::launch_quant_act_int8(x, x_dtype, M, K, ldx, q, K, s, (hipStream_t)stream), "quant_act_int8");
+  if (st != BFP8_OK) return st;
+  const bfp8::Int8GemmArgs args{q, K, s, b, ldb, bs, bias, c, ldc, (int)M, (int)N, (int)K, x_dtype == BFP8_IN_F16};
+  return launched(bfp8::launch_gemm_int8(args, (hipStream_t)stream), "gemm_int8");
 }
 
 bfp8_status_t bfp8_set_schedule(int schedule) {

@@ -1,0 +1,408 @@
+// Product of 8-bit integers with a scale for each token and each channel:
+//   C[m, n] = round16((sum_k A[m, k] B[n, k]) As[m] Bs[n] + bias[n])
+// The sum runs in 32-bit integers on the matrix cores and is exact (K <= 65536), so its order does not matter; it is
+// converted to float32 (an error of 2^-24 at most), scaled and biased there, and rounded once to bf16 or fp16.
+//
+// As the scales are those of whole rows, nothing but the product happens along K. Both kernels form C^T = B A^T
+// (weight rows on the matrix instruction's first operand, so that a lane's results are neighbours in a row of C), and
+// copy operands to LDS in pieces of 8 rows x 128 bytes, whose 16-byte columns are XORed by the row (lds_swizzle), so
+// that fragment reads are free of bank conflicts. Rows past M or N repeat the last one and are not stored. Where the
+// last 128-byte block holds fewer bytes, its missing pieces are read from its first one (nothing past K is touched) and
+// cleared in the activations' fragments: an integer product with zero is zero whatever stands on the other side.
+//   * K-split (few rows; reading the weights is the work): the 8 waves of a workgroup take the K blocks of a small
+//     tile in turn, each from slots of its own, and add their sums through LDS.
+//   * tiled: a workgroup's waves share stages of a K block, two to four of them, with one barrier a block.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "device_latent.h"
+#include "int8.h"
+#include "launch.h"
+
+namespace bfp8 {
+
+namespace {
+
+typedef int v16i __attribute__((ext_vector_type(16)));
+
+// One output: the sum times the scales, plus the bias, as 16 bits.
+template <bool kF16>
+__device__ __forceinline__ float bias_value(uint16_t b) {
+  if constexpr (kF16) return f16_value(b);
+  else return __uint_as_float((uint32_t)b << 16);
+}
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (kF16) return f32_to_f16_rne(lo) | f32_to_f16_rne(hi) << 16;
+  else return pack_bf16(lo, hi);
+}
+
+// 4 neighbouring outputs n .. n + 3 of a row.
+__device__ __forceinline__ void store4(uint16_t* c, int n, int N, bool vec_ok, uint32_t p0, uint32_t p1) {
+  if (vec_ok && n + 3 < N) {
+    *reinterpret_cast<uint2*>(c) = make_uint2(p0, p1);
+  } else {
+    if (n < N) c[0] = (uint16_t)p0;
+    if (n + 1 < N) c[1] = (uint16_t)(p0 >> 16);
+    if (n + 2 < N) c[2] = (uint16_t)p1;
+    if (n + 3 < N) c[3] = (uint16_t)(p1 >> 16);
+  }
+}
+
+// Clears the pieces of a fragment past K: `piece` is its 16-byte column in a block that has `bytes` of them.
+__device__ __forceinline__ v4i keep_valid(v4i f, int piece, int bytes) {
+  const bool in = 16 * piece < bytes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = in ? f[i] : 0;
+  return f;
+}
+
+constexpr int kWaves = 8;
+
+// ---------------------------------------------------------------- few rows: the waves split K
+
+// A workgroup's tile is BN = 16 TN weight rows x BM = 16 TM activation rows.
+template <int TN, int TM, int SLOTS, bool kF16>
+__global__ __launch_bounds__(kWaves * 64) void gemm_int8_ksplit_kernel(Int8GemmArgs args) {
+  constexpr int BN = 16 * TN, BM = 16 * TM;
+  constexpr int kPieces = (BN + BM) / 8;
+  constexpr int kSlot = (BN + BM) * kBlock;
+  static_assert(BN * BM * 4 <= SLOTS * kSlot, "the sums of a wave fit its slots");
+  static_assert((SLOTS - 1) * kPieces < 64, "copies in flight that a wait can count");
+  __shared__ __attribute__((aligned(1024))) uint8_t slots[kWaves][SLOTS][kSlot];
+
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, kc = lane >> 4;
+  const int n0 = blockIdx.x * BN, m0 = blockIdx.y * BM;
+  const int M = args.M, N = args.N;
+  const int KB = (args.K + kBlock - 1) / kBlock;
+  const int last_bytes = args.K - (KB - 1) * kBlock;
+  const int nkb = KB > w ? (KB - w + kWaves - 1) / kWaves : 0;  // this wave's blocks: w + 8 i
+
+  // piece j: rows 8 j .. 8 j + 7 of the tile, lane l at row 8 j + l / 8, physical column l % 8
+  uint32_t off[kPieces];
+  const int8_t* bmat = args.b + (int64_t)n0 * args.ldb;
+  const int8_t* amat = args.a + (int64_t)m0 * args.lda;
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int row = j * 8 + (lane >> 3);
+    const int col = (lane & 7) ^ lds_swizzle(row);
+    off[j] = (j * 8 < BN ? (uint32_t)min(row, N - 1 - n0) * (uint32_t)args.ldb
+                         : (uint32_t)min(row - BN, M - 1 - m0) * (uint32_t)args.lda) + (uint32_t)(col * 16);
+  }
+  auto issue = [&](int slot, int kb) __attribute__((always_inline)) {
+    const uint32_t dst = lds_addr(&slots[w][slot][0]);
+    const bool part = kb == KB - 1 && last_bytes < kBlock;  // uniform
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int col = (lane & 7) ^ lds_swizzle(j * 8 + (lane >> 3));
+      const uint32_t o = part && 16 * col >= last_bytes ? off[j] - (uint32_t)(col * 16) : off[j];
+      copy16_m0((j * 8 < BN ? bmat : amat) + (int64_t)kb * kBlock, o, dst + (uint32_t)(j * 1024));
+    }
+  };
+  const int sw = lds_swizzle(r);
+  const uint32_t at_lo = (uint32_t)(r * kBlock + (((2 * kc) ^ sw) << 4)), at_hi = (uint32_t)(r * kBlock + (((2 * kc + 1) ^ sw) << 4));
+
+  v4i acc[TN][TM];
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) acc[tn][tm] = v4i{0, 0, 0, 0};
+
+  // workgroups with the same weight rows start at different blocks: one fetches a block from HBM, the others find
+  // it in L2
+  const int rot = nkb > 0 ? (int)((int64_t)blockIdx.y * nkb / gridDim.y) : 0;
+  auto block_of = [&](int i) __attribute__((always_inline)) { return w + (i + rot < nkb ? i + rot : i + rot - nkb) * kWaves; };
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s)
+    if (s < nkb) issue(s, block_of(s));
+  int slot = 0;
+  for (int i = 0; i < nkb; ++i) {
+    const int kb = block_of(i);
+    if (i + SLOTS - 1 < nkb) wait_copies_upto<(SLOTS - 1) * kPieces>();
+    else wait_copies();
+    const uint8_t* sl = &slots[w][slot][0];
+    const bool part = kb == KB - 1 && last_bytes < kBlock;
+    v4i fb[TN][2], fa[TM][2];
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) {
+      fb[tn][0] = *reinterpret_cast<const v4i*>(sl + at_lo + tn * 16 * kBlock);
+      fb[tn][1] = *reinterpret_cast<const v4i*>(sl + at_hi + tn * 16 * kBlock);
+    }
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+      fa[tm][0] = *reinterpret_cast<const v4i*>(sl + at_lo + (BN + tm * 16) * kBlock);
+      fa[tm][1] = *reinterpret_cast<const v4i*>(sl + at_hi + (BN + tm * 16) * kBlock);
+      if (part) {
+        fa[tm][0] = keep_valid(fa[tm][0], 2 * kc, last_bytes);
+        fa[tm][1] = keep_valid(fa[tm][1], 2 * kc + 1, last_bytes);
+      }
+    }
+    // the slot is refilled after this wave's reads of it have returned
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (i + SLOTS < nkb) issue(slot, block_of(i + SLOTS));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+          acc[tn][tm] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[tn][h], fa[tm][h], acc[tn][tm], 0, 0, 0);
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
+  }
+
+  // result register i of lane l: weight row 4 (l / 16) + i, activation row l % 16
+  int* sums = reinterpret_cast<int*>(&slots[w][0][0]);  // (no copy of this wave is in flight)
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) *reinterpret_cast<v4i*>(sums + ((tn * TM + tm) * 64 + lane) * 4) = acc[tn][tm];
+  __syncthreads();
+  const bool vec_ok = (args.ldc & 3) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 7) == 0;
+  for (int q = threadIdx.x; q < TN * TM * 64; q += kWaves * 64) {
+    const int ln = q & 63, tile = q >> 6;
+    const int m = m0 + (tile % TM) * 16 + (ln & 15), n = n0 + (tile / TM) * 16 + 4 * (ln >> 4);
+    if (m >= M || n >= N) continue;
+    const float ms = args.as[m];
+    float ns[4], add[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = min(n + e, N - 1);
+      ns[e] = args.bs[at];
+      add[e] = args.bias != nullptr ? bias_value<kF16>(args.bias[at]) : 0.f;
+    }
+    v4i v = {0, 0, 0, 0};
+#pragma unroll
+    for (int ww = 0; ww < kWaves; ++ww) v += *reinterpret_cast<const v4i*>(reinterpret_cast<const int*>(&slots[ww][0][0]) + q * 4);
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = fmaf((float)v[e] * ms, ns[e], add[e]);
+    store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
+  }
+}
+
+// ---------------------------------------------------------------- tiles of LDS stages
+
+// A BN x BM tile of C^T, WGN x WGM waves of 32 TN x 32 TM. A K block is four steps of 32x32x32 products; the fragments
+// of a step are read while the one before is multiplied. At the end of a block's third step its last fragments have
+// been read and the next block has landed; past the barrier there its stage is refilled, and the next block's first
+// fragments are read.
+template <int BN, int BM, int WGN, int WGM, int STAGES, bool kPart, bool kF16>
+__global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8GemmArgs args) {
+  constexpr int kNumWaves = WGN * WGM;
+  constexpr int WN = BN / WGN, WM = BM / WGM, TN = WN / 32, TM = WM / 32;
+  constexpr int kStage = (BN + BM) * kBlock;
+  constexpr int kCopies = (BN + BM) / 8 / kNumWaves;  // pieces of a block that a wave copies
+  static_assert((BN + BM) % (8 * kNumWaves) == 0 && BN % 8 == 0 && WN % 32 == 0 && WM % 32 == 0, "whole pieces and products");
+  static_assert(STAGES >= 2 && (STAGES - 2) * kCopies < 64, "stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * kStage];
+  __shared__ __attribute__((aligned(16))) float channel[2][BN];  // scale and bias
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = w % WGN, wm = w / WGN;
+  const int r = lane & 31, g = lane >> 5;
+  const int M = args.M, N = args.N;
+  const int KB = (args.K + kBlock - 1) / kBlock;
+  const int last_bytes = args.K - (KB - 1) * kBlock;
+  int tile_n, tile_m;
+  map_tile(blockIdx.x, (N + BN - 1) / BN, (M + BM - 1) / BM, 8, tile_n, tile_m);
+  const int n0 = __builtin_amdgcn_readfirstlane(tile_n * BN), m0 = __builtin_amdgcn_readfirstlane(tile_m * BM);
+
+  const int8_t* bmat = args.b + (int64_t)n0 * args.ldb;
+  const int8_t* amat = args.a + (int64_t)m0 * args.lda;
+  const int first = w * kCopies * 8;  // the wave's first row of a stage: weights, then activations
+  uint32_t off[kCopies];
+#pragma unroll
+  for (int j = 0; j < kCopies; ++j) {
+    const int row = first + j * 8 + (lane >> 3);
+    const int col = (lane & 7) ^ lds_swizzle(row);
+    off[j] = (first + j * 8 < BN ? (uint32_t)min(row, N - 1 - n0) * (uint32_t)args.ldb
+                                 : (uint32_t)min(row - BN, M - 1 - m0) * (uint32_t)args.lda) + (uint32_t)(col * 16);
+  }
+  const uint32_t lds = lds_addr(smem);
+  auto issue_piece = [&](int stage, int kb, int j) __attribute__((always_inline)) {
+    uint32_t o = off[j];
+    if (kPart && kb == KB - 1) {  // uniform
+      const uint32_t col = (uint32_t)((lane & 7) ^ lds_swizzle(first + j * 8 + (lane >> 3)));
+      if ((int)(16 * col) >= last_bytes) o -= 16 * col;
+    }
+    copy16_m0((first + j * 8 < BN ? bmat : amat) + (int64_t)kb * kBlock, o,
+              __builtin_amdgcn_readfirstlane(lds + (uint32_t)(stage * kStage + (first + j * 8) * kBlock)));
+  };
+
+  v16i acc[TN][TM];
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[tn][tm][i] = 0;
+
+  // fragments: lane l holds row l % 32 and, in step s, the 16-byte column 2 s + l / 32
+  const int sw = lds_swizzle(r);
+  uint32_t at[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) at[s] = (uint32_t)(r * kBlock + (((2 * s + g) ^ sw) << 4));
+  v4i fb[2][TN], fa[2][TM];
+  auto read_b = [&](const uint8_t* stage, int s, int tn) __attribute__((always_inline)) {
+    fb[s & 1][tn] = *reinterpret_cast<const v4i*>(stage + at[s] + (wn * WN + tn * 32) * kBlock);
+  };
+  auto read_a = [&](const uint8_t* stage, int s, int tm, bool part) __attribute__((always_inline)) {
+    fa[s & 1][tm] = *reinterpret_cast<const v4i*>(stage + at[s] + (BN + wm * WM + tm * 32) * kBlock);
+    if (kPart && part) fa[s & 1][tm] = keep_valid(fa[s & 1][tm], 2 * s + g, last_bytes);
+  };
+
+  constexpr int kProducts = TN * TM;
+  // refill: kb + STAGES blocks exist; more: a next block exists
+  auto block = [&](int kb, int stage, auto steady) __attribute__((always_inline)) {
+    constexpr bool kSteady = decltype(steady)::value;
+    const int next = stage + 1 == STAGES ? 0 : stage + 1;
+    const uint8_t* here = smem + stage * kStage;
+    const uint8_t* then = smem + next * kStage;
+    const bool part_here = kb == KB - 1, part_then = kb + 1 == KB - 1;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const uint8_t* from = s < 3 ? here : then;  // (after the last block: stale bytes, not used)
+#pragma unroll
+      for (int p = 0; p < kProducts; ++p) {
+        const int tm = p / TN, tn = p % TN;
+        acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[s & 1][tn], fa[s & 1][tm], acc[tn][tm], 0, 0, 0);
+        // the next step's fragments, as early as they fit
+#pragma unroll
+        for (int x = 0; x < TN + TM; ++x)
+          if (x * kProducts / (TN + TM) == p) {
+            if (x < TM) read_a(from, (s + 1) & 3, x, s < 3 ? part_here : part_then);
+            else read_b(from, (s + 1) & 3, x - TM);
+          }
+        if constexpr (kSteady) {
+          if (s == 3)
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j)
+              if (j * kProducts / kCopies == p) issue_piece(stage, kb + STAGES, j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (s == 2) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (kSteady && STAGES > 2) wait_copies_upto<(STAGES - 2) * kCopies>();
+        else wait_copies();
+        lds_barrier();
+      }
+    }
+    return next;
+  };
+
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i)
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) issue_piece(i, min(i, KB - 1), j);
+  wait_copies_upto<(STAGES - 1) * kCopies>();
+  lds_barrier();
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) read_a(smem, 0, tm, KB == 1);
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) read_b(smem, 0, tn);
+  int stage = 0, kb = 0;
+  for (; kb + STAGES < KB; ++kb) stage = block(kb, stage, std::true_type{});
+  for (; kb < KB; ++kb) stage = block(kb, stage, std::false_type{});
+  lds_barrier();  // every wave is done with the stages (no copy is in flight: the last block waited for all)
+
+  for (int i = tid; i < BN; i += kNumWaves * 64) {
+    const int n = min(n0 + i, N - 1);
+    channel[0][i] = args.bs[n];
+    channel[1][i] = args.bias != nullptr ? bias_value<kF16>(args.bias[n]) : 0.f;
+  }
+  __syncthreads();
+
+  // result register v of lane l: weight row 8 (v / 4) + 4 (l / 32) + v % 4, activation row l % 32. Where rows of C allow
+  // it, a wave's 32 rows go through LDS (rows padded by 16 bytes) so that whole segments are stored.
+  constexpr int kRowBytes = WN * 2 + 16;
+  static_assert(kNumWaves * 32 * kRowBytes <= STAGES * kStage, "staged output");
+  uint8_t* staged = smem + w * 32 * kRowBytes;
+  const bool vec16 = (args.ldc & 7) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 15) == 0;
+  const bool vec8 = (args.ldc & 3) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 7) == 0;
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) {
+    const int m = m0 + wm * WM + tm * 32 + r;
+    const float ms = args.as[min(m, M - 1)];
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = tn * 32 + 8 * q + 4 * g, n = n0 + wn * WN + col;
+        const v4f ns = *reinterpret_cast<const v4f*>(&channel[0][wn * WN + col]);
+        const v4f add = *reinterpret_cast<const v4f*>(&channel[1][wn * WN + col]);
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = fmaf((float)acc[tn][tm][4 * q + e] * ms, ns[e], add[e]);
+        const uint32_t p0 = pack16<kF16>(y[0], y[1]), p1 = pack16<kF16>(y[2], y[3]);
+        if (vec16) *reinterpret_cast<uint2*>(staged + r * kRowBytes + col * 2) = make_uint2(p0, p1);
+        else if (m < M && n < N) store4(args.c + (int64_t)m * args.ldc + n, n, N, vec8, p0, p1);
+      }
+    if (!vec16) continue;
+    // (LDS executes a wave's accesses in order; this keeps the compiler to it)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    constexpr int kLanes = WN / 8, kPass = 64 / kLanes;  // lanes a row, rows a pass
+#pragma unroll
+    for (int p = 0; p < 32 / kPass; ++p) {
+      const int row = p * kPass + lane / kLanes, seg = lane % kLanes;
+      const v4i v = *reinterpret_cast<const v4i*>(staged + row * kRowBytes + seg * 16);
+      const int mr = m0 + wm * WM + tm * 32 + row, n = n0 + wn * WN + seg * 8;
+      if (mr < M && n < N) {
+        uint16_t* c = args.c + (int64_t)mr * args.ldc + n;
+        if (n + 8 <= N) {
+          *reinterpret_cast<v4i*>(c) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < N) c[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+  }
+}
+
+template <int TN, int TM, int SLOTS>
+hipError_t ksplit(const Int8GemmArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.N + 16 * TN - 1) / (16 * TN)), (unsigned)((a.M + 16 * TM - 1) / (16 * TM)));
+  if (a.out_f16) hipLaunchKernelGGL((gemm_int8_ksplit_kernel<TN, TM, SLOTS, true>), grid, dim3(kWaves * 64), 0, stream, a);
+  else hipLaunchKernelGGL((gemm_int8_ksplit_kernel<TN, TM, SLOTS, false>), grid, dim3(kWaves * 64), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int BN, int BM, int WGN, int WGM, int STAGES, bool kPart>
+hipError_t tiled_as(const Int8GemmArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)(a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM))), threads(WGN * WGM * 64);
+  if (a.out_f16) hipLaunchKernelGGL((gemm_int8_tiled_kernel<BN, BM, WGN, WGM, STAGES, kPart, true>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((gemm_int8_tiled_kernel<BN, BM, WGN, WGM, STAGES, kPart, false>), grid, threads, 0, stream, a);
+  return hipGetLastError();
+}
+template <int BN, int BM, int WGN, int WGM, int STAGES>
+hipError_t tiled(const Int8GemmArgs& a, hipStream_t stream) {
+  return a.K % kBlock ? tiled_as<BN, BM, WGN, WGM, STAGES, true>(a, stream) : tiled_as<BN, BM, WGN, WGM, STAGES, false>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_int8(const Int8GemmArgs& a, hipStream_t stream) {
+  if (a.M <= 16) return ksplit<1, 1, 4>(a, stream);
+  if (a.M <= 32) return ksplit<1, 2, 2>(a, stream);
+  if (a.M <= 64) return ksplit<2, 2, 2>(a, stream);
+  if (a.M <= 128) return ksplit<4, 2, 1>(a, stream);
+  if (a.M <= 256) return ksplit<4, 4, 1>(a, stream);
+  auto tiles = [&](int64_t bn, int64_t bm) { return ((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm); };
+  if (tiles(256, 256) >= 256) return tiled<256, 256, 2, 4, 2>(a, stream);
+  if (tiles(256, 128) >= 256) return tiled<256, 128, 4, 2, 3>(a, stream);
+  if (tiles(128, 128) >= 256) return tiled<128, 128, 2, 4, 4>(a, stream);
+  return tiled<128, 64, 4, 2, 4>(a, stream);
+}
+
+}  // namespace bfp8

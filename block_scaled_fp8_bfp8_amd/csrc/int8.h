@@ -1,0 +1,30 @@
+// The 8-bit integer products (internal to libbfp8; arguments are validated by the C-ABI layer before any
+// launcher is called).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace bfp8 {
+
+constexpr int kInt8MaxK = 65536;  // a sum of 65536 products of codes stays within 2^30
+
+hipError_t launch_quant_act_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ldq,
+                                 float* s, hipStream_t stream);
+
+struct Int8GemmArgs {
+  const int8_t* a;  // [M][lda] activation codes
+  int64_t lda;
+  const float* as;  // [M] scale of each token
+  const int8_t* b;  // [N][ldb] weight codes
+  int64_t ldb;
+  const float* bs;       // [N] scale of each channel
+  const uint16_t* bias;  // [N] in the output's type, or NULL
+  uint16_t* c;           // [M][ldc] bf16, or fp16 with out_f16
+  int64_t ldc;
+  int M, N, K;
+  bool out_f16;
+};
+hipError_t launch_gemm_int8(const Int8GemmArgs& args, hipStream_t stream);
+
+}  // namespace bfp8

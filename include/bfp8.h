@@ -610,6 +610,40 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
                                              const int32_t* cu_k, int64_t B, float scale, uint16_t* out,
                                              int64_t out_token_stride, int64_t out_head_stride, void* stream);
 
+/*
+ * 8-bit integer products with one scale a token and one a channel ("W8A8" with integer codes):
+ *   C[m, n] = round16((sum_k a[m, k] * b[n, k]) * as[m] * bs[n] + bias[n])
+ * The sum is exact (32-bit integers); it is scaled and biased in float32 and rounded once.
+ *
+ * bfp8_quant_act_int8: for every row m of x [M][ldx] (any BFP8_IN_ type):
+ *   top = max(max_k |x[m, k]|, 1e-10),  s[m] = fl32(top / 127)      (correctly rounded divide)
+ *   q[m, k] = 127 x[m, k] / top to the nearest integer, ties to even (of the exact quotient)
+ * A row with an infinite or NaN element gets a NaN scale and zero codes, so that its products are
+ * NaN. Columns past K are not written. x may not overlap q or s. A weight [N][K] is quantized by
+ * the same call, row by row: its channels are its rows.
+ *   M >= 0, K a multiple of 16, at most 65536; x and q 16-byte aligned, their row strides multiples
+ *   of 16 bytes; s float32 [M]
+ *
+ * bfp8_gemm_int8: a int8 [M][lda], b int8 [N][ldb] (any codes, -128 among them), as float32 [M],
+ * bs float32 [N], bias [N] of the output's type or NULL, c [M][ldc] of out_dtype (BFP8_IN_BF16 or
+ * BFP8_IN_F16). Unlike the FP8 products, rows need not be padded: nothing past K is read.
+ *   K a multiple of 16, at most 65536; a and b 16-byte aligned; lda, ldb multiples of 16, >= K,
+ *   below 2^23
+ *
+ * bfp8_linear_int8: quantizes x [M][ldx] (bf16 or fp16) and multiplies; c has x's type. The
+ * workspace (bfp8_linear_int8_workspace_bytes, 256-byte aligned, contents arbitrary) holds codes
+ * and scales between its launches. Bit-identical to the two calls above.
+ */
+bfp8_status_t bfp8_quant_act_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int8_t* q,
+                                  int64_t ldq, float* s, void* stream);
+bfp8_status_t bfp8_gemm_int8(const int8_t* a, int64_t lda, const float* as, const int8_t* b, int64_t ldb,
+                             const float* bs, const uint16_t* bias, uint16_t* c, int out_dtype, int64_t ldc,
+                             int64_t M, int64_t N, int64_t K, void* stream);
+size_t bfp8_linear_int8_workspace_bytes(int64_t M, int64_t K);
+bfp8_status_t bfp8_linear_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, const int8_t* b,
+                               int64_t ldb, const float* bs, const uint16_t* bias, uint16_t* c, int64_t ldc,
+                               int64_t N, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Process-wide schedule override for bfp8_gemm (tests and benchmarks):
  * BFP8_SCHED_AUTO restores the automatic choice. Returns BFP8_ERR_INVALID_ARGUMENT
  * for an unknown value. The grouped GEMM always uses the tiled schedule. */
