@@ -31,6 +31,7 @@ __all__ = [
     "moe_forward_workspace_bytes", "nn_to_nt_weights", "pad_k", "expand_act_scales", "expand_weight_scale", "set_schedule", "get_schedule", "schedule_for",
     "rmsnorm_quant", "rmsnorm_quant_ue8m0", "latent_cache_write", "latent_cache_read", "latent_cache_gather",
     "latent_attention", "latent_attention_workspace_bytes", "latent_attention_expanded",
+    "latent_attention_mass", "latent_attention_mass_workspace_bytes", "latent_cache_evict",
     "quant_act_int8", "gemm_int8", "linear_int8", "linear_int8_workspace_bytes",
     "abi_version", "BfpError", "LibraryMissing",
 ]
@@ -884,6 +885,17 @@ def rmsnorm_quant_ue8m0(x: torch.Tensor, weight: torch.Tensor, residual: torch.T
     return _rmsnorm_quant(x, weight, residual, eps, out, True)
 
 
+def _call(device: torch.device, name: str, *args):
+    """The C entry `name` on the device of its tensors and that device's current stream (its last argument)."""
+    entry = getattr(_native.lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = entry(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = entry(*args, _stream(device))
+    _check(st, name)
+
+
 LATENT_DIM, ROPE_DIM, LATENT_ROW = 512, 64, 640  # latents, rotary key, bytes of a cache row
 
 
@@ -1085,15 +1097,113 @@ def latent_attention_expanded(q: torch.Tensor, kv: torch.Tensor, rope: torch.Ten
     return out
 
 
-def _call(device: torch.device, name: str, *args):
-    """The C entry `name` on the device of its tensors and that device's current stream (its last argument)."""
-    entry = getattr(_native.lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = entry(*args, _stream(device))
+def latent_attention_mass_workspace_bytes(t: int, b: int, heads: int, max_keys: int) -> int:
+    """Workspace bytes of latent_attention_mass (max_keys: page table width * page size)."""
+    return _native.lib().bfp8_latent_attention_mass_workspace_bytes(t, b, heads, max_keys)
+
+
+def _lens_arg(lens: torch.Tensor, name: str, b: int):
+    _require(lens, name, torch.int32, 1)
+    if lens.shape[0] != b or not lens.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {b} entries")
+
+
+def _mass_arg(mass: torch.Tensor, name: str, b: int, reach: int, width: int | None = None) -> int:
+    """Checks masses [B, columns] and returns their row stride."""
+    _require(mass, name, torch.float32, 2)
+    if mass.shape[0] != b or mass.shape[1] < reach or (width is not None and mass.shape[1] != width):
+        raise ValueError(f"{name} must be [{b}, {reach if width is None else width}{' or more' if width is None else ''}], "
+                         f"got {tuple(mass.shape)}")
+    if mass.shape[1] > 1 and mass.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return mass.stride(0) if b > 1 else mass.shape[1]
+
+
+def latent_attention_mass(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
+                          seq_lens: torch.Tensor, scale: float, mass: torch.Tensor | None = None,
+                          cu_q: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          out_mass: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """latent_attention, and the attention weight that every cached token gathers: returns (out, mass).
+
+    mass float32 [B, S], S at least width * page_size of page_table [B, width], holds the weight that
+    token j of sequence b has gathered so far in column j (None: nothing yet). The mass returned adds to it the
+    weights of all new tokens and heads; tokens that are new in this call start from zero, and columns past a
+    sequence are zero. out_mass: where to put it (it may be mass itself). T == 0 new tokens are
+    allowed (with cu_q). Other arguments as for latent_attention; the workspace is
+    latent_attention_mass_workspace_bytes."""
+    _require(q, "q", torch.bfloat16, 3)
+    t, heads, dim = q.shape
+    if dim != LATENT_DIM + ROPE_DIM or q.stride(2) != 1:
+        raise ValueError(f"q must be [T, H, {LATENT_DIM + ROPE_DIM}] with contiguous rows, got {tuple(q.shape)}")
+    rows, ps, sc, ss, pages, page = _latent_cache_args(cache, scales)
+    table, ts, width = _page_table_args(page_table)
+    b, reach = page_table.shape[0], width * page
+    _lens_arg(seq_lens, "seq_lens", b)
+    if cu_q is not None:
+        _starts_arg(cu_q, "cu_q", b)
+    elif t != b:
+        raise ValueError(f"without cu_q every sequence has one query token, got {t} tokens and {b} sequences")
+    if out is None:
+        out = torch.empty((t, heads, LATENT_DIM), dtype=torch.bfloat16, device=q.device)
     else:
-        with torch.cuda.device(device):
-            st = entry(*args, _stream(device))
-    _check(st, name)
+        _require(out, "out", torch.bfloat16, 3)
+        if out.shape != (t, heads, LATENT_DIM) or out.stride(2) != 1:
+            raise ValueError(f"out must be [{t}, {heads}, {LATENT_DIM}] with contiguous rows")
+    columns = reach if mass is None and out_mass is None else (out_mass if mass is None else mass).shape[-1]
+    in_stride = columns if mass is None else _mass_arg(mass, "mass", b, reach)
+    if out_mass is None:
+        out_mass = torch.empty((b, columns), dtype=torch.float32, device=q.device)
+    out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
+    _same_device(q, cache=cache, page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, out=out, mass=mass,
+                 out_mass=out_mass, workspace=workspace)
+    if workspace is None:
+        ws_ptr, ws_bytes, workspace = _workspace(q.device, latent_attention_mass_workspace_bytes(t, b, heads, reach))
+    else:
+        _require(workspace, "workspace", torch.uint8, 1)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _call(q.device, "bfp8_latent_attention_mass", q.data_ptr(), t, heads, q.stride(0), q.stride(1), rows, ps, sc, ss, pages,
+          page, table, ts, width, seq_lens.data_ptr(), b, None if cu_q is None else cu_q.data_ptr(), scale, out.data_ptr(),
+          out.stride(0), out.stride(1), None if mass is None else mass.data_ptr(), in_stride, out_mass.data_ptr(),
+          out_stride, columns, ws_ptr or None, ws_bytes)
+    return out, out_mass
+
+
+def latent_cache_evict(cache: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                       mass: torch.Tensor, budget: int, recent: int = 0, out_table: torch.Tensor | None = None,
+                       out_mass: torch.Tensor | None = None):
+    """Cut sequences of the latent cache down to `budget` tokens each: a longer one keeps its last
+    `recent` tokens and, of the earlier ones, those with the largest mass (float32 [B, S] as
+    latent_attention_mass returns it; NaN above all, of equal ones the earlier), in their order.
+
+    Returns (kept int32 [B, budget], lens int32 [B], mass [B, S]): which token became token i of its
+    sequence (-1 past its new length), the new lengths, and the kept tokens' masses in their new places. Rows
+    and scale codes move within the sequence's pages, none of which may appear twice in page_table;
+    or, with out_table (int32 [B, width], pages that are not in page_table), onto those, and the old pages
+    are left as they are. out_mass: where to put the masses (it may be mass itself). Lengths are read on
+    the GPU: nothing here waits for them."""
+    rows, ps, sc, ss, pages, page = _latent_cache_args(cache, scales)
+    table, ts, width = _page_table_args(page_table)
+    b, reach = page_table.shape[0], width * page
+    _lens_arg(seq_lens, "seq_lens", b)
+    in_stride = _mass_arg(mass, "mass", b, reach)
+    columns = mass.shape[1]
+    if budget < 1 or not 0 <= recent <= budget:
+        raise ValueError(f"budget must be at least 1 and recent 0 .. budget, got {budget} and {recent}")
+    to, to_stride, to_width = None, 0, 0
+    if out_table is not None:
+        to, to_stride, to_width = _page_table_args(out_table)
+        if out_table.shape[0] != b or to_width == 0:
+            raise ValueError(f"out_table must have {b} rows of pages, got shape {tuple(out_table.shape)}")
+    if out_mass is None:
+        out_mass = torch.empty((b, columns), dtype=torch.float32, device=cache.device)
+    out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
+    _same_device(cache, page_table=page_table, seq_lens=seq_lens, mass=mass, out_table=out_table, out_mass=out_mass)
+    kept = torch.empty((b, budget), dtype=torch.int32, device=cache.device)
+    lens = torch.empty((b,), dtype=torch.int32, device=cache.device)
+    _call(cache.device, "bfp8_latent_cache_evict", rows, ps, sc, ss, pages, page, table, ts, width, seq_lens.data_ptr(), b,
+          mass.data_ptr(), in_stride, columns, budget, recent, to, to_stride, to_width, kept.data_ptr(), lens.data_ptr(),
+          out_mass.data_ptr(), out_stride)
+    return kept, lens, out_mass
 
 
 def _int8_scales(s: torch.Tensor, name: str, n: int):

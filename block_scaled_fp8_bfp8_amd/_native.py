@@ -83,6 +83,13 @@ SIGNATURES = [
     ("bfp8_latent_attention_expanded", ctypes.c_int,
      [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, ctypes.c_float, _vp, _i64,
       _i64, _vp]),
+    ("bfp8_latent_attention_mass_workspace_bytes", _sz, [_i64, _i64, _i64, _i64]),
+    ("bfp8_latent_attention_mass", ctypes.c_int,
+     [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, ctypes.c_float,
+      _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _sz, _vp]),
+    ("bfp8_latent_cache_evict", ctypes.c_int,
+     [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp,
+      _vp, _i64, _vp]),
     ("bfp8_quant_act_int8", ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
     ("bfp8_gemm_int8", ctypes.c_int,
      [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp]),

@@ -7,6 +7,7 @@
 // contract of page "prhub.com.cn ... vllm/pull/49932", section "实现拆解" item 2).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -1137,6 +1138,132 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
   args.scale = scale;
   return launched(bfp8::launch_latent_expanded(args, dtype == BFP8_IN_F16, (hipStream_t)stream),
                   "latent_attention_expanded");
+}
+
+}  // extern "C"
+
+namespace {
+
+// The arguments that both entries of the bounded cache share.
+bfp8_status_t check_mass(int64_t B, int64_t page_size, int64_t table_width, const int32_t* lens, int64_t width,
+                         const float* mass_in, int64_t in_stride, const float* mass_out, int64_t out_stride) {
+  if (B > (int64_t)1 << 24) return fail(BFP8_ERR_UNSUPPORTED, "more than 2^24 sequences");
+  if (table_width > 0 && page_size > INT32_MAX / table_width)
+    return fail(BFP8_ERR_UNSUPPORTED, "a page table reaches 2^31 tokens or more");
+  if (!lens) return fail(BFP8_ERR_INVALID_ARGUMENT, "seq_lens must not be NULL");
+  if (width < table_width * page_size)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "mass has %lld columns, the page table reaches %lld tokens", (long long)width,
+                (long long)(table_width * page_size));
+  if (width > INT32_MAX - 65536) return fail(BFP8_ERR_UNSUPPORTED, "mass has 2^31 columns or more");
+  if (width > 0 && !mass_out) return fail(BFP8_ERR_INVALID_ARGUMENT, "the masses must not be NULL");
+  if (B > 1 && (out_stride < width || (mass_in && in_stride < width)))
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "strides of the masses must be at least %lld", (long long)width);
+  if (!aligned(mass_in, 4) || !aligned(mass_out, 4) || !aligned(lens, 4))
+    return fail(BFP8_ERR_MISALIGNED, "masses and lengths must be 4-byte aligned");
+  return BFP8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bfp8_latent_attention_mass_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t max_keys) {
+  if (T < 1 || B < 1 || H < 1 || max_keys < 0 || T > kMaxDim || B > kMaxDim || T > kMaxDim / H || max_keys > INT32_MAX)
+    return 0;
+  const bfp8::LatentMassPlan p = bfp8::plan_latent_mass(T, H, max_keys);
+  return (bfp8_latent_attention_workspace_bytes(T, B, H, max_keys) + 255) / 256 * 256 + p.parts_bytes + p.lse_bytes;
+}
+
+bfp8_status_t bfp8_latent_attention_mass(const uint16_t* q, int64_t T, int64_t H, int64_t q_token_stride,
+                                         int64_t q_head_stride, const uint8_t* rows, int64_t page_stride,
+                                         const uint8_t* scales, int64_t scale_stride, int64_t pages,
+                                         int64_t page_size, const int32_t* page_table, int64_t table_stride,
+                                         int64_t table_width, const int32_t* seq_lens, int64_t B, const int32_t* cu_q,
+                                         float scale, uint16_t* out, int64_t out_token_stride, int64_t out_head_stride,
+                                         const float* mass_in, int64_t mass_in_stride, float* mass_out,
+                                         int64_t mass_out_stride, int64_t width, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  if (B < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "B = %lld is negative", (long long)B);
+  if (T < 0 || H < 1)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "T = %lld must not be negative and H = %lld must be >= 1", (long long)T, (long long)H);
+  if (T > kMaxDim || H > kMaxDim || T > kMaxDim / H)
+    return fail(BFP8_ERR_UNSUPPORTED, "T x H = %lld x %lld has more than 2^30 query rows", (long long)T, (long long)H);
+  if (T == 0 && B == 0) return ok();
+  bfp8_status_t st = check_latent_cache(rows, scales, pages, page_size, page_stride, scale_stride);
+  if (st == BFP8_OK) st = check_page_table(page_table, B, table_stride, table_width);
+  if (st == BFP8_OK) st = check_mass(B, page_size, table_width, seq_lens, width, mass_in, mass_in_stride, mass_out, mass_out_stride);
+  if (st != BFP8_OK) return st;
+  if (!cu_q && T != B)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "without cu_q every sequence has one query token: T = %lld, B = %lld",
+                (long long)T, (long long)B);
+  if (!aligned(cu_q, 4)) return fail(BFP8_ERR_MISALIGNED, "cu_q must be 4-byte aligned");
+  const int64_t max_keys = table_width * page_size;
+  const size_t need = bfp8_latent_attention_mass_workspace_bytes(T, B, H, max_keys);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(BFP8_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  if (need > 0 && !aligned(workspace, 256)) return fail(BFP8_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  // (checks the rest before it launches)
+  st = bfp8_latent_attention(q, T, H, q_token_stride, q_head_stride, rows, page_stride, scales, scale_stride, pages,
+                             page_size, page_table, table_stride, table_width, seq_lens, B, cu_q, scale, out,
+                             out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
+  if (st == BFP8_OK && T == 0) st = check_device();
+  if (st != BFP8_OK) return st;
+  const bfp8::LatentMassPlan plan = bfp8::plan_latent_mass(T, H, max_keys);
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + (bfp8_latent_attention_workspace_bytes(T, B, H, max_keys) + 255) / 256 * 256;
+  bfp8::LatentMassArgs args{};
+  args.q = q;
+  args.q_tok = q_token_stride;
+  args.q_head = q_head_stride;
+  args.cache =
+      latent_cache(rows, page_stride, scales, scale_stride, pages, page_size, page_table, table_stride, table_width);
+  args.lens = seq_lens;
+  args.cu_q = cu_q;
+  args.T = (int)T;
+  args.B = (int)B;
+  args.H = (int)H;
+  args.scale = scale;
+  args.mass_in = mass_in;
+  args.in_stride = mass_in_stride;
+  args.mass = mass_out;
+  args.out_stride = mass_out_stride;
+  args.width = (int)width;
+  if (T > 0) {
+    args.parts = reinterpret_cast<float2*>(ws);
+    args.lse = reinterpret_cast<float*>(ws + plan.parts_bytes);
+  }
+  return launched(bfp8::launch_latent_mass(args, (hipStream_t)stream), "latent_attention_mass");
+}
+
+bfp8_status_t bfp8_latent_cache_evict(uint8_t* rows, int64_t page_stride, uint8_t* scales, int64_t scale_stride,
+                                      int64_t pages, int64_t page_size, const int32_t* page_table, int64_t table_stride,
+                                      int64_t table_width, const int32_t* seq_lens, int64_t B, const float* mass,
+                                      int64_t mass_stride, int64_t width, int64_t budget, int64_t recent,
+                                      const int32_t* out_table, int64_t out_table_stride, int64_t out_table_width,
+                                      int32_t* kept, int32_t* lens_out, float* mass_out, int64_t mass_out_stride,
+                                      void* stream) {
+  if (B < 0) return fail(BFP8_ERR_INVALID_ARGUMENT, "B = %lld is negative", (long long)B);
+  if (budget < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "budget = %lld must be >= 1", (long long)budget);
+  if (recent < 0 || recent > budget)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "recent = %lld must be 0 .. budget = %lld", (long long)recent, (long long)budget);
+  if (budget > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "budget must be at most 2^30");
+  if (B == 0) return ok();
+  bfp8_status_t st = check_latent_cache(rows, scales, pages, page_size, page_stride, scale_stride);
+  if (st == BFP8_OK) st = check_page_table(page_table, B, table_stride, table_width);
+  if (st == BFP8_OK && out_table) st = check_page_table(out_table, B, out_table_stride, out_table_width);
+  if (st == BFP8_OK) st = check_mass(B, page_size, table_width, seq_lens, width, mass, mass_stride, mass_out, mass_out_stride);
+  if (st != BFP8_OK) return st;
+  if (width > 0 && !mass) return fail(BFP8_ERR_INVALID_ARGUMENT, "the masses must not be NULL");
+  if (!kept || !lens_out) return fail(BFP8_ERR_INVALID_ARGUMENT, "kept and lens_out must not be NULL");
+  if (!aligned(kept, 4) || !aligned(lens_out, 4)) return fail(BFP8_ERR_MISALIGNED, "kept and lens_out must be 4-byte aligned");
+  if (mass == mass_out && B > 1 && mass_stride != mass_out_stride)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "masses updated in place have one stride");
+  st = check_device();
+  if (st != BFP8_OK) return st;
+  const bfp8::LatentEvictArgs args{
+      latent_cache(rows, page_stride, scales, scale_stride, pages, page_size, page_table, table_stride, table_width),
+      rows, scales, out_table, out_table_stride, (int)std::min<int64_t>(out_table_width, INT32_MAX), seq_lens, mass,
+      mass_stride, (int)width, (int)B, (int)budget, (int)recent, kept, lens_out, mass_out, mass_out_stride};
+  return launched(bfp8::launch_latent_evict(args, (hipStream_t)stream), "latent_cache_evict");
 }
 
 }  // extern "C"

@@ -79,4 +79,48 @@ struct LatentExpandedArgs {
 int64_t latent_expanded_blocks(int64_t Tq, int64_t B);
 hipError_t launch_latent_expanded(const LatentExpandedArgs& args, bool f16, hipStream_t stream);
 
+// Accumulated attention weights of cached tokens. Strides in elements.
+struct LatentMassArgs {
+  const uint16_t* q;  // [T][H][576] bf16
+  int64_t q_tok, q_head;
+  LatentCache cache;
+  const int32_t* lens;  // as in LatentAttnArgs
+  const int32_t* cu_q;
+  int T, B, H;
+  float scale;
+  const float* mass_in;  // [B][in_stride], or NULL: zeros
+  int64_t in_stride;
+  float* mass;  // [B][out_stride]
+  int64_t out_stride;
+  int width;      // columns of mass that are written, at least the page table's reach
+  int each;       // workgroups a sequence (set by the launch)
+  float2* parts;  // workspace [blocks][T * H]: maximum and sum of a row over a block of keys
+  float* lse;     // workspace [T * H]: log2 of a row's sum, infinity where it sees no key
+};
+struct LatentMassPlan {
+  size_t parts_bytes, lse_bytes;
+};
+LatentMassPlan plan_latent_mass(int64_t T, int64_t H, int64_t max_keys);
+hipError_t launch_latent_mass(const LatentMassArgs& args, hipStream_t stream);
+
+// Eviction by accumulated weight.
+struct LatentEvictArgs {
+  LatentCache cache;  // its table names the pages that tokens lie on
+  uint8_t* rows;      // the same cache, to write
+  uint8_t* scales;
+  const int32_t* to;  // [B][to_stride] pages the kept tokens go to, or NULL: in place
+  int64_t to_stride;
+  int to_width;
+  const int32_t* lens;
+  const float* mass;
+  int64_t mass_stride;
+  int width;  // columns of mass
+  int B, budget, recent;
+  int32_t* kept;  // [B][budget]
+  int32_t* lens_out;
+  float* mass_out;  // [B][mass_out_stride]; may be mass
+  int64_t mass_out_stride;
+};
+hipError_t launch_latent_evict(const LatentEvictArgs& args, hipStream_t stream);
+
 }  // namespace bfp8

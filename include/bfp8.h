@@ -611,6 +611,59 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
                                              int64_t out_token_stride, int64_t out_head_stride, void* stream);
 
 /*
+ * A cache of bounded length. mass [B][mass_stride] (float32) holds the attention weight that each
+ * token of each sequence has gathered so far, column j that of the sequence's token j (not of a
+ * cache slot: sequences may share pages).
+ *
+ * bfp8_latent_attention_mass: bfp8_latent_attention (same arguments, same out), and
+ *   mass_out[b][j] = mass_in[b][j] + sum over the sequence's new tokens t and heads h of
+ *                    softmax_j(scale * q[t, h] . [c_j, r_j])
+ * for the tokens j that were there before, the sum alone for those that are new in this call, and
+ * 0 in the columns past the sequence. The weights are those of exact products of q with the cached
+ * values, in float32 throughout. A row that is NaN (see bfp8_latent_attention) adds NaN to the
+ * tokens it sees.
+ *   mass_in   NULL: zeros; may be mass_out
+ *   width     columns of mass_in and mass_out, at least table_width * page_size
+ *   T == 0    is allowed: mass_in is copied, with zeros past each sequence
+ *   workspace bfp8_latent_attention_mass_workspace_bytes bytes, 256-byte aligned: that of
+ *             bfp8_latent_attention, then 8 bytes for every query row and 128 keys of
+ *             table_width * page_size, and 4 a query row
+ *
+ * bfp8_latent_cache_evict: a sequence longer than `budget` keeps its last `recent` tokens and, of
+ * the earlier ones, the budget - recent with the largest mass (NaN above all others, of equal ones
+ * the earlier), in their order, as its tokens 0 .. budget - 1; a shorter one keeps all.
+ *   kept      int32 [B][budget]: which token became token i, -1 past the new length
+ *   lens_out  int32 [B]: the new lengths; may be seq_lens
+ *   mass_out  the masses of the kept tokens in their new places, then zeros up to `width`; may be
+ *             mass (then with its stride)
+ *   out_table NULL: tokens move within their own pages, of which no page may appear twice in the
+ *             call's tables (pages past the new length are then free). Or int32
+ *             [B][out_table_stride]: every kept token goes to out_table_width pages of its own,
+ *             none of them a page of page_table, and the old pages are left as they are (they may
+ *             be shared with other sequences). A token whose new page is not one of the cache is
+ *             not stored; one whose old page is not reads as NaN there.
+ *   budget    >= 1, recent 0 .. budget; lengths past table_width * page_size count as that
+ *   width     columns of mass and mass_out, at least table_width * page_size
+ */
+size_t bfp8_latent_attention_mass_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t max_keys);
+bfp8_status_t bfp8_latent_attention_mass(const uint16_t* q, int64_t T, int64_t H, int64_t q_token_stride,
+                                         int64_t q_head_stride, const uint8_t* rows, int64_t page_stride,
+                                         const uint8_t* scales, int64_t scale_stride, int64_t pages,
+                                         int64_t page_size, const int32_t* page_table, int64_t table_stride,
+                                         int64_t table_width, const int32_t* seq_lens, int64_t B, const int32_t* cu_q,
+                                         float scale, uint16_t* out, int64_t out_token_stride, int64_t out_head_stride,
+                                         const float* mass_in, int64_t mass_in_stride, float* mass_out,
+                                         int64_t mass_out_stride, int64_t width, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+bfp8_status_t bfp8_latent_cache_evict(uint8_t* rows, int64_t page_stride, uint8_t* scales, int64_t scale_stride,
+                                      int64_t pages, int64_t page_size, const int32_t* page_table, int64_t table_stride,
+                                      int64_t table_width, const int32_t* seq_lens, int64_t B, const float* mass,
+                                      int64_t mass_stride, int64_t width, int64_t budget, int64_t recent,
+                                      const int32_t* out_table, int64_t out_table_stride, int64_t out_table_width,
+                                      int32_t* kept, int32_t* lens_out, float* mass_out, int64_t mass_out_stride,
+                                      void* stream);
+
+/*
  * 8-bit integer products with one scale a token and one a channel ("W8A8" with integer codes):
  *   C[m, n] = round16((sum_k a[m, k] * b[n, k]) * as[m] * bs[n] + bias[n])
  * The sum is exact (32-bit integers); it is scaled and biased in float32 and rounded once.
