@@ -1170,8 +1170,8 @@ extern "C" {
 size_t bfp8_latent_attention_mass_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t max_keys) {
   if (T < 1 || B < 1 || H < 1 || max_keys < 0 || T > kMaxDim || B > kMaxDim || T > kMaxDim / H || max_keys > INT32_MAX)
     return 0;
-  const bfp8::LatentMassPlan p = bfp8::plan_latent_mass(T, H, max_keys);
-  return (bfp8_latent_attention_workspace_bytes(T, B, H, max_keys) + 255) / 256 * 256 + p.parts_bytes + p.lse_bytes;
+  const bfp8::LatentMassPlan p = bfp8::plan_latent_mass(T, B, H, max_keys);
+  return (bfp8_latent_attention_workspace_bytes(T, B, H, max_keys) + 255) / 256 * 256 + p.first_bytes + p.stats_bytes + p.rest_bytes;
 }
 
 bfp8_status_t bfp8_latent_attention_mass(const uint16_t* q, int64_t T, int64_t H, int64_t q_token_stride,
@@ -1208,30 +1208,37 @@ bfp8_status_t bfp8_latent_attention_mass(const uint16_t* q, int64_t T, int64_t H
                              out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
   if (st == BFP8_OK && T == 0) st = check_device();
   if (st != BFP8_OK) return st;
-  const bfp8::LatentMassPlan plan = bfp8::plan_latent_mass(T, H, max_keys);
+  const bfp8::LatentMassPlan plan = bfp8::plan_latent_mass(T, B, H, max_keys);
   uint8_t* ws = static_cast<uint8_t*>(workspace) + (bfp8_latent_attention_workspace_bytes(T, B, H, max_keys) + 255) / 256 * 256;
   bfp8::LatentMassArgs args{};
-  args.q = q;
-  args.q_tok = q_token_stride;
-  args.q_head = q_head_stride;
-  args.cache =
+  args.work.q = q;
+  args.work.q_tok = q_token_stride;
+  args.work.q_head = q_head_stride;
+  args.work.cache =
       latent_cache(rows, page_stride, scales, scale_stride, pages, page_size, page_table, table_stride, table_width);
-  args.lens = seq_lens;
-  args.cu_q = cu_q;
-  args.T = (int)T;
-  args.B = (int)B;
-  args.H = (int)H;
-  args.scale = scale;
+  args.work.lens = seq_lens;
+  args.work.cu_q = cu_q;
+  args.work.T = (int)T;
+  args.work.B = (int)B;
+  args.work.H = (int)H;
+  args.work.scale = scale;
+  args.work.target_parts = args.work.max_slots = plan.target_parts;
+  args.work.min_tiles = plan.min_tiles;
+  args.work.max_tiles = plan.max_tiles;
   args.mass_in = mass_in;
   args.in_stride = mass_in_stride;
   args.mass = mass_out;
   args.out_stride = mass_out_stride;
   args.width = (int)width;
+  args.ids = (int)plan.ids;
+  args.pitch = plan.pitch;
   if (T > 0) {
-    args.parts = reinterpret_cast<float2*>(ws);
-    args.lse = reinterpret_cast<float*>(ws + plan.parts_bytes);
+    args.first = reinterpret_cast<int2*>(ws);
+    args.stats = reinterpret_cast<float2*>(ws + plan.first_bytes);
+    float* rest = reinterpret_cast<float*>(ws + plan.first_bytes + plan.stats_bytes);
+    (plan.keeps_scores ? args.scores : args.partial) = rest;
   }
-  return launched(bfp8::launch_latent_mass(args, (hipStream_t)stream), "latent_attention_mass");
+  return launched(bfp8::launch_latent_mass(args, plan, (hipStream_t)stream), "latent_attention_mass");
 }
 
 bfp8_status_t bfp8_latent_cache_evict(uint8_t* rows, int64_t page_stride, uint8_t* scales, int64_t scale_stride,

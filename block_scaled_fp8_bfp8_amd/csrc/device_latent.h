@@ -107,4 +107,19 @@ __device__ __forceinline__ float wave_max(float v) {
   return wave_fold(v, [](float a, float b) { return max_nan(a, b); });
 }
 
+// f(Const<0>) .. f(Const<kCount - 1>).
+template <int kCount, typename F>
+__device__ __forceinline__ void static_for(F f) {
+  if constexpr (kCount > 0) {
+    static_for<kCount - 1>(f);
+    f(Const<kCount - 1>{});
+  }
+}
+// copy16_m0 of the bytes kOffset further on. The instruction's offset counts for both addresses: `lds` lies that
+// much before the destination.
+template <int kOffset>
+__device__ __forceinline__ void copy16_block(const uint8_t* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off offset:%2" : : "v"(src), "s"(lds), "n"(kOffset) : "memory");
+}
+
 }  // namespace bfp8

@@ -79,29 +79,30 @@ struct LatentExpandedArgs {
 int64_t latent_expanded_blocks(int64_t Tq, int64_t B);
 hipError_t launch_latent_expanded(const LatentExpandedArgs& args, bool f16, hipStream_t stream);
 
-// Accumulated attention weights of cached tokens. Strides in elements.
+// Accumulated attention weights of cached tokens.
 struct LatentMassArgs {
-  const uint16_t* q;  // [T][H][576] bf16
-  int64_t q_tok, q_head;
-  LatentCache cache;
-  const int32_t* lens;  // as in LatentAttnArgs
-  const int32_t* cu_q;
-  int T, B, H;
-  float scale;
+  LatentAttnArgs work;   // the rows, the keys and how the work is cut (out, counts, stats and states are not used)
   const float* mass_in;  // [B][in_stride], or NULL: zeros
   int64_t in_stride;
   float* mass;  // [B][out_stride]
   int64_t out_stride;
-  int width;      // columns of mass that are written, at least the page table's reach
-  int each;       // workgroups a sequence (set by the launch)
-  float2* parts;  // workspace [blocks][T * H]: maximum and sum of a row over a block of keys
-  float* lse;     // workspace [T * H]: log2 of a row's sum, infinity where it sees no key
+  int width;        // columns of mass that are written, at least the page table's reach
+  int each;         // workgroups a sequence of the last launch (set by the launch)
+  int ids;          // parts of all blocks, at most
+  int2* first;      // workspace [B]: of a sequence's first block the first part, and its parts
+  float2* stats;    // workspace [ids][128]: maximum and sum of the rows of a part
+  float* scores;    // workspace [T * H][pitch]: scores times log2(e)
+  float* partial;   // workspace [T * H / 128 + B + 1][pitch]: weights summed over a block of rows
+  int64_t pitch;
 };
 struct LatentMassPlan {
-  size_t parts_bytes, lse_bytes;
+  int target_parts, min_tiles, max_tiles;
+  int64_t ids, pitch;
+  bool keeps_scores;
+  size_t first_bytes, stats_bytes, rest_bytes;
 };
-LatentMassPlan plan_latent_mass(int64_t T, int64_t H, int64_t max_keys);
-hipError_t launch_latent_mass(const LatentMassArgs& args, hipStream_t stream);
+LatentMassPlan plan_latent_mass(int64_t T, int64_t B, int64_t H, int64_t max_keys);
+hipError_t launch_latent_mass(LatentMassArgs args, const LatentMassPlan& plan, hipStream_t stream);
 
 // Eviction by accumulated weight.
 struct LatentEvictArgs {

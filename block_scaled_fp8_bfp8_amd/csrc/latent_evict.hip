@@ -40,6 +40,14 @@ __device__ __forceinline__ Length length_of(const LatentEvictArgs& a, int b) {
   return {n, min(n, a.budget)};
 }
 
+// Sum over 16 lanes, in the last of them.
+__device__ __forceinline__ int sum16(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // 1, 2, 4, 8 lanes up
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+}
+
 // The masses are read a chunk at a time, thread t's i-th of a chunk being token 1024 i + t of it.
 __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs a) {
   __shared__ int wave_sums[2][kHeld][kSelectWaves];
@@ -54,6 +62,13 @@ __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs
   const int old = cut ? n - a.recent : n;  // tokens that may go
   const int want = len.kept - (n - old);   // of these stay
 
+  float first[kHeld];  // masses of the first chunk
+  const int held_chunks = min((n + kThreads - 1) / kThreads, kHeld);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int j = i * kThreads + tid;
+    first[i] = j < n ? mass[j] : 0.f;
+  }
   uint32_t least = 0;  // the least mass that stays, as an integer (0: all stay), and how many of those that equal it
   int equals = 0;
   if (cut && want == 0) least = 0xffffffffu;
@@ -61,8 +76,7 @@ __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs
     uint32_t held[kHeld];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const int j = i * kThreads + tid;
-      held[i] = j < old ? rising(mass[j]) : 0u;
+      held[i] = i * kThreads + tid < old ? rising(first[i]) : 0u;
     }
     int above = 0;  // masses above every value that starts with the bits found so far
     for (int shift = 30; shift >= 0; shift -= 2) {
@@ -72,7 +86,8 @@ __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs
         for (uint32_t k = 0; k < 3; ++k) c[k] += __popcll(__ballot(u >= (least | (k + 1) << shift)));
       };
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) count(held[i]);
+      for (int i = 0; i < kHeld; ++i)
+        if (i < held_chunks) count(held[i]);  // (uniform)
       for (int j0 = kChunk; j0 < old; j0 += kThreads) count(j0 + tid < old ? rising(mass[j0 + tid]) : 0u);
       const int turn = (shift >> 1) & 1;
       if (lane == 0)
@@ -81,12 +96,9 @@ __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs
       __syncthreads();
       int total[3];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        int v = counts[turn][k][lane & (kSelectWaves - 1)];
+      for (int k = 0; k < 3; ++k) total[k] = counts[turn][k][lane & (kSelectWaves - 1)];
 #pragma unroll
-        for (int mask = 1; mask < kSelectWaves; mask <<= 1) v += __shfl_xor(v, mask);
-        total[k] = v;
-      }
+      for (int k = 0; k < 3; ++k) total[k] = __builtin_amdgcn_readlane(sum16(total[k]), 15);
       // the largest candidate that `want` masses reach
       const int k = total[2] >= want ? 3 : total[1] >= want ? 2 : total[0] >= want ? 1 : 0;
       if (k < 3) above = total[k];
@@ -104,7 +116,7 @@ __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int j = j0 + i * kThreads + tid;
-      m[i] = j < n ? mass[j] : 0.f;
+      m[i] = j0 == 0 ? first[i] : j < n ? mass[j] : 0.f;
       const uint32_t u = rising(m[i]);
       const bool may_go = j < old && cut;
       same[i] = may_go && u == least && want > 0;

@@ -1,297 +1,416 @@
 // Accumulated attention weights of the tokens in the paged FP8 latent cache:
 //   mass[b, j] += sum over new tokens t and heads h of softmax_j(scale q[t, h] . [c_j, r_j])
 //
-// A weight needs its row's maximum and sum over all keys first, so keys are scored twice: a first launch leaves each
-// row's maximum and sum over every block of 128 keys, a second joins them, and a third forms the weights and adds them
-// up over the rows. Scores are bf16 products on the cached codes, which bf16 holds exactly (32x32x16 instructions,
-// latents and rotary part in accumulators of their own, as the key's scale belongs to the first alone), so a weight is
-// off by float32 roundings only: the sums of thousands of weights stay good to 1e-5 or better.
+// A weight needs its row's maximum and sum over all keys first. A first launch scores the keys and leaves each row's
+// maximum and sum over a part of the keys. A second forms the weights and adds them up over the rows: from the scores,
+// where the first launch had room to leave them too, else by scoring the keys again, whose sums over blocks of 128 rows a
+// third launch then adds up. Nothing is added by atomics: results do not depend on the order of the workgroups.
 //
-// A wave holds 32 keys in registers and walks the query rows of their sequence in tiles of 32, which the waves of a
-// workgroup share through LDS (9 blocks of 128 bytes a row, columns XORed by the row: no bank conflicts). One
-// instruction serves both directions: with the keys as its second operand a lane holds one key and 16 rows, so that
-// their weights add up in registers (no atomics: one wave owns a key); with the keys first a lane holds one row and 16
-// keys, whose maximum and sum are as near.
+// Scores are bf16 products on the cached codes, which bf16 holds exactly (32x32x16 instructions, latents and
+// rotary part in accumulators of their own, as the key's scale belongs to the first alone), so a weight is off by float32
+// roundings only: the sums of thousands of weights stay good to 1e-5 or better.
+//
+// A workgroup holds 128 query rows of one sequence, 32 a wave, in registers and walks tiles of 32 keys, of which two are on
+// their way to LDS while a third is multiplied (the layout is that of the attention kernel, without bank conflicts). Where
+// the keys of its part lie is looked up before, 2048 at a time, so that the loop holds no dependent load. One
+// instruction serves both directions: with the keys first a lane holds one row and 16 keys, whose maximum and sum are near;
+// with the rows first it holds one key and 16 rows, whose weights add up in registers. Two workgroups run on a compute unit,
+// so that one's softmax and conversions (128 instructions a tile) run beside the other's products.
 #include <algorithm>
 
 #include "device_latent.h"
 #include "latent.h"
+#include "latent_work.h"
 #include "launch.h"
 
 namespace bfp8 {
 
 namespace {
 
-constexpr int kKeys = 128;                 // of a workgroup: 4 groups of 32
-constexpr int kRowsTile = 32;
-constexpr int kTileBytes = 9 * kRowsTile * 128;
+constexpr int kRows = 128;  // of a block
+constexpr int kTile = 32;   // keys
+// A tile in LDS: groups of 8 rows, each in 5 blocks of 128 bytes of every row and 64 bytes of padding; of each 64 bytes the
+// 16-byte columns are XORed with bits 2 and 1 of the row.
+constexpr int kBlockBytes = 8 * 128, kGroupBytes = 5 * kBlockBytes + 64;
+constexpr int kTileBytes = 4 * kGroupBytes;
+constexpr int kBuffers = 3;
+constexpr int kMap = 2048;  // keys that are looked up at a time
+constexpr float kNone = -1e30f;
 constexpr float kNegInf = -__builtin_inff();
+constexpr uint32_t kNowhere = 0xffffffffu;
 
 // The row that a key without a page stands on.
 __device__ const uint4 kNoRow[kLatentRow / 16] = {};
 
-// Sequence b: its new tokens, its length, and how many of its keys the page table reaches (a row that sees one past
-// that is NaN).
-struct Seq {
-  int q0, n, len, reach;
-};
-__device__ __forceinline__ Seq sequence(const LatentMassArgs& a, int b) {
-  Seq s{b, 1, 0, 0};
-  if (a.cu_q != nullptr) {
-    s.q0 = min(max(a.cu_q[b], 0), a.T);
-    s.n = max(min(max(a.cu_q[b + 1], 0), a.T) - s.q0, 0);
-  }
-  s.len = max(a.lens[b], 0);
-  s.reach = min(s.len, a.cache.table_width * a.cache.page_size);  // (below 2^31)
-  return s;
-}
-// The keys that token `tok` of its new ones sees.
+// The keys that token `tok` of a sequence's new ones sees, and how many the page table reaches (a row that sees one past that is NaN).
 __device__ __forceinline__ int sees(const Seq& s, int tok) { return min(max(s.len - s.n + tok + 1, 0), s.len); }
+__device__ __forceinline__ int reach_of(const LatentAttnArgs& a) { return a.cache.table_width * a.cache.page_size; }  // (below 2^31)
 
 // 8 codes as bf16, exactly.
-__device__ __forceinline__ v8bf codes_bf16(uint32_t lo, uint32_t hi) {
-  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-  const v2bf x[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true),
-                     __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true)};
-  return v8bf{x[0][0], x[0][1], x[1][0], x[1][1], x[2][0], x[2][1], x[3][0], x[3][1]};
+__device__ __forceinline__ v8bf codes_bf16(int lo, int hi) {
+  auto two = [](auto v) { return __builtin_bit_cast(int, v); };
+  return __builtin_bit_cast(v8bf, v4i{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false)),
+                                      two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true)),
+                                      two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false)),
+                                      two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true))});
 }
 
-// kHalves groups of 4 waves take the tiles of rows in turn. kMass: weights (the third launch), else maxima and sums.
-template <int kHalves, bool kMass>
-__global__ __launch_bounds__(kHalves * 256, 2) void latent_mass_kernel(LatentMassArgs a) {
-  constexpr int kBuffers = 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t tiles_lds[kHalves][kBuffers][kTileBytes];
-  __shared__ float2 found[2][kHalves][4][kRowsTile];                  // maxima and sums of a tile, by group of keys
-  __shared__ __attribute__((aligned(16))) float row_lse[2][kHalves][kRowsTile];
-  __shared__ __attribute__((aligned(16))) int row_limit[2][kHalves][kRowsTile];
-  __shared__ float sums[kHalves][kKeys];
+// A row's maximum and sum over more keys.
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2);
+  l = l * __builtin_amdgcn_exp2f(m - top) + l2 * __builtin_amdgcn_exp2f(m2 - top);
+  m = top;
+}
+// log2 of the sum over all keys: infinity for a row that sees none (its weights are zero), NaN for one that sees a key past the table.
+__device__ __forceinline__ float log_sum(float m, float l, int limit, int reach) {
+  if (limit > reach) return __builtin_nanf("");
+  return l == 0.f ? __builtin_inff() : m + __builtin_amdgcn_logf(l);  // (logf: base 2)
+}
 
-  const int b = (int)(blockIdx.x / (unsigned)a.each), first_block = (int)(blockIdx.x - (unsigned)b * a.each);
-  const Seq seq = sequence(a, b);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = wave & 3, half = wave >> 2;
+enum class Pass { kSums, kScores, kWeights };  // maxima and sums; the scores too; sums of weights by key
+
+template <Pass kPass>
+__global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args) {
+  constexpr bool kWeights = kPass == Pass::kWeights;
+  const LatentAttnArgs& a = args.work;
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles_lds[kBuffers * kTileBytes];
+  __shared__ __attribute__((aligned(16))) uint32_t map_unit[kMap];  // where a key lies, in 128 bytes
+  __shared__ __attribute__((aligned(16))) float map_scale[kMap];    // its scale times scale log2(e)
+  __shared__ __attribute__((aligned(16))) float row_lse[kRows];
+  __shared__ __attribute__((aligned(16))) int row_limit[kRows];
+  __shared__ float sums[2][4][kTile];
+  Work work;
+  if (!find_work<kRows, kTile>(a, work)) return;
+  if (work.id - work.part + work.parts > args.ids) return;  // (starts that are not rising)
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, g = lane >> 5;
-  const int64_t rows = (int64_t)seq.n * a.H;
-  const int tiles = (int)((rows + kRowsTile - 1) / kRowsTile), rounds = (tiles + kHalves - 1) / kHalves;
+  const Seq seq = work.seq;
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int rows = uniform((int)min((int64_t)seq.n * a.H - (int64_t)work.block * kRows, (int64_t)kRows));
+  const int reach = reach_of(a);
+  const int row = wave * 32 + r;
+  const bool row_ok = row < rows;
+  const bool active = uniform(wave * 32) < rows;
+  const int flat = work.block * kRows + row;
+  const int tok = row_ok ? flat / a.H : 0, head = row_ok ? flat - tok * a.H : 0;
+  const int limit = row_ok ? sees(seq, tok) : 0;
+  const int last_tok = uniform((work.block * kRows + rows - 1) / a.H);
+  const int keys = min(sees(seq, last_tok), reach);
+  const int tiles = (keys + kTile - 1) / kTile;
+  const int t_begin = uniform((int)((int64_t)tiles * work.part / work.parts));
+  const int t_end = uniform((int)((int64_t)tiles * (work.part + 1) / work.parts));
+  // keys that every row of the wave sees: tiles before need no mask
+  const int all = uniform(wave * 32 + 32 <= rows ? limit : 0);
   const float c = a.scale * 1.44269504088896341f;
-  const int64_t all_rows = (int64_t)a.T * a.H, row0 = (int64_t)seq.q0 * a.H;
+  if (!kWeights && work.block == 0 && work.part == 0 && tid == 0) args.first[work.index] = make_int2(work.id, work.parts);
 
-  // copies of a tile: group w brings rows 8 w .. 8 w + 7, lanes 8 i .. 8 i + 7 row i
-  const int copy_row = group * 8 + (lane >> 3);
-  const int copy_col = ((lane & 7) ^ lds_swizzle(copy_row)) * 16;
-  auto copy_tile = [&](int t, int buffer) {
-    const int64_t flat = min((int64_t)t * kRowsTile + copy_row, rows - 1);  // (past the last row: it again)
-    const int tok = (int)(flat / a.H), head = (int)(flat - (int64_t)tok * a.H);
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.q + (int64_t)(seq.q0 + tok) * a.q_tok + (int64_t)head * a.q_head) + copy_col;
-    const uint32_t dst = lds_addr(&tiles_lds[half][buffer][group * 1024]);
-#pragma unroll
-    for (int i = 0; i < 9; ++i) copy16_m0(src + i * 128, __builtin_amdgcn_readfirstlane(dst + i * kRowsTile * 128));
-  };
-  const int sw = lds_swizzle(r);
-  auto row_piece = [&](const uint8_t* tile, int column) {  // 16 bytes of row r
-    return __builtin_bit_cast(v8bf, *reinterpret_cast<const v4i*>(tile + (column >> 3) * kRowsTile * 128 + r * 128 + (((column & 7) ^ sw) << 4)));
-  };
-
-  for (int kb = first_block; kb < (kMass ? (a.width + kKeys - 1) / kKeys : (seq.reach + kKeys - 1) / kKeys); kb += a.each) {
-    const int key0 = kb * kKeys, key = key0 + group * 32 + r;
-    const bool any = key0 < seq.reach && rows > 0;  // (the same in the whole workgroup)
-    float total = 0.f;
-    if (any) {
-      copy_tile(min(half, tiles - 1), 0);
-      // ---- the keys
-      const int col = key / a.cache.page_size, off = key - col * a.cache.page_size;
-      const int page = key < seq.reach ? a.cache.table[(int64_t)b * a.cache.table_stride + col] : -1;
-      const bool none = page < 0 || page >= a.cache.pages;
-      const uint8_t* src = none ? reinterpret_cast<const uint8_t*>(kNoRow)
-                                : a.cache.rows + (int64_t)page * a.cache.page_stride + (int64_t)off * kLatentRow;
-      uint4 codes[16];
-      v8bf rope[4];
-#pragma unroll
-      for (int s = 0; s < 16; ++s) codes[s] = *reinterpret_cast<const uint4*>(src + (2 * s + g) * 16);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) rope[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4i*>(src + kLatentDim + (2 * s + g) * 16));
-      const float unit = (none ? __builtin_nanf("") : e8_value(a.cache.scales[(int64_t)page * a.cache.scale_stride + off])) * c;
-      v8bf keys[32];
-#pragma unroll
-      for (int s = 0; s < 16; ++s) {
-        keys[2 * s] = codes_bf16(codes[s].x, codes[s].y);
-        keys[2 * s + 1] = codes_bf16(codes[s].z, codes[s].w);
-      }
-      float units[kMass ? 1 : 16];  // of the lane's key, or of its 16 keys
-      if constexpr (kMass) units[0] = unit;
-      else
-#pragma unroll
-        for (int i = 0; i < 16; ++i) units[i] = __shfl(unit, 8 * (i >> 2) + 4 * g + (i & 3));
-
-      for (int round = 0; round < rounds; ++round) {
-        const int t = round * kHalves + half, turn = round & 1;
-        const bool real = t < tiles;
-        // ---- this tile's rows: what they see, and (kMass) the log2 of their sums
-        const int64_t flat = (int64_t)t * kRowsTile + r;
-        const int tok = (int)(min(flat, rows - 1) / a.H);
-        const int limit = flat < rows ? sees(seq, tok) : 0;
-        if constexpr (kMass) {
-          if (group == 0 && g == 0) {
-            row_limit[turn][half][r] = limit;
-            row_lse[turn][half][r] = flat < rows ? a.lse[row0 + flat] : __builtin_inff();
-          }
+  if constexpr (kWeights) {
+    // the rows' sums, joined over the parts of their block
+    if (tid < kRows) {
+      const int mine = work.block * kRows + tid;
+      const int lim = tid < rows ? sees(seq, mine / a.H) : 0;
+      float m = kNone, l = 0.f;
+      const float2* p = args.stats + (int64_t)(work.id - work.part) * kRows + tid;
+      if (tid < rows)
+        for (int i = 0; i < work.parts; ++i) {
+          const float2 f = p[(int64_t)i * kRows];
+          join(m, l, f.x, f.y);
         }
-        wait_copies();
-        lds_barrier();
-        if (round + 1 < rounds) copy_tile(min(t + kHalves, tiles - 1), turn ^ 1);
-        if constexpr (!kMass) {
-          // the tile before: its groups' maxima and sums as one
-          if (round > 0 && group == 0 && g == 0 && t - kHalves < tiles) {
-            const int64_t before = flat - kHalves * kRowsTile;
-            if (before < rows) {
-              float m = kNegInf, l = 0.f;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) m = fmaxf(m, found[turn ^ 1][half][i][r].x);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 f = found[turn ^ 1][half][i][r];
-                l += f.x == kNegInf ? f.y : f.y * __builtin_amdgcn_exp2f(f.x - m);
-              }
-              a.parts[(int64_t)kb * all_rows + row0 + before] = make_float2(m, l);
-            }
-          }
-        }
-        if (!real) continue;
-        const uint8_t* tile = &tiles_lds[half][turn][0];
-        v16f lat, rot;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) lat[i] = rot[i] = 0.f;
-#pragma unroll
-        for (int s = 0; s < 32; ++s) {
-          // key piece s: codes 16 (2 (s / 2) + g) + 8 (s % 2) .. + 7
-          const v8bf x = row_piece(tile, 4 * (s >> 1) + 2 * g + (s & 1));
-          lat = kMass ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, keys[s], lat, 0, 0, 0)
-                      : __builtin_amdgcn_mfma_f32_32x32x16_bf16(keys[s], x, lat, 0, 0, 0);
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const v8bf x = row_piece(tile, 64 + 2 * s + g);
-          rot = kMass ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, rope[s], rot, 0, 0, 0)
-                      : __builtin_amdgcn_mfma_f32_32x32x16_bf16(rope[s], x, rot, 0, 0, 0);
-        }
-        if constexpr (kMass) {
-          // rows 8 (i / 4) + 4 g + i % 4 of the lane's key
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const v4f lse = *reinterpret_cast<const v4f*>(&row_lse[turn][half][8 * i4 + 4 * g]);
-            const v4i lim = *reinterpret_cast<const v4i*>(&row_limit[turn][half][8 * i4 + 4 * g]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = fmaf(lat[4 * i4 + i], units[0], fmaf(rot[4 * i4 + i], c, -lse[i]));
-              const float p = __builtin_amdgcn_exp2f(x);
-              total += key < lim[i] ? p : 0.f;
-            }
-          }
-        } else {
-          float x[16], m = kNegInf, l = 0.f;
-          const int left = limit - (key0 + group * 32 + 4 * g);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] = fmaf(lat[i], units[i], rot[i] * c);
-            if (8 * (i >> 2) + (i & 3) >= left) x[i] = kNegInf;
-            m = fmaxf(m, x[i]);
-          }
-          m = fmaxf(m, __shfl_xor(m, 32));
-          const float ref = m == kNegInf ? 0.f : m;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) l += __builtin_amdgcn_exp2f(x[i] - ref);
-          l += __shfl_xor(l, 32);
-          if (g == 0) found[turn][half][group][r] = make_float2(m, l);
-        }
-      }
-      if constexpr (!kMass) {
-        lds_barrier();
-        const int64_t flat = (int64_t)((rounds - 1) * kHalves + half) * kRowsTile + r;
-        if (group == 0 && g == 0 && flat < rows) {
-          const int turn = (rounds - 1) & 1;
-          float m = kNegInf, l = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m = fmaxf(m, found[turn][half][i][r].x);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = found[turn][half][i][r];
-            l += f.x == kNegInf ? f.y : f.y * __builtin_amdgcn_exp2f(f.x - m);
-          }
-          a.parts[(int64_t)kb * all_rows + row0 + flat] = make_float2(m, l);
-        }
-      }
-      lds_barrier();  // the tiles and the lists are free for the next block of keys
-    }
-    if constexpr (kMass) {
-      total += __shfl_xor(total, 32);
-      if (g == 0) sums[half][group * 32 + r] = total;
-      lds_barrier();
-      if (half == 0 && g == 0 && key < a.width) {
-#pragma unroll
-        for (int h = 1; h < kHalves; ++h) total += sums[h][group * 32 + r];
-        // tokens that are new in this call start at zero; past the sequence there are none
-        const float before = a.mass_in != nullptr && key < seq.len - seq.n ? a.mass_in[(int64_t)b * a.in_stride + key] : 0.f;
-        a.mass[(int64_t)b * a.out_stride + key] = key < seq.reach ? before + total : 0.f;
-      }
-      lds_barrier();
+      row_lse[tid] = tid < rows ? log_sum(m, l, lim, reach) : __builtin_inff();
+      row_limit[tid] = lim;
     }
   }
-}
+  // ---- the wave's rows: step s holds dimensions 16 (2 (s / 2) + g) + 8 (s % 2) .. + 7, then the rotary part
+  v8bf q[36];
+  {
+    const uint16_t* from = a.q + (int64_t)(seq.q0 + tok) * a.q_tok + (int64_t)head * a.q_head;
+#pragma unroll
+    for (int s = 0; s < 36; ++s) {
+      v4i v = {0, 0, 0, 0};
+      if (row_ok) v = *reinterpret_cast<const v4i*>(from + (s < 32 ? 16 * (2 * (s >> 1) + g) + 8 * (s & 1) : kLatentDim + 8 * (2 * (s - 32) + g)));
+      q[s] = __builtin_bit_cast(v8bf, v);
+    }
+  }
+  float lse[kWeights ? 16 : 1];
+  if constexpr (kWeights) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v4f v = *reinterpret_cast<const v4f*>(&row_lse[wave * 32 + 8 * i + 4 * g]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lse[4 * i + j] = v[j];
+    }
+  }
 
-// The log2 of each row's sum over all its keys.
-__global__ __launch_bounds__(256) void latent_lse_kernel(LatentMassArgs a) {
-  const int b = (int)(blockIdx.x / (unsigned)a.each), first = (int)(blockIdx.x - (unsigned)b * a.each);
-  const Seq seq = sequence(a, b);
-  const int64_t rows = (int64_t)seq.n * a.H, all_rows = (int64_t)a.T * a.H, row0 = (int64_t)seq.q0 * a.H;
-  const int blocks = (seq.reach + kKeys - 1) / kKeys;
-  for (int64_t row = (int64_t)first * 256 + threadIdx.x; row < rows; row += (int64_t)a.each * 256) {
-    const float2* p = a.parts + row0 + row;
-    float m = kNegInf, l = 0.f;
-    for (int i = 0; i < blocks; ++i) {
-      const float2 f = p[(int64_t)i * all_rows];
-      const float top = fmaxf(m, f.x);
-      if (top == kNegInf) {
-        l += f.y;  // (no key seen so far, or NaN)
+  // ---- copies: the wave's 8 keys of a tile, lanes 8 i .. 8 i + 7 at key i
+  auto swizzle = [](int k) { return ((k >> 2) & 1) | (k & 2); };
+  const uint32_t lane_off = (uint32_t)(((lane & 7) ^ swizzle(lane >> 3)) << 4);
+  const uint32_t lds = lds_addr(tiles_lds);
+  auto copy_tile = [&](int i, int buffer) {  // tile i of those looked up
+    const uint32_t unit = map_unit[i * kTile + wave * 8 + (lane >> 3)];
+    const uint8_t* src = (unit == kNowhere ? reinterpret_cast<const uint8_t*>(kNoRow) : a.cache.rows + (uint64_t)unit * 128) + lane_off;
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(lds + buffer * kTileBytes + wave * kGroupBytes);
+    static_for<5>([&](auto b) {
+      constexpr int block = decltype(b)::v;
+      copy16_block<128 * block>(src, dst + (kBlockBytes - 128) * block);
+    });
+  };
+  const uint32_t key_base = (r >> 3) * kGroupBytes + (r & 7) * 128;
+  const uint32_t key_first = key_base + ((g ^ swizzle(r)) << 4), key_second = key_base + (((2 + g) ^ swizzle(r)) << 4);
+
+  float m = kNone, l = 0.f;  // of the lane's row, over its 16 keys of every tile
+  float x[16];               // scores of a tile (kScores: stored a tile later)
+  const int64_t row0 = (int64_t)seq.q0 * a.H;
+  float* partial = kWeights ? args.partial + (row0 / kRows + work.index + work.block) * args.pitch : nullptr;
+  float* scores = kPass == Pass::kScores ? args.scores + (row0 + flat) * args.pitch + 4 * g : nullptr;
+  const int waves_on = (rows + 31) / 32;
+  // what the tile before left, to memory
+  auto flush = [&](int t, int turn) {
+    if constexpr (kPass == Pass::kScores) {
+      if (row_ok)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(scores + t * kTile + 8 * i) = v4f{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+    }
+    if constexpr (kWeights) {
+      if (wave == (t & 3) && lane < kTile) {
+        float v = sums[turn][0][lane];
+        for (int w = 1; w < waves_on; ++w) v += sums[turn][w][lane];
+        partial[t * kTile + lane] = v;
+      }
+    }
+  };
+
+  for (int t0 = t_begin; t0 < t_end; t0 += kMap / kTile) {
+    const int n = min(t_end - t0, kMap / kTile);
+    if (t0 > t_begin) __syncthreads();
+    // ---- where the keys lie
+    for (int i = tid; i < n * kTile; i += 256) {
+      const int key = t0 * kTile + i;
+      const int col = key / a.cache.page_size, off = key - col * a.cache.page_size;
+      const int page = key < keys ? a.cache.table[(int64_t)work.index * a.cache.table_stride + col] : -1;
+      const bool none = page < 0 || page >= a.cache.pages;
+      map_unit[i] = none ? kNowhere : (uint32_t)page * (uint32_t)(a.cache.page_stride / 128) + (uint32_t)off * (kLatentRow / 128);
+      map_scale[i] = none ? __builtin_nanf("") : e8_value(a.cache.scales[(int64_t)page * a.cache.scale_stride + off]) * c;
+    }
+    __syncthreads();
+    copy_tile(0, 0);
+    if (n > 1) copy_tile(1, 1);
+    int buffer = 0;
+    for (int i = 0; i < n; ++i) {
+      const int t = t0 + i;
+      // tile t has landed (the five copies of the next may be under way), and every wave is done with the one before
+      if (i + 1 < n) wait_copies_upto<5>();
+      else wait_copies();
+      lds_barrier();
+      if (t > t_begin && (kWeights || active)) flush(t - 1, (t - 1) & 1);
+      if (i + 2 < n) copy_tile(i + 2, buffer == 0 ? 2 : buffer - 1);
+      const uint8_t* tile = tiles_lds + buffer * kTileBytes;
+      buffer = buffer == 2 ? 0 : buffer + 1;
+      if (!active) continue;
+      v16f lat, rot;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) lat[j] = rot[j] = 0.f;
+#pragma unroll
+      for (int s = 0; s < 16; ++s) {  // 16 bytes of codes: two products
+        const v4i k = *reinterpret_cast<const v4i*>(tile + (s & 1 ? key_second : key_first) + (s >> 2) * kBlockBytes + ((s >> 1) & 1) * 64);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const v8bf key = codes_bf16(k[2 * h], k[2 * h + 1]);
+          lat = kWeights ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[2 * s + h], key, lat, 0, 0, 0)
+                         : __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[2 * s + h], lat, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const v8bf key = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4i*>(tile + (s & 1 ? key_second : key_first) + 4 * kBlockBytes + (s >> 1) * 64));
+        rot = kWeights ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[32 + s], key, rot, 0, 0, 0)
+                       : __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[32 + s], rot, 0, 0, 0);
+      }
+      if constexpr (kWeights) {
+        const float unit = map_scale[i * kTile + r];
+        float total = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = __builtin_amdgcn_exp2f(fmaf(lat[j], unit, fmaf(rot[j], c, -lse[j])));
+        if (t * kTile + kTile > all) {
+#pragma unroll
+          for (int j4 = 0; j4 < 4; ++j4) {
+            const v4i lim = *reinterpret_cast<const v4i*>(&row_limit[wave * 32 + 8 * j4 + 4 * g]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * j4 + j] = t * kTile + r < lim[j] ? x[4 * j4 + j] : 0.f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) total += x[j];
+        total += __shfl_xor(total, 32);
+        if (g == 0) sums[t & 1][wave][r] = total;
       } else {
-        l = l * __builtin_amdgcn_exp2f(m - top) + f.y * __builtin_amdgcn_exp2f(f.x - top);
+#pragma unroll
+        for (int j4 = 0; j4 < 4; ++j4) {
+          const v4f unit = *reinterpret_cast<const v4f*>(&map_scale[i * kTile + 8 * j4 + 4 * g]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[4 * j4 + j] = fmaf(lat[4 * j4 + j], unit[j], rot[4 * j4 + j] * c);
+        }
+        if (t * kTile + kTile > all) {
+          const int left = limit - t * kTile - 4 * g;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = 8 * (j >> 2) + (j & 3) >= left ? kNegInf : x[j];
+        }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
+        float more[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) more[j & 1] += __builtin_amdgcn_exp2f(x[j] - top);
+        l = fmaf(l, __builtin_amdgcn_exp2f(m - top), more[0] + more[1]);
         m = top;
       }
     }
-    if (sees(seq, (int)(row / a.H)) > seq.reach) l = __builtin_nanf("");
-    a.lse[row0 + row] = l == 0.f ? __builtin_inff() : m + __builtin_amdgcn_logf(l);  // (logf: base 2)
+  }
+  if constexpr (kWeights) lds_barrier();
+  if (t_begin < t_end && (kWeights || active)) flush(t_end - 1, (t_end - 1) & 1);
+  if constexpr (!kWeights) {
+    join(m, l, __shfl_xor(m, 32), __shfl_xor(l, 32));
+    if (g == 0 && row_ok) args.stats[(int64_t)work.id * kRows + row] = make_float2(m, l);
   }
 }
 
-template <int kHalves>
-hipError_t launch(LatentMassArgs a, hipStream_t stream) {
-  // Workgroups a sequence: one a block of keys, but a page table may reach much further than its sequences do.
-  const int64_t most = 8192 / a.B + 1;
-  auto each = [&](int64_t n) { return (int)std::max<int64_t>(std::min(n, most), 1); };
-  const int64_t reach = (int64_t)a.cache.table_width * a.cache.page_size;
-  if (reach > 0) {
-    a.each = each((reach + kKeys - 1) / kKeys);
-    hipLaunchKernelGGL((latent_mass_kernel<kHalves, false>), dim3((unsigned)(a.each * a.B)), dim3(kHalves * 256), 0, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+// The keys of a workgroup of the last launch.
+constexpr int kSumKeys = 256;
+
+// What the masses become. tokens that are new in this call start at zero; past the sequence there are none.
+__device__ __forceinline__ void store_mass(const LatentMassArgs& args, const Seq& seq, int b, int key, int reach, float total) {
+  if (key >= args.width) return;
+  const float before = args.mass_in != nullptr && key < seq.len - seq.n ? args.mass_in[(int64_t)b * args.in_stride + key] : 0.f;
+  args.mass[(int64_t)b * args.out_stride + key] = key < min(seq.len, reach) ? before + total : 0.f;
+}
+
+// Weights from the scores: lanes hold 4 keys each, the four waves take every fourth row.
+__global__ __launch_bounds__(256) void latent_sum_kernel(LatentMassArgs args) {
+  const LatentAttnArgs& a = args.work;
+  __shared__ float row_lse[kRows];
+  __shared__ int row_limit[kRows];
+  __shared__ __attribute__((aligned(16))) v4f sums[3][64];
+  const int b = (int)(blockIdx.x / (unsigned)args.each), first = (int)(blockIdx.x - (unsigned)b * args.each);
+  const Seq seq = sequence(a, b);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t rows = (int64_t)seq.n * a.H, row0 = (int64_t)seq.q0 * a.H;
+  const int reach = reach_of(a), blocks = (int)((rows + kRows - 1) / kRows);
+  const int2 parts = rows > 0 ? args.first[b] : make_int2(0, 1);
+  for (int k0 = first * kSumKeys; k0 < args.width; k0 += args.each * kSumKeys) {
+    const int key = k0 + lane * 4;
+    v4f total = {0.f, 0.f, 0.f, 0.f};
+    for (int blk = 0; blk < blocks && k0 < min(seq.len, reach); ++blk) {
+      const int id = parts.x + blk * parts.y, count = (int)min(rows - (int64_t)blk * kRows, (int64_t)kRows);
+      if (id < 0 || parts.y < 1 || parts.y > args.ids - id) break;  // (starts that are not rising)
+      __syncthreads();
+      if (tid < count) {
+        float m = kNone, l = 0.f;
+        for (int i = 0; i < parts.y; ++i) {
+          const float2 f = args.stats[(int64_t)(id + i) * kRows + tid];
+          join(m, l, f.x, f.y);
+        }
+        const int limit = sees(seq, (int)(((int64_t)blk * kRows + tid) / a.H));
+        row_lse[tid] = log_sum(m, l, limit, reach);
+        row_limit[tid] = min(limit, reach);
+      }
+      __syncthreads();
+      const float* from = args.scores + (row0 + (int64_t)blk * kRows) * args.pitch + key;
+      constexpr int kTogether = 8;
+      for (int p = wave; p < count; p += 4 * kTogether) {
+        v4f x[kTogether];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {  // (a row's scores reach to the last tile with a key that its block sees)
+          x[i] = v4f{kNegInf, kNegInf, kNegInf, kNegInf};
+          if (p + 4 * i < count && key < row_limit[p + 4 * i]) x[i] = *reinterpret_cast<const v4f*>(from + (int64_t)(p + 4 * i) * args.pitch);
+        }
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          const int at = min(p + 4 * i, count - 1);
+          const float lse = row_lse[at];
+          const int limit = p + 4 * i < count ? row_limit[at] : 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float w = __builtin_amdgcn_exp2f(x[i][j] - lse);
+            total[j] += key + j < limit ? w : 0.f;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (wave > 0) sums[wave - 1][lane] = total;
+    __syncthreads();
+    if (wave == 0) {
+      total += sums[0][lane] + sums[1][lane] + sums[2][lane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) store_mass(args, seq, b, key + j, reach, total[j]);
+    }
   }
-  a.each = each(((int64_t)a.T * a.H / a.B + 255) / 256);
-  hipLaunchKernelGGL(latent_lse_kernel, dim3((unsigned)(a.each * a.B)), dim3(256), 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.width < 1) return e;
-  a.each = each((a.width + kKeys - 1) / kKeys);
-  hipLaunchKernelGGL((latent_mass_kernel<kHalves, true>), dim3((unsigned)(a.each * a.B)), dim3(kHalves * 256), 0, stream, a);
+}
+
+// The sums of a sequence's blocks of rows.
+__global__ __launch_bounds__(kSumKeys) void latent_blocks_kernel(LatentMassArgs args) {
+  const LatentAttnArgs& a = args.work;
+  const int b = (int)(blockIdx.x / (unsigned)args.each), first = (int)(blockIdx.x - (unsigned)b * args.each);
+  const Seq seq = sequence(a, b);
+  const int64_t rows = (int64_t)seq.n * a.H, row0 = (int64_t)seq.q0 * a.H;
+  const int reach = reach_of(a), blocks = (int)((rows + kRows - 1) / kRows);
+  for (int key = first * kSumKeys + threadIdx.x; key < args.width; key += args.each * kSumKeys) {
+    float total = 0.f;
+    if (blocks > 0 && key < min(seq.len, reach)) {
+      // the first block whose last row sees the key: later ones all do
+      const int64_t from = (int64_t)max(key - (seq.len - seq.n), 0) * a.H / kRows;
+      const float* p = args.partial + (row0 / kRows + b) * args.pitch + key;
+#pragma unroll 4
+      for (int64_t i = from; i < blocks; ++i) total += p[i * args.pitch];
+    }
+    store_mass(args, seq, b, key, reach, total);
+  }
+}
+
+template <Pass kPass>
+hipError_t launch_pass(const LatentMassArgs& args, int64_t grid, hipStream_t stream) {
+  hipLaunchKernelGGL((latent_mass_kernel<kPass>), dim3((unsigned)grid), dim3(256), 0, stream, args);
   return hipGetLastError();
 }
 
 }  // namespace
 
-LatentMassPlan plan_latent_mass(int64_t T, int64_t H, int64_t max_keys) {
-  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  return {up((size_t)((max_keys + kKeys - 1) / kKeys) * (size_t)(T * H) * sizeof(float2)), up((size_t)(T * H) * sizeof(float))};
+// Scores are kept where they take this much at most and a sequence has 128 rows or fewer on average: a score costs 8 bytes of
+// traffic, scoring a key again its 641 bytes and the products.
+constexpr int64_t kMostScores = (int64_t)512 << 20;
+
+LatentMassPlan plan_latent_mass(int64_t T, int64_t B, int64_t H, int64_t max_keys) {
+  auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
+  LatentMassPlan p{};
+  const int64_t blocks = T * H / kRows + std::min(T, B), tiles = (max_keys + kTile - 1) / kTile;
+  p.max_tiles = (int)tiles;
+  p.min_tiles = 4;
+  p.target_parts = 512;
+  const int64_t cut = std::min<int64_t>(blocks * std::max<int64_t>((tiles + p.min_tiles - 1) / p.min_tiles, 1), p.target_parts);
+  p.ids = (std::max(blocks, cut) + 15) / 16 * 16;
+  p.pitch = tiles * kTile;
+  p.keeps_scores = T * H <= kRows * B && T * H <= kMostScores / 4 / std::max<int64_t>(p.pitch, 1);
+  p.first_bytes = up(B * (int64_t)sizeof(int2));
+  p.stats_bytes = up(p.ids * kRows * (int64_t)sizeof(float2));
+  p.rest_bytes = up((p.keeps_scores ? T * H : T * H / kRows + B + 1) * p.pitch * (int64_t)sizeof(float));
+  return p;
 }
 
-hipError_t launch_latent_mass(const LatentMassArgs& a, hipStream_t stream) {
-  return (int64_t)a.T * a.H <= (int64_t)a.B * kRowsTile ? launch<1>(a, stream) : launch<2>(a, stream);
+hipError_t launch_latent_mass(LatentMassArgs args, const LatentMassPlan& plan, hipStream_t stream) {
+  LatentAttnArgs& a = args.work;
+  hipError_t e = hipSuccess;
+  if (a.T > 0) {
+    e = plan.keeps_scores ? launch_pass<Pass::kScores>(args, plan.ids, stream) : launch_pass<Pass::kSums>(args, plan.ids, stream);
+    if (e == hipSuccess && !plan.keeps_scores) e = launch_pass<Pass::kWeights>(args, plan.ids, stream);
+  }
+  if (e != hipSuccess || args.width < 1) return e;
+  // Workgroups a sequence: one for every 256 columns, but a page table may reach much further than its sequences do.
+  const int64_t columns = (args.width + kSumKeys - 1) / kSumKeys;
+  args.each = (int)std::min<int64_t>(columns, 8192 / a.B + 1);
+  const dim3 grid((unsigned)(args.each * a.B));
+  if (a.T > 0 && plan.keeps_scores) hipLaunchKernelGGL(latent_sum_kernel, grid, dim3(256), 0, stream, args);
+  else hipLaunchKernelGGL(latent_blocks_kernel, grid, dim3(kSumKeys), 0, stream, args);
+  return hipGetLastError();
 }
 
 }  // namespace bfp8

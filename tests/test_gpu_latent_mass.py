@@ -153,6 +153,24 @@ def test_no_new_tokens(gpu):
         assert torch.equal(mass[b, :n], before[b, :n]) and bool((mass[b, n:] == 0).all())
 
 
+@pytest.mark.parametrize("heads,width", [(1, 36), (150, 36), (8, 1 << 14)])
+def test_many_sequences_of_shared_pages(gpu, heads, width):
+    """520 sequences on the pages of one, so that none is cut and each walks more than 2048 keys; a page table that reaches
+    far further than its sequences (2^20 tokens, too many for scores to be kept)."""
+    b, length = (520, 2200) if width == 36 else (17, 700)
+    c, keys = make(gpu, [length], [1], 1, 64, seed=77)
+    table = torch.full((b, width), -1, dtype=torch.int32, device=gpu)
+    table[:, :c["table"].shape[1]] = c["table"]
+    lens = torch.full((b,), length, dtype=torch.int32, device=gpu)
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(b, heads, 576, generator=g).to(torch.bfloat16).to(gpu)
+    announce("latent_attention_mass shared pages", heads, width)
+    _, mass = bfp8.latent_attention_mass(q, c["cache"], c["scales"], table, lens, SCALE)
+    some = [0, 1, b // 2, b - 1]
+    check(mass[some], None, q[some], keys * 4, [length] * 4, [1] * 4)
+    assert bool(((mass.double().sum(dim=1) - heads).abs() <= 2.0 ** -15 * heads).all())
+
+
 def test_captured_beside_eager_calls(gpu):
     """A replay follows later lengths, and larger eager calls on the stream do not disturb it."""
     lens, new, heads = [900, 400, 33], [1, 1, 1], 16
