@@ -887,13 +887,15 @@ def rmsnorm_quant_ue8m0(x: torch.Tensor, weight: torch.Tensor, residual: torch.T
 
 def _call(device: torch.device, name: str, *args):
     """The C entry `name` on the device of its tensors and that device's current stream (its last argument)."""
+    index = device.index
     entry = getattr(_native.lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = entry(*args, _stream(device))
+    if index == torch._C._cuda_getDevice():
+        st = entry(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            st = entry(*args, _stream(device))
-    _check(st, name)
+            st = entry(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _raise(st, name)
 
 
 LATENT_DIM, ROPE_DIM, LATENT_ROW = 512, 64, 640  # latents, rotary key, bytes of a cache row

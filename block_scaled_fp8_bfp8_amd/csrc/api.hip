@@ -1285,7 +1285,7 @@ bfp8_status_t check_int8_sizes(int64_t M, int64_t N, int64_t K) {
   if (K % 16 != 0) return fail(BFP8_ERR_UNSUPPORTED, "K = %lld is not a multiple of 16", (long long)K);
   if (K > bfp8::kInt8MaxK) return fail(BFP8_ERR_UNSUPPORTED, "K = %lld is more than %d", (long long)K, bfp8::kInt8MaxK);
   if (M > kMaxDim || N > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "M and N must each be at most 2^30");
-  if (((M + 63) / 64) * ((N + 127) / 128) > (int64_t)INT32_MAX)
+  if (((M + 63) / 64) * ((N + 63) / 64) > (int64_t)INT32_MAX)
     return fail(BFP8_ERR_UNSUPPORTED, "M x N = %lld x %lld has more output tiles than one launch grid holds",
                 (long long)M, (long long)N);
   return BFP8_OK;
@@ -1385,9 +1385,11 @@ bfp8_status_t bfp8_linear_int8(const void* x, int x_dtype, int64_t M, int64_t K,
   if (M == 0) return ok();
   st = check_device();
   if (st != BFP8_OK) return st;
+  const bfp8::Int8GemmArgs args{q, K, s, b, ldb, bs, bias, c, ldc, (int)M, (int)N, (int)K, x_dtype == BFP8_IN_F16};
+  if (bfp8::linear_int8_fuses(M, N, K))
+    return launched(bfp8::launch_linear_int8(args, static_cast<const uint16_t*>(x), ldx, (hipStream_t)stream), "linear_int8");
   st = launched(bfp8::launch_quant_act_int8(x, x_dtype, M, K, ldx, q, K, s, (hipStream_t)stream), "quant_act_int8");
   if (st != BFP8_OK) return st;
-  const bfp8::Int8GemmArgs args{q, K, s, b, ldb, bs, bias, c, ldc, (int)M, (int)N, (int)K, x_dtype == BFP8_IN_F16};
   return launched(bfp8::launch_gemm_int8(args, (hipStream_t)stream), "gemm_int8");
 }
 

@@ -16,7 +16,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "device_latent.h"
+#include "device_int8.h"
 #include "int8.h"
 #include "launch.h"
 
@@ -59,6 +59,7 @@ __device__ __forceinline__ v4i keep_valid(v4i f, int piece, int bytes) {
 }
 
 constexpr int kWaves = 8;
+constexpr int kFusedCodes = 16384;  // codes of all tokens that the linear layer's small-batch kernel holds (two workgroups on a compute unit)
 
 // ---------------------------------------------------------------- few rows: the waves split K
 
@@ -183,19 +184,141 @@ __global__ __launch_bounds__(kWaves * 64) void gemm_int8_ksplit_kernel(Int8GemmA
   }
 }
 
+// ---------------------------------------------------------------- one to eight rows, quantized here
+
+// The linear layer of kRows tokens at most: every workgroup quantizes the tokens into LDS while its first weights are on
+// their way, and then is the kernel above (16 weight rows a workgroup), with activations that are there already. Each workgroup repeats the
+// quantization, which for few codes costs less than a launch of its own.
+template <int kIn, int kRows>
+__global__ __launch_bounds__(kWaves * 64) void linear_int8_kernel(Int8GemmArgs args, const uint16_t* x, int64_t ldx) {
+  constexpr bool kF16 = kIn == kInF16;
+  constexpr int BN = 16, SLOTS = 3;
+  constexpr int kPieces = BN / 8, kSlot = BN * kBlock;
+  constexpr int kShare = kWaves / kRows;  // waves that share a token
+  static_assert(kRows * kShare == kWaves && 16 * BN * 4 <= SLOTS * kSlot, "tokens share the waves evenly, sums fit the slots");
+  __shared__ __attribute__((aligned(1024))) uint8_t slots[kWaves][SLOTS][kSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t codes[kFusedCodes];  // [K block][kRows][128], columns XORed as elsewhere
+  __shared__ float top[kWaves];
+  __shared__ float scales[kRows];
+
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, kc = lane >> 4;
+  const int n0 = blockIdx.x * BN, M = args.M, N = args.N, K = args.K;
+  const int KB = (K + kBlock - 1) / kBlock, last_bytes = K - (KB - 1) * kBlock;
+  const int nkb = KB > w ? (KB - w + kWaves - 1) / kWaves : 0;
+
+  // ---- a share of a token (a row past the last is it again)
+  const int token = w / kShare, share = w - token * kShare;
+  const uint16_t* row = x + (int64_t)min(token, M - 1) * ldx;
+  // (read twice, in loops: code for pieces held in registers takes longer to fetch than they take to come from L2 again)
+  const int pieces = (K + kShare * 512 - 1) / (kShare * 512);
+  float amax = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const int col = ((i * kShare + share) * 64 + lane) * 8;
+    Piece<kIn> v = {};
+    if (col < K) v = load_piece<kIn>(row, col);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(element<kIn>(v, e)));
+  }
+  // ---- the first weights
+  uint32_t off[kPieces];
+  const int8_t* bmat = args.b + (int64_t)n0 * args.ldb;
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int at = j * 8 + (lane >> 3);
+    off[j] = (uint32_t)min(at, N - 1 - n0) * (uint32_t)args.ldb + (uint32_t)(((lane & 7) ^ lds_swizzle(at)) * 16);
+  }
+  auto issue = [&](int slot, int kb) __attribute__((always_inline)) {
+    const uint32_t dst = lds_addr(&slots[w][slot][0]);
+    const bool part = kb == KB - 1 && last_bytes < kBlock;  // uniform
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int col = (lane & 7) ^ lds_swizzle(j * 8 + (lane >> 3));
+      copy16_m0(bmat + (int64_t)kb * kBlock, part && 16 * col >= last_bytes ? off[j] - (uint32_t)(col * 16) : off[j],
+                dst + (uint32_t)(j * 1024));
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s)
+    if (s < nkb) issue(s, w + s * kWaves);
+  // ---- codes and scales
+  amax = wave_max(amax);
+  if constexpr (kShare > 1) {
+    if (lane == 0) top[w] = amax;
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < kShare; ++i) amax = max_nan(amax, top[token * kShare + i]);
+  }
+  const Int8Scale scale(amax);
+  if (share == 0 && lane == 0) scales[token] = scale.value();
+#pragma unroll 2
+  for (int i = 0; i < pieces; ++i) {
+    const int col = ((i * kShare + share) * 64 + lane) * 8;
+    Piece<kIn> v = {};
+    if (col < K) v = load_piece<kIn>(row, col);
+    if (col < KB * kBlock)  // (zeros past K)
+      *reinterpret_cast<uint2*>(codes + ((col >> 7) * kRows + token) * kBlock + ((((col >> 4) & 7) ^ lds_swizzle(token)) << 4) + (col & 8)) =
+          row_codes(v, scale);
+  }
+  lds_barrier();
+
+  const int sw = lds_swizzle(r);
+  const uint32_t at_lo = (uint32_t)(r * kBlock + (((2 * kc) ^ sw) << 4)), at_hi = (uint32_t)(r * kBlock + (((2 * kc + 1) ^ sw) << 4));
+  const int ra = r % kRows, swa = lds_swizzle(ra);
+  const uint32_t a_lo = (uint32_t)(ra * kBlock + (((2 * kc) ^ swa) << 4)), a_hi = (uint32_t)(ra * kBlock + (((2 * kc + 1) ^ swa) << 4));
+  v4i acc = {0, 0, 0, 0};
+  int slot = 0;
+  for (int i = 0; i < nkb; ++i) {
+    const int kb = w + i * kWaves;
+    if (i + SLOTS - 1 < nkb) wait_copies_upto<(SLOTS - 1) * kPieces>();
+    else wait_copies();
+    const uint8_t* sl = &slots[w][slot][0];
+    const uint8_t* block = codes + kb * kRows * kBlock;
+    const v4i fb[2] = {*reinterpret_cast<const v4i*>(sl + at_lo), *reinterpret_cast<const v4i*>(sl + at_hi)};
+    const v4i fa[2] = {*reinterpret_cast<const v4i*>(block + a_lo), *reinterpret_cast<const v4i*>(block + a_hi)};
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
+    if (i + SLOTS < nkb) issue(slot, kb + SLOTS * kWaves);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h], fa[h], acc, 0, 0, 0);
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
+  }
+  *reinterpret_cast<v4i*>(reinterpret_cast<int*>(&slots[w][0][0]) + lane * 4) = acc;  // (no copy of this wave is in flight)
+  __syncthreads();
+  const bool vec_ok = (args.ldc & 3) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 7) == 0;
+  const int m = r, n = n0 + 4 * kc;
+  if (w == 0 && m < M && n < N) {
+    const float ms = scales[m];
+    v4i sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int ww = 0; ww < kWaves; ++ww) sum += *reinterpret_cast<const v4i*>(reinterpret_cast<const int*>(&slots[ww][0][0]) + lane * 4);
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = min(n + e, N - 1);
+      y[e] = fmaf((float)sum[e] * ms, args.bs[at], args.bias != nullptr ? bias_value<kF16>(args.bias[at]) : 0.f);
+    }
+    store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
+  }
+}
+
 // ---------------------------------------------------------------- tiles of LDS stages
 
 // A BN x BM tile of C^T, WGN x WGM waves of 32 TN x 32 TM. A K block is four steps of 32x32x32 products; the fragments
 // of a step are read while the one before is multiplied. At the end of a block's third step its last fragments have
 // been read and the next block has landed; past the barrier there its stage is refilled, and the next block's first
-// fragments are read.
+// fragments are read. With two stages (kEarly) that leaves a block's time for its copies to arrive in; so the activations
+// are read ahead, all by the end of the first step, and their half of the stage is refilled past a barrier there.
 template <int BN, int BM, int WGN, int WGM, int STAGES, bool kPart, bool kF16>
 __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8GemmArgs args) {
   constexpr int kNumWaves = WGN * WGM;
   constexpr int WN = BN / WGN, WM = BM / WGM, TN = WN / 32, TM = WM / 32;
   constexpr int kStage = (BN + BM) * kBlock;
-  constexpr int kCopies = (BN + BM) / 8 / kNumWaves;  // pieces of a block that a wave copies
-  static_assert((BN + BM) % (8 * kNumWaves) == 0 && BN % 8 == 0 && WN % 32 == 0 && WM % 32 == 0, "whole pieces and products");
+  constexpr int kCopiesB = BN / 8 / kNumWaves, kCopiesA = BM / 8 / kNumWaves;  // pieces of a block that a wave copies
+  constexpr int kCopies = kCopiesB + kCopiesA;
+  constexpr bool kEarly = STAGES == 2;
+  static_assert(BN % (8 * kNumWaves) == 0 && BM % (8 * kNumWaves) == 0 && WN % 32 == 0 && WM % 32 == 0, "whole pieces and products");
   static_assert(STAGES >= 2 && (STAGES - 2) * kCopies < 64, "stages");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * kStage];
   __shared__ __attribute__((aligned(16))) float channel[2][BN];  // scale and bias
@@ -213,24 +336,27 @@ __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8Gem
 
   const int8_t* bmat = args.b + (int64_t)n0 * args.ldb;
   const int8_t* amat = args.a + (int64_t)m0 * args.lda;
-  const int first = w * kCopies * 8;  // the wave's first row of a stage: weights, then activations
+  // a wave's pieces: kCopiesB of the weights' rows, then kCopiesA of the activations'
   uint32_t off[kCopies];
+  auto row_of = [&](int j) __attribute__((always_inline)) {  // of the stage
+    return j < kCopiesB ? (w * kCopiesB + j) * 8 : BN + (w * kCopiesA + j - kCopiesB) * 8;
+  };
 #pragma unroll
   for (int j = 0; j < kCopies; ++j) {
-    const int row = first + j * 8 + (lane >> 3);
+    const int row = row_of(j) + (lane >> 3);
     const int col = (lane & 7) ^ lds_swizzle(row);
-    off[j] = (first + j * 8 < BN ? (uint32_t)min(row, N - 1 - n0) * (uint32_t)args.ldb
-                                 : (uint32_t)min(row - BN, M - 1 - m0) * (uint32_t)args.lda) + (uint32_t)(col * 16);
+    off[j] = (j < kCopiesB ? (uint32_t)min(row, N - 1 - n0) * (uint32_t)args.ldb
+                           : (uint32_t)min(row - BN, M - 1 - m0) * (uint32_t)args.lda) + (uint32_t)(col * 16);
   }
   const uint32_t lds = lds_addr(smem);
   auto issue_piece = [&](int stage, int kb, int j) __attribute__((always_inline)) {
     uint32_t o = off[j];
     if (kPart && kb == KB - 1) {  // uniform
-      const uint32_t col = (uint32_t)((lane & 7) ^ lds_swizzle(first + j * 8 + (lane >> 3)));
+      const uint32_t col = (uint32_t)((lane & 7) ^ lds_swizzle(row_of(j) + (lane >> 3)));
       if ((int)(16 * col) >= last_bytes) o -= 16 * col;
     }
-    copy16_m0((first + j * 8 < BN ? bmat : amat) + (int64_t)kb * kBlock, o,
-              __builtin_amdgcn_readfirstlane(lds + (uint32_t)(stage * kStage + (first + j * 8) * kBlock)));
+    copy16_m0((j < kCopiesB ? bmat : amat) + (int64_t)kb * kBlock, o,
+              __builtin_amdgcn_readfirstlane(lds + (uint32_t)(stage * kStage + row_of(j) * kBlock)));
   };
 
   v16i acc[TN][TM];
@@ -246,48 +372,60 @@ __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8Gem
   uint32_t at[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) at[s] = (uint32_t)(r * kBlock + (((2 * s + g) ^ sw) << 4));
-  v4i fb[2][TN], fa[2][TM];
+  v4i fb[2][TN], fa[kEarly ? 4 : 2][TM];
   auto read_b = [&](const uint8_t* stage, int s, int tn) __attribute__((always_inline)) {
     fb[s & 1][tn] = *reinterpret_cast<const v4i*>(stage + at[s] + (wn * WN + tn * 32) * kBlock);
   };
   auto read_a = [&](const uint8_t* stage, int s, int tm, bool part) __attribute__((always_inline)) {
-    fa[s & 1][tm] = *reinterpret_cast<const v4i*>(stage + at[s] + (BN + wm * WM + tm * 32) * kBlock);
-    if (kPart && part) fa[s & 1][tm] = keep_valid(fa[s & 1][tm], 2 * s + g, last_bytes);
+    v4i& f = fa[kEarly ? s : s & 1][tm];
+    f = *reinterpret_cast<const v4i*>(stage + at[s] + (BN + wm * WM + tm * 32) * kBlock);
+    if (kPart && part) f = keep_valid(f, 2 * s + g, last_bytes);
   };
 
   constexpr int kProducts = TN * TM;
-  // refill: kb + STAGES blocks exist; more: a next block exists
   auto block = [&](int kb, int stage, auto steady) __attribute__((always_inline)) {
-    constexpr bool kSteady = decltype(steady)::value;
+    constexpr bool kSteady = decltype(steady)::value;  // block kb + STAGES exists
     const int next = stage + 1 == STAGES ? 0 : stage + 1;
     const uint8_t* here = smem + stage * kStage;
-    const uint8_t* then = smem + next * kStage;
+    const uint8_t* then = smem + next * kStage;  // (after the last block: stale bytes, not used)
     const bool part_here = kb == KB - 1, part_then = kb + 1 == KB - 1;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const uint8_t* from = s < 3 ? here : then;  // (after the last block: stale bytes, not used)
+      // the fragments read in this step: kEarly: activations of the next block's steps 0 to 2 in the last step, those of
+      // step 3 in the first; else each a step ahead
+      const int reads_a = !kEarly ? TM : s == 3 ? 3 * TM : s == 0 ? TM : 0, reads = reads_a + TN;
 #pragma unroll
       for (int p = 0; p < kProducts; ++p) {
         const int tm = p / TN, tn = p % TN;
-        acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[s & 1][tn], fa[s & 1][tm], acc[tn][tm], 0, 0, 0);
-        // the next step's fragments, as early as they fit
+        acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[s & 1][tn], fa[kEarly ? s : s & 1][tm], acc[tn][tm], 0, 0, 0);
 #pragma unroll
-        for (int x = 0; x < TN + TM; ++x)
-          if (x * kProducts / (TN + TM) == p) {
-            if (x < TM) read_a(from, (s + 1) & 3, x, s < 3 ? part_here : part_then);
-            else read_b(from, (s + 1) & 3, x - TM);
+        for (int x = 0; x < reads; ++x)
+          if (x * kProducts / reads == p) {
+            // (weights first: the next step needs them whole)
+            if (x < TN) read_b(s < 3 ? here : then, (s + 1) & 3, x);
+            else if (!kEarly) read_a(s < 3 ? here : then, (s + 1) & 3, x - TN, s < 3 ? part_here : part_then);
+            else if (s == 3) read_a(then, (x - TN) / TM, (x - TN) % TM, part_then);
+            else read_a(here, 3, x - TN, part_here);
           }
         if constexpr (kSteady) {
-          if (s == 3)
+          if (kEarly ? s == 3 || s == 1 : s == 3) {
+            const int from = kEarly && s == 1 ? kCopiesB : 0, to = kEarly && s == 3 ? kCopiesB : kCopies;
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j)
-              if (j * kProducts / kCopies == p) issue_piece(stage, kb + STAGES, j);
+            for (int j = from; j < to; ++j)
+              if ((j - from) * kProducts / (to - from) == p) issue_piece(stage, kb + STAGES, j);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (kEarly && s == 0) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        lds_barrier();
+      }
       if (s == 2) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (kSteady && STAGES > 2) wait_copies_upto<(STAGES - 2) * kCopies>();
+        // what may be under way past the next block: its successors, and of the refill begun above the activations
+        constexpr int kLater = kEarly ? kCopiesA : (STAGES - 2) * kCopies;
+        if (kSteady) wait_copies_upto<kLater>();
         else wait_copies();
         lds_barrier();
       }
@@ -302,7 +440,9 @@ __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8Gem
   wait_copies_upto<(STAGES - 1) * kCopies>();
   lds_barrier();
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) read_a(smem, 0, tm, KB == 1);
+  for (int s = 0; s < (kEarly ? 3 : 1); ++s)
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) read_a(smem, s, tm, KB == 1);
 #pragma unroll
   for (int tn = 0; tn < TN; ++tn) read_b(smem, 0, tn);
   int stage = 0, kb = 0;
@@ -390,19 +530,77 @@ hipError_t tiled(const Int8GemmArgs& a, hipStream_t stream) {
   return a.K % kBlock ? tiled_as<BN, BM, WGN, WGM, STAGES, true>(a, stream) : tiled_as<BN, BM, WGN, WGM, STAGES, false>(a, stream);
 }
 
+// A kernel's predicted time in microseconds, as sums of what it moves and does, fitted to times measured with cold weights
+// over 19 weight shapes from 12 x 25600 to 51200 x 5120 and 1 to 8192 tokens: the choice by it takes 1 % longer than
+// the fastest of the 13 on (geometric) average, 30 % at worst. (Per workgroup round: 256 run at once.)
+struct Shape {
+  int bn, bm;
+  hipError_t (*launch)(const Int8GemmArgs&, hipStream_t);
+  // a launch, a K block of a round and a round; MB copied by all workgroups, MB of weights, 10^6 outputs
+  double base, per_block, per_round, copied, weights, outputs;
+};
+constexpr Shape kTiled[] = {
+    {256, 256, tiled<256, 256, 2, 4, 2>, 3.00, 0.797, 4.77, 0.0461, 0.0155, 0.208},
+    {256, 128, tiled<256, 128, 4, 2, 3>, 2.49, 0.614, 3.09, 0.0267, 0.0680, 0.211},
+    {128, 256, tiled<128, 256, 2, 4, 3>, 2.70, 0.508, 2.99, 0.0340, 0.0500, 0.224},
+    {128, 128, tiled<128, 128, 2, 4, 4>, 2.75, 0.404, 0.68, 0.0191, 0.0743, 0.568},
+    {64, 128, tiled<64, 128, 2, 4, 4>, 1.55, 0.289, 1.49, 0.0152, 0.0453, 0.452},
+    {64, 64, tiled<64, 64, 2, 2, 4>, 2.48, 0.217, 0.40, 0.0, 0.0922, 0.523},
+};
+struct SplitShape {
+  int bn, bm;
+  hipError_t (*launch)(const Int8GemmArgs&, hipStream_t);
+};
+constexpr SplitShape kSplit[] = {{16, 16, ksplit<1, 1, 2>}, {16, 32, ksplit<1, 2, 2>}, {32, 16, ksplit<2, 1, 3>}, {32, 32, ksplit<2, 2, 2>},
+                                 {64, 16, ksplit<4, 1, 1>}, {32, 64, ksplit<2, 4, 1>}, {64, 64, ksplit<4, 4, 1>}};
+
 }  // namespace
 
 hipError_t launch_gemm_int8(const Int8GemmArgs& a, hipStream_t stream) {
-  if (a.M <= 16) return ksplit<1, 1, 4>(a, stream);
-  if (a.M <= 32) return ksplit<1, 2, 2>(a, stream);
-  if (a.M <= 64) return ksplit<2, 2, 2>(a, stream);
-  if (a.M <= 128) return ksplit<4, 2, 1>(a, stream);
-  if (a.M <= 256) return ksplit<4, 4, 1>(a, stream);
-  auto tiles = [&](int64_t bn, int64_t bm) { return ((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm); };
-  if (tiles(256, 256) >= 256) return tiled<256, 256, 2, 4, 2>(a, stream);
-  if (tiles(256, 128) >= 256) return tiled<256, 128, 4, 2, 3>(a, stream);
-  if (tiles(128, 128) >= 256) return tiled<128, 128, 2, 4, 4>(a, stream);
-  return tiled<128, 64, 4, 2, 4>(a, stream);
+  const double blocks = (a.K + kBlock - 1) / kBlock, weights = 1e-6 * a.N * (double)a.K, outputs = 1e-6 * a.N * (double)a.M;
+  double best = 1e30;
+  hipError_t (*launch)(const Int8GemmArgs&, hipStream_t) = nullptr;
+  auto tiles = [&](int bn, int bm) { return (double)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm); };
+  for (const SplitShape& s : kSplit) {
+    if ((a.M + s.bm - 1) / s.bm > 65535) continue;  // the grid's second dimension
+    const double n = tiles(s.bn, s.bm), rounds = std::ceil(n / 256), mb = 1e-6 * kBlock * (s.bn + s.bm) * blocks;
+    const double us = 1.91 + 0.107 * weights + 9.02 * rounds * mb + 0.0146 * n * mb + 0.354 * rounds +
+                      0.000238 * rounds * s.bn * s.bm + 0.893 * outputs;
+    if (us < best) best = us, launch = s.launch;
+  }
+  for (const Shape& s : kTiled) {
+    const double n = tiles(s.bn, s.bm), rounds = std::ceil(n / 256), mb = 1e-6 * kBlock * (s.bn + s.bm) * blocks;
+    const double us = s.base + rounds * (s.per_block * blocks + s.per_round) + s.copied * n * mb + s.weights * weights + s.outputs * outputs;
+    if (us < best) best = us, launch = s.launch;
+  }
+  return launch(a, stream);
+}
+
+namespace {
+template <int kIn, int kRows>
+hipError_t linear_rows(const Int8GemmArgs& a, const uint16_t* x, int64_t ldx, hipStream_t stream) {
+  hipLaunchKernelGGL((linear_int8_kernel<kIn, kRows>), dim3((unsigned)((a.N + 15) / 16)), dim3(kWaves * 64), 0, stream, a, x, ldx);
+  return hipGetLastError();
+}
+template <int kIn>
+hipError_t linear_small(const Int8GemmArgs& a, const uint16_t* x, int64_t ldx, hipStream_t stream) {
+  if (a.M == 1) return linear_rows<kIn, 1>(a, x, ldx, stream);
+  if (a.M == 2) return linear_rows<kIn, 2>(a, x, ldx, stream);
+  if (a.M <= 4) return linear_rows<kIn, 4>(a, x, ldx, stream);
+  return linear_rows<kIn, 8>(a, x, ldx, stream);
+}
+}  // namespace
+
+// Where one launch is faster (bf16, cold weights, us for one launch and for two, 1 and 8 tokens): 1024 x 1024 3.4 and 5.0, 4.2 and 5.2;
+// 4096 x 4096 7.3 and 9.5 (3 tokens 8.9 and 8.9); 7168 x 2048 6.0 and 7.9, 8.3 and 8.2. Not past one round of workgroups, two a compute unit:
+// 25600 x 1600 15.9 and 13.0, 22.0 and 13.3.
+bool linear_int8_fuses(int64_t M, int64_t N, int64_t K) {
+  const int64_t rows = M <= 2 ? M : M <= 4 ? 4 : 8;
+  return M >= 1 && M <= 8 && N <= 16 * 512 && rows * ((K + kBlock - 1) / kBlock * kBlock) <= kFusedCodes;
+}
+
+hipError_t launch_linear_int8(const Int8GemmArgs& a, const uint16_t* x, int64_t ldx, hipStream_t stream) {
+  return a.out_f16 ? linear_small<kInF16>(a, x, ldx, stream) : linear_small<kInBf16>(a, x, ldx, stream);
 }
 
 }  // namespace bfp8

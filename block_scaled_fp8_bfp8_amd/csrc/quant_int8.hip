@@ -1,55 +1,14 @@
 // Per-token quantization of activations to 8-bit integers.
 //
-// For every row m of x [M][K]:  a = max(max_k |x|, 1e-10),  s = a / 127 (correctly rounded),
-// q = 127 x / a rounded to the nearest integer, ties to even, of the exact quotient.
-// In float32, t = x * (127 / a) is off by at most 2^-23 of |t| <= 127 and so is decided unless it lies
-// within 2^-16 of the middle of two integers; there 127 x and (middle) a, both exact in 64 bits, are
-// compared. (bf16 and fp16 tokens hold many exact middles: a token whose largest element is 127 times a
-// power of two, for one.) A row with an infinite or NaN element has a NaN scale and zero codes.
-//
 // HBM-bound: x is read once, q written once. A row lives in the registers of the waves that share it, 8
 // elements a thread and chunk, as loaded; the waves exchange its largest element through LDS.
-#include "device_latent.h"
+#include "device_int8.h"
 #include "int8.h"
 #include "launch.h"
 
 namespace bfp8 {
 
 namespace {
-
-// 8 elements of type kIn, as loaded.
-template <int kIn>
-struct Piece {
-  uint4 v[kIn == kInF32 ? 2 : 1];
-};
-template <int kIn>
-__device__ __forceinline__ Piece<kIn> load_piece(const void* row, int col) {
-  Piece<kIn> p;
-  const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (int64_t)col * (kIn == kInF32 ? 4 : 2));
-  p.v[0] = at[0];
-  if constexpr (kIn == kInF32) p.v[1] = at[1];
-  return p;
-}
-template <int kIn>
-__device__ __forceinline__ float element(const Piece<kIn>& p, int i) {  // (i is known at compile time)
-  if constexpr (kIn == kInF32) {
-    const uint4& v = p.v[i >> 2];
-    return __uint_as_float((i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w);
-  } else {
-    const uint4& v = p.v[0];
-    const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
-    if constexpr (kIn == kInBf16) return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-    else return f16_value(i & 1 ? w >> 16 : w & 0xffffu);
-  }
-}
-
-// x rounded where t, its quotient in float32, is too near the middle of two integers to tell.
-__device__ __noinline__ float decide(float x, float a, float t) {
-  const float below = floorf(t);
-  const double d = 127.0 * (double)x - ((double)below + 0.5) * (double)a;  // both products are exact
-  const bool odd = (int)below & 1;
-  return d > 0.0 || (d == 0.0 && odd) ? below + 1.0f : below;
-}
 
 // kWaves waves share a row (kWaves == 1: four rows a workgroup), kChunks chunks of 8 elements a thread.
 template <int kIn, int kWaves, int kChunks>
@@ -83,38 +42,14 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void quant_int8_ke
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) amax = max_nan(amax, part[i]);
   }
-  const bool finite = amax < __builtin_inff();
-  const float a = fmaxf(amax, 1e-10f);
-  const float f = finite ? 127.0f / a : 0.f;
-  if (tid == 0 && row_ok) s[m] = finite ? a / 127.0f : __builtin_nanf("");
+  const Int8Scale scale(amax);
+  if (tid == 0 && row_ok) s[m] = scale.value();
 
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     const int col = (c * kThreads + tid) * 8;
     if (col >= K || !row_ok) continue;
-    float r[8];
-    bool near = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = element<kIn>(v[c], i) * f;
-      r[i] = rintf(t);
-      near |= fabsf(t - r[i]) > 0.5f - 0x1p-16f;
-    }
-    if (__builtin_expect(near, 0)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = element<kIn>(v[c], i), t = e * f;
-        if (fabsf(t - r[i]) > 0.5f - 0x1p-16f) r[i] = decide(e, a, t);
-      }
-    }
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int b0 = finite ? (int)r[4 * h] : 0, b1 = finite ? (int)r[4 * h + 1] : 0;
-      const int b2 = finite ? (int)r[4 * h + 2] : 0, b3 = finite ? (int)r[4 * h + 3] : 0;
-      w[h] = (b0 & 0xff) | (b1 & 0xff) << 8 | (b2 & 0xff) << 16 | (uint32_t)b3 << 24;
-    }
-    *reinterpret_cast<uint2*>(q + m * ldq + col) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(q + m * ldq + col) = row_codes(v[c], scale);
   }
 }
 

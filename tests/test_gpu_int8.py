@@ -103,6 +103,11 @@ SIZES = [(1, 1, 16), (1, 64, 128), (2, 17, 48), (1, 576, 7168), (16, 100, 400), 
          (64, 95, 2064), (83, 576, 7168), (100, 640, 1168), (128, 129, 144), (129, 130, 640), (200, 1000, 384), (256, 515, 1024),
          (257, 129, 128), (300, 1111, 784), (513, 520, 4112), (1000, 2500, 256), (1024, 4096, 1040), (1100, 8200, 384),
          (2100, 4097, 528), (4096, 4096, 128), (4100, 4200, 272)]
+# one whole and one partial last block of K for each of the 13 kernels that the choice may fall on
+SIZES += [(5121, 1, 128), (4098, 1, 16), (3, 4402, 128), (1, 4471, 16), (17, 4838, 16), (36, 5690, 128), (4232, 34, 16), (2, 10717, 640),
+          (1, 8942, 16), (294, 1732, 2304), (132, 2769, 2080), (171, 10944, 128), (385, 4935, 144), (7478, 556, 256), (6951, 1045, 32),
+          (1483, 2798, 640), (415, 9425, 16), (3354, 2438, 128), (2982, 2737, 272), (198, 4658, 384), (135, 5905, 16), (72, 5772, 128),
+          (19, 8799, 16)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
@@ -164,7 +169,9 @@ def test_bad_tokens_stay_alone(gpu):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (1, 40, 16), (3, 576, 7168), (5, 5120, 8192), (8, 1000, 528), (9, 333, 1040),
-                                   (64, 512, 2064), (300, 777, 640), (1000, 2048, 1024)])
+                                   (64, 512, 2064), (300, 777, 640), (1000, 2048, 1024), (1, 4500, 65536), (2, 100, 32768), (2, 48, 32784),
+                                   (4, 5000, 16384), (3, 130, 16400), (6, 77, 8192), (8, 4200, 8208), (7, 20, 112), (2, 1, 144),
+                                   (1, 8192, 16384), (1, 8193, 144), (2, 77, 8192), (2, 77, 8208), (4, 500, 4096), (3, 500, 4112), (8, 19, 2048), (5, 8192, 2000)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_linear_is_quantizer_and_product(gpu, m, n, k, dtype):
     announce("linear_int8", m, n, k, dtype)
