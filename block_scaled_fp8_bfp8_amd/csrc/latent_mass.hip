@@ -120,17 +120,6 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
       row_limit[tid] = lim;
     }
   }
-  // ---- the wave's rows: step s holds dimensions 16 (2 (s / 2) + g) + 8 (s % 2) .. + 7, then the rotary part
-  v8bf q[36];
-  {
-    const uint16_t* from = a.q + (int64_t)(seq.q0 + tok) * a.q_tok + (int64_t)head * a.q_head;
-#pragma unroll
-    for (int s = 0; s < 36; ++s) {
-      v4i v = {0, 0, 0, 0};
-      if (row_ok) v = *reinterpret_cast<const v4i*>(from + (s < 32 ? 16 * (2 * (s >> 1) + g) + 8 * (s & 1) : kLatentDim + 8 * (2 * (s - 32) + g)));
-      q[s] = __builtin_bit_cast(v8bf, v);
-    }
-  }
   float lse[kWeights ? 16 : 1];
   if constexpr (kWeights) {
     __syncthreads();
@@ -180,17 +169,51 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
     }
   };
 
-  for (int t0 = t_begin; t0 < t_end; t0 += kMap / kTile) {
-    const int n = min(t_end - t0, kMap / kTile);
-    if (t0 > t_begin) __syncthreads();
-    // ---- where the keys lie
-    for (int i = tid; i < n * kTile; i += 256) {
-      const int key = t0 * kTile + i;
-      const int col = key / a.cache.page_size, off = key - col * a.cache.page_size;
-      const int page = key < keys ? a.cache.table[(int64_t)work.index * a.cache.table_stride + col] : -1;
-      const bool none = page < 0 || page >= a.cache.pages;
-      map_unit[i] = none ? kNowhere : (uint32_t)page * (uint32_t)(a.cache.page_stride / 128) + (uint32_t)off * (kLatentRow / 128);
-      map_scale[i] = none ? __builtin_nanf("") : e8_value(a.cache.scales[(int64_t)page * a.cache.scale_stride + off]) * c;
+  // ---- where the keys of tiles t0 .. t0 + n - 1 lie (four a thread at a time: their loads overlap)
+  auto look_up = [&](int t0, int n) {
+    for (int i0 = tid; i0 < n * kTile; i0 += 4 * 256) {
+      int page[4], off[4], code[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = t0 * kTile + i0 + 256 * j, col = key / a.cache.page_size;
+        off[j] = key - col * a.cache.page_size;
+        page[j] = -1;
+        if (i0 + 256 * j < n * kTile && key < keys) page[j] = a.cache.table[(int64_t)work.index * a.cache.table_stride + col];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (page[j] >= a.cache.pages) page[j] = -1;
+        code[j] = 255;
+        if (page[j] >= 0) code[j] = a.cache.scales[(int64_t)page[j] * a.cache.scale_stride + off[j]];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + 256 * j;
+        if (i >= n * kTile) break;
+        map_unit[i] = page[j] < 0 ? kNowhere : (uint32_t)page[j] * (uint32_t)(a.cache.page_stride / 128) + (uint32_t)off[j] * (kLatentRow / 128);
+        map_scale[i] = e8_value(code[j]) * c;
+      }
+    }
+  };
+  constexpr int kMapTiles = kMap / kTile;
+  if (t_begin < t_end) look_up(t_begin, min(t_end - t_begin, kMapTiles));
+  // ---- the wave's rows (asked for behind the look-up's chain of loads): step s holds dimensions 16 (2 (s / 2) + g) + 8 (s % 2) .. + 7,
+  // then the rotary part
+  v8bf q[36];
+  {
+    const uint16_t* from = a.q + (int64_t)(seq.q0 + tok) * a.q_tok + (int64_t)head * a.q_head;
+#pragma unroll
+    for (int s = 0; s < 36; ++s) {
+      v4i v = {0, 0, 0, 0};
+      if (row_ok) v = *reinterpret_cast<const v4i*>(from + (s < 32 ? 16 * (2 * (s >> 1) + g) + 8 * (s & 1) : kLatentDim + 8 * (2 * (s - 32) + g)));
+      q[s] = __builtin_bit_cast(v8bf, v);
+    }
+  }
+  for (int t0 = t_begin; t0 < t_end; t0 += kMapTiles) {
+    const int n = min(t_end - t0, kMapTiles);
+    if (t0 > t_begin) {
+      __syncthreads();
+      look_up(t0, n);
     }
     __syncthreads();
     copy_tile(0, 0);
@@ -284,29 +307,53 @@ __device__ __forceinline__ void store_mass(const LatentMassArgs& args, const Seq
   args.mass[(int64_t)b * args.out_stride + key] = key < min(seq.len, reach) ? before + total : 0.f;
 }
 
-// Weights from the scores: lanes hold 4 keys each, the four waves take every fourth row.
+// Weights from the scores: lanes hold 4 keys each, the four waves take every fourth row. The first scores are on their way
+// while the rows' sums are joined.
 __global__ __launch_bounds__(256) void latent_sum_kernel(LatentMassArgs args) {
+  constexpr int kTogether = 8;
   const LatentAttnArgs& a = args.work;
   __shared__ float row_lse[kRows];
   __shared__ int row_limit[kRows];
+  __shared__ float2 joined[256];
   __shared__ __attribute__((aligned(16))) v4f sums[3][64];
   const int b = (int)(blockIdx.x / (unsigned)args.each), first = (int)(blockIdx.x - (unsigned)b * args.each);
   const Seq seq = sequence(a, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t rows = (int64_t)seq.n * a.H, row0 = (int64_t)seq.q0 * a.H;
-  const int reach = reach_of(a), blocks = (int)((rows + kRows - 1) / kRows);
+  const int reach = reach_of(a), keys = min(seq.len, reach), blocks = (int)((rows + kRows - 1) / kRows);
   const int2 parts = rows > 0 ? args.first[b] : make_int2(0, 1);
   for (int k0 = first * kSumKeys; k0 < args.width; k0 += args.each * kSumKeys) {
     const int key = k0 + lane * 4;
     v4f total = {0.f, 0.f, 0.f, 0.f};
-    for (int blk = 0; blk < blocks && k0 < min(seq.len, reach); ++blk) {
+    for (int blk = 0; blk < blocks && k0 < keys; ++blk) {
       const int id = parts.x + blk * parts.y, count = (int)min(rows - (int64_t)blk * kRows, (int64_t)kRows);
       if (id < 0 || parts.y < 1 || parts.y > args.ids - id) break;  // (starts that are not rising)
+      const float* from = args.scores + (row0 + (int64_t)blk * kRows) * args.pitch + key;
+      v4f x[kTogether];
+      auto read = [&](int p) {  // (what no key of the row's block filled is not used below)
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i)
+          if (p + 4 * i < count && key < keys) x[i] = *reinterpret_cast<const v4f*>(from + (int64_t)(p + 4 * i) * args.pitch);
+      };
+      read(wave);
+      // ---- the rows' sums: 2 to 16 threads a row take every so many parts, then one joins theirs
+      const int held = count > 64 ? 128 : count > 32 ? 64 : count > 16 ? 32 : 16, ways = 256 / held;
+      const int row = tid & (held - 1), way = tid / held;
+      float m = kNone, l = 0.f;
+      const float2* from_stats = args.stats + (int64_t)id * kRows + min(row, count - 1);
+      for (int i = way; i < parts.y; i += 4 * ways) {
+        float2 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = from_stats[(int64_t)min(i + j * ways, parts.y - 1) * kRows];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j * ways < parts.y) join(m, l, f[j].x, f[j].y);
+      }
+      joined[tid] = make_float2(m, l);
       __syncthreads();
       if (tid < count) {
-        float m = kNone, l = 0.f;
-        for (int i = 0; i < parts.y; ++i) {
-          const float2 f = args.stats[(int64_t)(id + i) * kRows + tid];
+        for (int i = 1; i < ways; ++i) {
+          const float2 f = joined[i * held + tid];
           join(m, l, f.x, f.y);
         }
         const int limit = sees(seq, (int)(((int64_t)blk * kRows + tid) / a.H));
@@ -314,15 +361,8 @@ __global__ __launch_bounds__(256) void latent_sum_kernel(LatentMassArgs args) {
         row_limit[tid] = min(limit, reach);
       }
       __syncthreads();
-      const float* from = args.scores + (row0 + (int64_t)blk * kRows) * args.pitch + key;
-      constexpr int kTogether = 8;
       for (int p = wave; p < count; p += 4 * kTogether) {
-        v4f x[kTogether];
-#pragma unroll
-        for (int i = 0; i < kTogether; ++i) {  // (a row's scores reach to the last tile with a key that its block sees)
-          x[i] = v4f{kNegInf, kNegInf, kNegInf, kNegInf};
-          if (p + 4 * i < count && key < row_limit[p + 4 * i]) x[i] = *reinterpret_cast<const v4f*>(from + (int64_t)(p + 4 * i) * args.pitch);
-        }
+        if (p > wave) read(p);
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
           const int at = min(p + 4 * i, count - 1);
@@ -335,8 +375,8 @@ __global__ __launch_bounds__(256) void latent_sum_kernel(LatentMassArgs args) {
           }
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
     if (wave > 0) sums[wave - 1][lane] = total;
     __syncthreads();
     if (wave == 0) {
@@ -344,6 +384,7 @@ __global__ __launch_bounds__(256) void latent_sum_kernel(LatentMassArgs args) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) store_mass(args, seq, b, key + j, reach, total[j]);
     }
+    __syncthreads();
   }
 }
 
@@ -384,7 +425,7 @@ LatentMassPlan plan_latent_mass(int64_t T, int64_t B, int64_t H, int64_t max_key
   LatentMassPlan p{};
   const int64_t blocks = T * H / kRows + std::min(T, B), tiles = (max_keys + kTile - 1) / kTile;
   p.max_tiles = (int)tiles;
-  p.min_tiles = 4;
+  p.min_tiles = T * H <= 32 * B || blocks * tiles <= 512 ? 2 : 4;
   p.target_parts = 512;
   const int64_t cut = std::min<int64_t>(blocks * std::max<int64_t>((tiles + p.min_tiles - 1) / p.min_tiles, 1), p.target_parts);
   p.ids = (std::max(blocks, cut) + 15) / 16 * 16;
