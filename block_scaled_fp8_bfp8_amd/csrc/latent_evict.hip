@@ -2,10 +2,10 @@
 // `recent` tokens and, of the earlier ones, the budget - recent with the largest mass (of equal ones the earlier), in
 // their order, as its tokens 0 .. budget - 1.
 //
-// Two launches. The first selects: a workgroup a sequence finds the least mass that stays, two bits at a time, by
-// counting how many reach each of three candidates (the masses, as integers that rise with them, stay in registers;
-// nothing is sorted and no counter is contended), and then places the tokens that stay by sums over the lanes, waves and
-// chunks before them. The second moves rows and scale codes. Onto other pages every token goes by itself; in place,
+// Two launches. The first selects: a workgroup a sequence finds the least mass that stays, a byte at a time from the top of
+// integers that rise with the masses, by counting the values of each byte among those that start like it (8192 masses stay
+// in registers; lanes that share a value count together), and then places the tokens that stay by sums over the lanes,
+// waves and chunks before them. The second moves rows and scale codes. Onto other pages every token goes by itself; in place,
 // where a kept token never moves up (its place is the number of kept ones before it), a workgroup moves one column of a
 // sequence's rows, a chunk of tokens at a time: what a chunk writes lies before everything that later chunks read, and
 // a barrier stands between the reads and the writes of a chunk. Selection is bound by its chain of barriers, the moves
@@ -40,19 +40,24 @@ __device__ __forceinline__ Length length_of(const LatentEvictArgs& a, int b) {
   return {n, min(n, a.budget)};
 }
 
-// Sum over 16 lanes, in the last of them.
-__device__ __forceinline__ int sum16(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // 1, 2, 4, 8 lanes up
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-  return v + __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+// Adds one to the bins of the lanes whose value counts. Most often many lanes share the first one's bin: they add together.
+__device__ __forceinline__ void count_bins(int* bins, uint32_t bin, bool counts, int lane) {
+  const uint64_t on = __ballot(counts);
+  if (on == 0) return;
+  const int leader = __builtin_ctzll(on);
+  const uint32_t common = (uint32_t)__builtin_amdgcn_readlane((int)bin, leader);
+  const bool together = counts && bin == common;
+  const int n = __popcll(__ballot(together));
+  if (lane == leader) atomicAdd(bins + common, n);
+  if (counts && !together) atomicAdd(bins + bin, 1);
 }
 
 // The masses are read a chunk at a time, thread t's i-th of a chunk being token 1024 i + t of it.
 __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs a) {
-  __shared__ int wave_sums[2][kHeld][kSelectWaves];
-  __shared__ int counts[2][3][kSelectWaves];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __attribute__((aligned(16))) int bins[4][256];  // of each byte, from the top
+  __shared__ int2 wave_sums[2][kHeld * kSelectWaves];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  reinterpret_cast<int*>(bins)[tid] = 0;
   const Length len = length_of(a, b);
   const int n = len.n;
   const float* mass = a.mass + (int64_t)b * a.mass_stride;
@@ -63,99 +68,86 @@ __global__ __launch_bounds__(kThreads) void latent_select_kernel(LatentEvictArgs
   const int want = len.kept - (n - old);   // of these stay
 
   float first[kHeld];  // masses of the first chunk
-  const int held_chunks = min((n + kThreads - 1) / kThreads, kHeld);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int j = i * kThreads + tid;
     first[i] = j < n ? mass[j] : 0.f;
   }
-  uint32_t least = 0;  // the least mass that stays, as an integer (0: all stay), and how many of those that equal it
+  uint32_t least = 0;  // the least mass that stays, as an integer, and how many of those that equal it
   int equals = 0;
-  if (cut && want == 0) least = 0xffffffffu;
   if (cut && want > 0) {
-    uint32_t held[kHeld];
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      held[i] = i * kThreads + tid < old ? rising(first[i]) : 0u;
-    }
-    int above = 0;  // masses above every value that starts with the bits found so far
-    for (int shift = 30; shift >= 0; shift -= 2) {
-      int c[3] = {0, 0, 0};
-      auto count = [&](uint32_t u) {
-#pragma unroll
-        for (uint32_t k = 0; k < 3; ++k) c[k] += __popcll(__ballot(u >= (least | (k + 1) << shift)));
+    equals = want;
+    const int held_chunks = min((old + kThreads - 1) / kThreads, kHeld);
+    __syncthreads();
+#pragma unroll 1
+    for (int byte = 0; byte < 4; ++byte) {
+      const int shift = 24 - 8 * byte;
+      auto count = [&](uint32_t u, bool there) {  // of the values that start with the bytes found so far
+        count_bins(bins[byte], (u >> shift) & 255u, there && (byte == 0 || (u ^ least) >> (shift + 8) == 0), lane);
       };
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
-        if (i < held_chunks) count(held[i]);  // (uniform)
-      for (int j0 = kChunk; j0 < old; j0 += kThreads) count(j0 + tid < old ? rising(mass[j0 + tid]) : 0u);
-      const int turn = (shift >> 1) & 1;
-      if (lane == 0)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) counts[turn][k][wave] = c[k];
+        if (i < held_chunks) count(rising(first[i]), i * kThreads + tid < old);
+      for (int j0 = kChunk; j0 < old; j0 += kThreads) count(j0 + tid < old ? rising(mass[j0 + tid]) : 0u, j0 + tid < old);
       __syncthreads();
-      int total[3];
+      // bins from the top, four a lane: the first at which the sum reaches what is still wanted (every wave finds it)
+      const v4i c = *reinterpret_cast<const v4i*>(&bins[byte][252 - 4 * lane]);
+      const int all = c[0] + c[1] + c[2] + c[3], through = wave_scan(all);
+      const uint64_t reached = __ballot(through >= equals);
+      const int at = reached ? __builtin_ctzll(reached) : 63;  // (always reached, unless the masses change under way)
+      int above = __builtin_amdgcn_readlane(through - all, at), bin = 255 - 4 * at;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) total[k] = counts[turn][k][lane & (kSelectWaves - 1)];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) total[k] = __builtin_amdgcn_readlane(sum16(total[k]), 15);
-      // the largest candidate that `want` masses reach
-      const int k = total[2] >= want ? 3 : total[1] >= want ? 2 : total[0] >= want ? 1 : 0;
-      if (k < 3) above = total[k];
-      least |= (uint32_t)k << shift;
+      for (int k = 3; k > 0; --k) {
+        const int here = __builtin_amdgcn_readlane(c[k], at);
+        if (bin == 252 - 4 * at + k && above + here < equals) above += here, --bin;
+      }
+      least |= (uint32_t)bin << shift;
+      equals -= above;
     }
-    equals = want - above;
   }
 
-  // ---- places
-  int placed = 0, equal_before = 0;
-  for (int j0 = 0; j0 < n; j0 += kChunk) {
+  // ---- places: of those that stay for certain, and of those that equal the least, of which the first `equals` stay
+  int certain_before = 0, same_before = 0, turn = 0;
+  for (int j0 = 0; j0 < n; j0 += kChunk, turn ^= 1) {
     float m[kHeld];
-    bool same[kHeld], keep[kHeld];
-    int before[kHeld];
+    uint64_t certain[kHeld], same[kHeld];
+    const int chunks = min((n - j0 + kThreads - 1) / kThreads, kHeld);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int j = j0 + i * kThreads + tid;
       m[i] = j0 == 0 ? first[i] : j < n ? mass[j] : 0.f;
       const uint32_t u = rising(m[i]);
       const bool may_go = j < old && cut;
-      same[i] = may_go && u == least && want > 0;
-      keep[i] = j < n && (!may_go || (want > 0 && u > least));
+      certain[i] = __ballot(j < n && (!may_go || (want > 0 && u > least)));
+      same[i] = __ballot(may_go && want > 0 && u == least);
+      if (lane == 0) wave_sums[turn][i * kSelectWaves + wave] = make_int2(__popcll(certain[i]), __popcll(same[i]));
     }
-    wait_copies();  // (every mass has been read before the barriers below, behind which they may be overwritten)
-    // of those that equal the least the first stay
-    auto count_before = [&](const bool* flag, int turn, int& carry, int* at) {
-      uint64_t votes[kHeld];
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        votes[i] = __ballot(flag[i]);
-        if (lane == 0) wave_sums[turn][i][wave] = __popcll(votes[i]);
-      }
-      __syncthreads();
-      // the kHeld * kSelectWaves = 128 sums in order: lane l scans sums 2 l and 2 l + 1
-      const int* flat = &wave_sums[turn][0][0];
-      const int x = flat[2 * lane], y = flat[2 * lane + 1], up = wave_scan(x + y);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const int e = i * kSelectWaves + wave;  // (the same in the whole wave)
-        const int through = __shfl(up, e >> 1), last = __shfl(y, e >> 1), first = __shfl(x, e >> 1);
-        at[i] = carry + through - last - (e & 1 ? 0 : first) + __popcll(votes[i] & ((1ull << lane) - 1));
-      }
-      carry += __builtin_amdgcn_readlane(up, 63);
-    };
-    count_before(same, 0, equal_before, before);
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) keep[i] = keep[i] || (same[i] && before[i] < equals);
-    count_before(keep, 1, placed, before);
-    // (places are no later than their tokens; no more than fit, should the masses change under way)
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (keep[i] && before[i] < len.kept) {
-        kept[before[i]] = j0 + i * kThreads + tid;
-        mass_out[before[i]] = m[i];
-      }
+    wait_copies();  // (every mass of the chunk has been read before the barrier, behind which they may be overwritten)
     __syncthreads();
+    // the 128 sums in order: lane l scans sums 2 l and 2 l + 1
+    const int2 x = wave_sums[turn][2 * lane], y = wave_sums[turn][2 * lane + 1];
+    const int certain_up = wave_scan(x.x + y.x), same_up = wave_scan(x.y + y.y);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (i >= chunks) break;
+      const int e = i * kSelectWaves + wave, at = e >> 1;  // (the same in the whole wave)
+      auto before = [&](int up, int x1, int y1, uint64_t votes) {
+        const int sums = __builtin_amdgcn_readlane(up, at) - __builtin_amdgcn_readlane(y1, at) - (e & 1 ? 0 : __builtin_amdgcn_readlane(x1, at));
+        return sums + __popcll(votes & ((1ull << lane) - 1));
+      };
+      const int c = certain_before + before(certain_up, x.x, y.x, certain[i]), s = same_before + before(same_up, x.y, y.y, same[i]);
+      const bool keep = (certain[i] >> lane & 1) || ((same[i] >> lane & 1) && s < equals);
+      const int place = c + min(s, equals);
+      // (places are no later than their tokens; no more than fit, should the masses change under way)
+      if (keep && place < len.kept) {
+        kept[place] = j0 + i * kThreads + tid;
+        mass_out[place] = m[i];
+      }
+    }
+    certain_before += __builtin_amdgcn_readlane(certain_up, 63);
+    same_before += __builtin_amdgcn_readlane(same_up, 63);
   }
+  __syncthreads();  // (the last chunk's masses have been read)
   for (int j = len.kept + tid; j < a.width; j += kThreads) mass_out[j] = 0.f;
   for (int j = len.kept + tid; j < a.budget; j += kThreads) kept[j] = -1;
   if (tid == 0) a.lens_out[b] = len.kept;
