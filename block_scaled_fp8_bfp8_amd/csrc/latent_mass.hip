@@ -233,21 +233,33 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
       v16f lat, rot;
 #pragma unroll
       for (int j = 0; j < 16; ++j) lat[j] = rot[j] = 0.f;
+      // 16 bytes of codes are two products, then of the rotary part one. They are read four steps ahead, in an order that is held to (left
+      // to itself the compiler reads them just before their products, which then wait).
+      constexpr int kSteps = 20, kAhead = 4;
+      v4i ring[kAhead];
+      auto read = [&](int s) __attribute__((always_inline)) {
+        const int block = s < 16 ? s >> 2 : 4, pair = s < 16 ? (s >> 1) & 1 : (s >> 1) - 8;
+        ring[s % kAhead] = *reinterpret_cast<const v4i*>(tile + (s & 1 ? key_second : key_first) + block * kBlockBytes + pair * 64);
+      };
+      auto product = [&](v16f& sum, const v8bf& key, int step) __attribute__((always_inline)) {
+        sum = kWeights ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[step], key, sum, 0, 0, 0)
+                       : __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[step], sum, 0, 0, 0);
+      };
 #pragma unroll
-      for (int s = 0; s < 16; ++s) {  // 16 bytes of codes: two products
-        const v4i k = *reinterpret_cast<const v4i*>(tile + (s & 1 ? key_second : key_first) + (s >> 2) * kBlockBytes + ((s >> 1) & 1) * 64);
+      for (int s = 0; s < kAhead; ++s) read(s);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v8bf key = codes_bf16(k[2 * h], k[2 * h + 1]);
-          lat = kWeights ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[2 * s + h], key, lat, 0, 0, 0)
-                         : __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[2 * s + h], lat, 0, 0, 0);
+      for (int s = 0; s < kSteps; ++s) {
+        const v4i k = ring[s % kAhead];
+        if (s < 16) {
+          const v8bf lo = codes_bf16(k[0], k[1]), hi = codes_bf16(k[2], k[3]);
+          if (s + kAhead < kSteps) read(s + kAhead);
+          product(lat, lo, 2 * s);
+          product(lat, hi, 2 * s + 1);
+        } else {
+          product(rot, __builtin_bit_cast(v8bf, k), 16 + s);
+          if (s + kAhead < kSteps) read(s + kAhead);
         }
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const v8bf key = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4i*>(tile + (s & 1 ? key_second : key_first) + 4 * kBlockBytes + (s >> 1) * 64));
-        rot = kWeights ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[32 + s], key, rot, 0, 0, 0)
-                       : __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[32 + s], rot, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (kWeights) {
         const float unit = map_scale[i * kTile + r];
