@@ -97,8 +97,9 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
   const int last_tok = uniform((work.block * kRows + rows - 1) / a.H);
   const int keys = min(sees(seq, last_tok), reach);
   const int tiles = (keys + kTile - 1) / kTile;
-  const int t_begin = uniform((int)((int64_t)tiles * work.part / work.parts));
-  const int t_end = uniform((int)((int64_t)tiles * (work.part + 1) / work.parts));
+  const int even = tiles / work.parts, odd = tiles - even * work.parts;  // (the first parts take one tile more)
+  const int t_begin = uniform(even * work.part + min(work.part, odd));
+  const int t_end = uniform(t_begin + even + (work.part < odd ? 1 : 0));
   // keys that every row of the wave sees: tiles before need no mask
   const int all = uniform(wave * 32 + 32 <= rows ? limit : 0);
   const float c = a.scale * 1.44269504088896341f;
@@ -311,92 +312,112 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
 
 // The keys of a workgroup of the last launch.
 constexpr int kSumKeys = 256;
+constexpr int sum_keys(bool more) { return more ? kSumKeys / 2 : kSumKeys; }
 
-// What the masses become. tokens that are new in this call start at zero; past the sequence there are none.
-__device__ __forceinline__ void store_mass(const LatentMassArgs& args, const Seq& seq, int b, int key, int reach, float total) {
-  if (key >= args.width) return;
-  const float before = args.mass_in != nullptr && key < seq.len - seq.n ? args.mass_in[(int64_t)b * args.in_stride + key] : 0.f;
-  args.mass[(int64_t)b * args.out_stride + key] = key < min(seq.len, reach) ? before + total : 0.f;
+// The mass that a token had: none if it is new in this call, and none is past the sequence.
+__device__ __forceinline__ float mass_before(const LatentMassArgs& args, const Seq& seq, int b, int key) {
+  return args.mass_in != nullptr && key < min(seq.len - seq.n, args.width) ? args.mass_in[(int64_t)b * args.in_stride + key] : 0.f;
+}
+__device__ __forceinline__ void store_mass(const LatentMassArgs& args, const Seq& seq, int b, int key, int reach, float mass) {
+  if (key < args.width) args.mass[(int64_t)b * args.out_stride + key] = key < min(seq.len, reach) ? mass : 0.f;
 }
 
-// Weights from the scores: lanes hold 4 keys each, the four waves take every fourth row. The first scores are on their way
-// while the rows' sums are joined.
+// Weights from the scores: lanes hold 4 keys each (2 of sequences with many rows, whose workgroups then read half as much), the four waves
+// take every fourth row, kTogether rows at a time. Bound by latency: what
+// does not depend on anything else is asked for at once, the masses that were there and the first scores before the rows' sums are
+// joined, and the scores of the next rows (where there are more) before these rows' weights are formed.
+template <int kTogether, bool kMore>
 __global__ __launch_bounds__(256) void latent_sum_kernel(LatentMassArgs args) {
-  constexpr int kTogether = 8;
+  constexpr int kVec = sum_keys(kMore) / 64;
+  typedef float vec __attribute__((ext_vector_type(kVec)));
   const LatentAttnArgs& a = args.work;
   __shared__ float row_lse[kRows];
   __shared__ int row_limit[kRows];
   __shared__ float2 joined[256];
-  __shared__ __attribute__((aligned(16))) v4f sums[3][64];
+  __shared__ __attribute__((aligned(16))) vec sums[4][64];
   const int b = (int)(blockIdx.x / (unsigned)args.each), first = (int)(blockIdx.x - (unsigned)b * args.each);
+  const int2 parts = args.first[b];  // (not set where a sequence has no rows)
   const Seq seq = sequence(a, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t rows = (int64_t)seq.n * a.H, row0 = (int64_t)seq.q0 * a.H;
   const int reach = reach_of(a), keys = min(seq.len, reach), blocks = (int)((rows + kRows - 1) / kRows);
-  const int2 parts = rows > 0 ? args.first[b] : make_int2(0, 1);
-  for (int k0 = first * kSumKeys; k0 < args.width; k0 += args.each * kSumKeys) {
-    const int key = k0 + lane * 4;
-    v4f total = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = first * 64 * kVec; k0 < args.width; k0 += args.each * 64 * kVec) {
+    const int key = k0 + lane * kVec;
+    const float before = tid < 64 * kVec ? mass_before(args, seq, b, k0 + tid) : 0.f;
+    vec total = 0.f;
     for (int blk = 0; blk < blocks && k0 < keys; ++blk) {
       const int id = parts.x + blk * parts.y, count = (int)min(rows - (int64_t)blk * kRows, (int64_t)kRows);
       if (id < 0 || parts.y < 1 || parts.y > args.ids - id) break;  // (starts that are not rising)
       const float* from = args.scores + (row0 + (int64_t)blk * kRows) * args.pitch + key;
-      v4f x[kTogether];
-      auto read = [&](int p) {  // (what no key of the row's block filled is not used below)
+      vec x[kMore ? 2 : 1][kTogether];
+      auto read = [&](int p, vec* to) __attribute__((always_inline)) {  // (what no key of the row's block filled is not used below)
 #pragma unroll
         for (int i = 0; i < kTogether; ++i)
-          if (p + 4 * i < count && key < keys) x[i] = *reinterpret_cast<const v4f*>(from + (int64_t)(p + 4 * i) * args.pitch);
+          if (p + 4 * i < count && key < keys) to[i] = *reinterpret_cast<const vec*>(from + (int64_t)(p + 4 * i) * args.pitch);
       };
-      read(wave);
+      read(wave, x[0]);
       // ---- the rows' sums: 2 to 16 threads a row take every so many parts, then one joins theirs
       const int held = count > 64 ? 128 : count > 32 ? 64 : count > 16 ? 32 : 16, ways = 256 / held;
-      const int row = tid & (held - 1), way = tid / held;
+      const int of = tid & (held - 1), way = tid / held;
       float m = kNone, l = 0.f;
-      const float2* from_stats = args.stats + (int64_t)id * kRows + min(row, count - 1);
-      for (int i = way; i < parts.y; i += 4 * ways) {
-        float2 f[4];
+      const float2* from_stats = args.stats + (int64_t)id * kRows + min(of, count - 1);
+      constexpr int kBatch = kMore ? 12 : 4;
+      for (int i = way; i < parts.y; i += kBatch * ways) {
+        float2 f[kBatch];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = from_stats[(int64_t)min(i + j * ways, parts.y - 1) * kRows];
+        for (int j = 0; j < kBatch; ++j) f[j] = from_stats[(int64_t)min(i + j * ways, parts.y - 1) * kRows];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kBatch; ++j)
           if (i + j * ways < parts.y) join(m, l, f[j].x, f[j].y);
       }
       joined[tid] = make_float2(m, l);
-      __syncthreads();
+      lds_barrier();
       if (tid < count) {
         for (int i = 1; i < ways; ++i) {
           const float2 f = joined[i * held + tid];
           join(m, l, f.x, f.y);
         }
-        const int limit = sees(seq, (int)(((int64_t)blk * kRows + tid) / a.H));
+        const int limit = sees(seq, (blk * kRows + tid) / a.H);
         row_lse[tid] = log_sum(m, l, limit, reach);
         row_limit[tid] = min(limit, reach);
       }
-      __syncthreads();
-      for (int p = wave; p < count; p += 4 * kTogether) {
-        if (p > wave) read(p);
+      lds_barrier();
+      auto add = [&](int p, const vec* y) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
           const int at = min(p + 4 * i, count - 1);
           const float lse = row_lse[at];
           const int limit = p + 4 * i < count ? row_limit[at] : 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float w = __builtin_amdgcn_exp2f(x[i][j] - lse);
+          for (int j = 0; j < kVec; ++j) {
+            const float w = __builtin_amdgcn_exp2f(y[i][j] - lse);
             total[j] += key + j < limit ? w : 0.f;
           }
         }
+      };
+      constexpr int kStep = 4 * kTogether;
+      if constexpr (kMore) {
+        for (int p = wave; p < count; p += 2 * kStep) {
+          read(p + kStep, x[1]);
+          add(p, x[0]);
+          read(p + 2 * kStep, x[0]);
+          add(p + kStep, x[1]);
+        }
+      } else {
+        for (int p = wave; p < count; p += kStep) {
+          if (p > wave) read(p, x[0]);
+          add(p, x[0]);
+        }
       }
-      __syncthreads();
+      lds_barrier();
     }
-    if (wave > 0) sums[wave - 1][lane] = total;
-    __syncthreads();
-    if (wave == 0) {
-      total += sums[0][lane] + sums[1][lane] + sums[2][lane];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) store_mass(args, seq, b, key + j, reach, total[j]);
+    sums[wave][lane] = total;
+    lds_barrier();
+    if (tid < 64 * kVec) {
+      const float* flat = reinterpret_cast<const float*>(sums) + tid;
+      store_mass(args, seq, b, k0 + tid, reach, before + ((flat[0] + flat[64 * kVec]) + (flat[128 * kVec] + flat[192 * kVec])));
     }
-    __syncthreads();
+    lds_barrier();
   }
 }
 
@@ -416,7 +437,7 @@ __global__ __launch_bounds__(kSumKeys) void latent_blocks_kernel(LatentMassArgs 
 #pragma unroll 4
       for (int64_t i = from; i < blocks; ++i) total += p[i * args.pitch];
     }
-    store_mass(args, seq, b, key, reach, total);
+    store_mass(args, seq, b, key, reach, mass_before(args, seq, b, key) + total);
   }
 }
 
@@ -457,11 +478,13 @@ hipError_t launch_latent_mass(LatentMassArgs args, const LatentMassPlan& plan, h
     if (e == hipSuccess && !plan.keeps_scores) e = launch_pass<Pass::kWeights>(args, plan.ids, stream);
   }
   if (e != hipSuccess || args.width < 1) return e;
-  // Workgroups a sequence: one for every 256 columns, but a page table may reach much further than its sequences do.
-  const int64_t columns = (args.width + kSumKeys - 1) / kSumKeys;
+  // Workgroups a sequence: one for its columns' every 128 or 256, but a page table may reach much further than its sequences do.
+  const bool sum = a.T > 0 && plan.keeps_scores, more = sum && (int64_t)a.T * a.H > 32 * (int64_t)a.B;
+  const int64_t columns = (args.width + sum_keys(more) - 1) / sum_keys(more);
   args.each = (int)std::min<int64_t>(columns, 8192 / a.B + 1);
   const dim3 grid((unsigned)(args.each * a.B));
-  if (a.T > 0 && plan.keeps_scores) hipLaunchKernelGGL(latent_sum_kernel, grid, dim3(256), 0, stream, args);
+  if (more) hipLaunchKernelGGL((latent_sum_kernel<8, true>), grid, dim3(256), 0, stream, args);
+  else if (sum) hipLaunchKernelGGL((latent_sum_kernel<4, false>), grid, dim3(256), 0, stream, args);
   else hipLaunchKernelGGL(latent_blocks_kernel, grid, dim3(kSumKeys), 0, stream, args);
   return hipGetLastError();
 }
