@@ -625,9 +625,11 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
  *   mass_in   NULL: zeros; may be mass_out
  *   width     columns of mass_in and mass_out, at least table_width * page_size
  *   T == 0    is allowed: mass_in is copied, with zeros past each sequence
- *   workspace bfp8_latent_attention_mass_workspace_bytes bytes, 256-byte aligned: that of
- *             bfp8_latent_attention, then 8 bytes for every query row and 128 keys of
- *             table_width * page_size, and 4 a query row
+ *   workspace bfp8_latent_attention_mass_workspace_bytes bytes, 256-byte aligned, contents arbitrary:
+ *             that of bfp8_latent_attention, at most 1 KB for each of T * H / 128 + B + 512 parts of the
+ *             work, 8 bytes a sequence, and 4 bytes for every token that a page table reaches and
+ *             every query row (while sequences have 128 rows or fewer on average and that is
+ *             512 MB or less; then scores are kept) or every 128 of them
  *
  * bfp8_latent_cache_evict: a sequence longer than `budget` keeps its last `recent` tokens and, of
  * the earlier ones, the budget - recent with the largest mass (NaN above all others, of equal ones

@@ -51,10 +51,13 @@ def test_mass_rejections(lib, kw, status):
 def test_mass_workspace(lib):
     size, attention = lib.bfp8_latent_attention_mass_workspace_bytes, lib.bfp8_latent_attention_workspace_bytes
     assert size(0, 4, 16, 256) == 0 and size(4, 4, 0, 256) == 0 and size(4, 4, 16, -1) == 0
-    for t, b, h, keys in ((4, 4, 16, 256), (1, 1, 128, 4096), (300, 6, 128, 3501), (5, 5, 7, 0)):
+    for t, b, h, keys in ((4, 4, 16, 256), (1, 1, 128, 4096), (300, 6, 128, 3501), (5, 5, 7, 0), (64, 64, 16, 1 << 20), (2048, 3, 128, 8192)):
         rest = size(t, b, h, keys) - attention(t, b, h, keys)
-        need = 8 * t * h * -(-keys // 128) + 4 * t * h
-        assert need <= rest <= need + 3 * 256
+        pitch = -(-keys // 32) * 32
+        scores = 4 * t * h * pitch
+        kept = t * h <= 128 * b and scores <= 512 << 20
+        need = scores if kept else 4 * (t * h // 128 + b + 1) * pitch
+        assert need <= rest <= need + 1024 * (t * h // 128 + b + 512 + 16) + 8 * b + 4 * 256
 
 
 def _evict(lib, rows=P[1], ps=64 * 640, sc=P[2], ss=64, pages=10, page=64, table=P[3], ts=4, tw=4, lens=P[4], B=4, m=P[5], ms=256,
