@@ -1146,7 +1146,7 @@ def latent_attention_mass(q: torch.Tensor, cache: torch.Tensor, scales: torch.Te
     elif t != b:
         raise ValueError(f"without cu_q every sequence has one query token, got {t} tokens and {b} sequences")
     if out is None:
-        out = torch.empty((t, heads, LATENT_DIM), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(t, heads, LATENT_DIM, dtype=torch.bfloat16, device=q.device)
     else:
         _require(out, "out", torch.bfloat16, 3)
         if out.shape != (t, heads, LATENT_DIM) or out.stride(2) != 1:
@@ -1154,7 +1154,7 @@ def latent_attention_mass(q: torch.Tensor, cache: torch.Tensor, scales: torch.Te
     columns = reach if mass is None and out_mass is None else (out_mass if mass is None else mass).shape[-1]
     in_stride = columns if mass is None else _mass_arg(mass, "mass", b, reach)
     if out_mass is None:
-        out_mass = torch.empty((b, columns), dtype=torch.float32, device=q.device)
+        out_mass = torch.empty(b, columns, dtype=torch.float32, device=q.device)
     out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
     _same_device(q, cache=cache, page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, out=out, mass=mass,
                  out_mass=out_mass, workspace=workspace)
@@ -1197,11 +1197,11 @@ def latent_cache_evict(cache: torch.Tensor, scales: torch.Tensor, page_table: to
         if out_table.shape[0] != b or to_width == 0:
             raise ValueError(f"out_table must have {b} rows of pages, got shape {tuple(out_table.shape)}")
     if out_mass is None:
-        out_mass = torch.empty((b, columns), dtype=torch.float32, device=cache.device)
+        out_mass = torch.empty(b, columns, dtype=torch.float32, device=cache.device)
     out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
     _same_device(cache, page_table=page_table, seq_lens=seq_lens, mass=mass, out_table=out_table, out_mass=out_mass)
-    kept = torch.empty((b, budget), dtype=torch.int32, device=cache.device)
-    lens = torch.empty((b,), dtype=torch.int32, device=cache.device)
+    kept = torch.empty(b, budget, dtype=torch.int32, device=cache.device)
+    lens = torch.empty(b, dtype=torch.int32, device=cache.device)
     _call(cache.device, "bfp8_latent_cache_evict", rows, ps, sc, ss, pages, page, table, ts, width, seq_lens.data_ptr(), b,
           mass.data_ptr(), in_stride, columns, budget, recent, to, to_stride, to_width, kept.data_ptr(), lens.data_ptr(),
           out_mass.data_ptr(), out_stride)
@@ -1230,6 +1230,16 @@ def _int8_weight(w_q: torch.Tensor, w_s: torch.Tensor, bias: torch.Tensor | None
     return n
 
 
+def _int8_out(out: torch.Tensor | None, m: int, n: int, dtype, device) -> tuple[torch.Tensor, int]:
+    """An output [M, N], made if there is none, and its row stride."""
+    if out is None:
+        return torch.empty(m, n, dtype=dtype, device=device), n
+    _require(out, "out", dtype, 2)
+    if out.shape != (m, n) or (n > 1 and out.stride(1) != 1):
+        raise ValueError(f"out must be [{m}, {n}] with contiguous rows")
+    return out, _row_stride(out, 1)
+
+
 def _row_stride(t: torch.Tensor, step: int) -> int:
     """Row stride of a matrix; a single row's carries no meaning (its length, rounded up to `step`)."""
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // step) * step
@@ -1243,22 +1253,24 @@ def quant_act_int8(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch
     scale a channel."""
     dt = _in_dtype(x, "quant_act_int8")
     _require(x, "x", x.dtype, 2)
+    (m, k), device = x.shape, x.device
     if x.stride(1) != 1:
         raise ValueError("x must be K-contiguous")
-    m, k = x.shape
+    ldq = k
     if q is None:
-        q = torch.empty((m, k), dtype=torch.int8, device=x.device)
+        q = torch.empty(m, k, dtype=torch.int8, device=device)
     else:
         _require(q, "q", torch.int8, 2)
         if q.shape != (m, k) or q.stride(1) != 1:
             raise ValueError(f"q must be [{m}, {k}] and K-contiguous")
+        _same_device(x, q=q)
+        ldq = _row_stride(q, 16)
     if scales is None:
-        scales = torch.empty((m,), dtype=torch.float32, device=x.device)
+        scales = torch.empty(m, dtype=torch.float32, device=device)
     else:
         _int8_scales(scales, "scales", m)
-    _same_device(x, q=q, scales=scales)
-    _call(x.device, "bfp8_quant_act_int8", x.data_ptr(), dt, m, k, _row_stride(x, 8), q.data_ptr(), _row_stride(q, 16),
-          scales.data_ptr())
+        _same_device(x, scales=scales)
+    _call(device, "bfp8_quant_act_int8", x.data_ptr(), dt, m, k, _row_stride(x, 8), q.data_ptr(), ldq, scales.data_ptr())
     return q, scales
 
 
@@ -1276,17 +1288,12 @@ def gemm_int8(a_q: torch.Tensor, a_s: torch.Tensor, w_q: torch.Tensor, w_s: torc
     if a_q.stride(1) != 1:
         raise ValueError("a_q must be K-contiguous")
     _int8_scales(a_s, "a_s", m)
-    n = _int8_weight(w_q, w_s, bias, k, dtype)
-    if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=a_q.device)
-    else:
-        _require(out, "out", dtype, 2)
-        if out.shape != (m, n) or (n > 1 and out.stride(1) != 1):
-            raise ValueError(f"out must be [{m}, {n}] with contiguous rows")
+    n, device = _int8_weight(w_q, w_s, bias, k, dtype), a_q.device
+    out, ldc = _int8_out(out, m, n, dtype, device)
     _same_device(a_q, a_s=a_s, w_q=w_q, w_s=w_s, bias=bias, out=out)
-    _call(a_q.device, "bfp8_gemm_int8", a_q.data_ptr(), _row_stride(a_q, 16), a_s.data_ptr(), w_q.data_ptr(),
+    _call(device, "bfp8_gemm_int8", a_q.data_ptr(), _row_stride(a_q, 16), a_s.data_ptr(), w_q.data_ptr(),
           _row_stride(w_q, 16), w_s.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
-          _IN_DTYPES[dtype], _row_stride(out, 1), m, n, k)
+          _IN_DTYPES[dtype], ldc, m, n, k)
     return out
 
 
@@ -1310,22 +1317,17 @@ def linear_int8(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, bias: tor
     if x.stride(1) != 1:
         raise ValueError("x must be K-contiguous")
     m, k = x.shape
-    n = _int8_weight(w_q, w_s, bias, k, x.dtype)
-    if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    else:
-        _require(out, "out", x.dtype, 2)
-        if out.shape != (m, n) or (n > 1 and out.stride(1) != 1):
-            raise ValueError(f"out must be [{m}, {n}] with contiguous rows")
+    n, device = _int8_weight(w_q, w_s, bias, k, x.dtype), x.device
+    out, ldc = _int8_out(out, m, n, x.dtype, device)
     _same_device(x, w_q=w_q, w_s=w_s, bias=bias, out=out, workspace=workspace)
     if workspace is None:
-        ws_ptr, ws_bytes, workspace = _workspace(x.device, linear_int8_workspace_bytes(m, k))
+        ws_ptr, ws_bytes, workspace = _workspace(device, linear_int8_workspace_bytes(m, k))
     else:
         _require(workspace, "workspace", torch.uint8, 1)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
-    _call(x.device, "bfp8_linear_int8", x.data_ptr(), _IN_DTYPES[x.dtype], m, k, _row_stride(x, 8), w_q.data_ptr(),
+    _call(device, "bfp8_linear_int8", x.data_ptr(), _IN_DTYPES[x.dtype], m, k, _row_stride(x, 8), w_q.data_ptr(),
           _row_stride(w_q, 16), w_s.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
-          _row_stride(out, 1), n, ws_ptr or None, ws_bytes)
+          ldc, n, ws_ptr or None, ws_bytes)
     return out
 
 
