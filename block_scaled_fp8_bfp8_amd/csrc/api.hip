@@ -1147,7 +1147,7 @@ namespace {
 // The arguments that both entries of the bounded cache share.
 bfp8_status_t check_mass(int64_t B, int64_t page_size, int64_t table_width, const int32_t* lens, int64_t width,
                          const float* mass_in, int64_t in_stride, const float* mass_out, int64_t out_stride) {
-  if (B > (int64_t)1 << 24) return fail(BFP8_ERR_UNSUPPORTED, "more than 2^24 sequences");
+  if (B > (int64_t)1 << 19) return fail(BFP8_ERR_UNSUPPORTED, "more than 2^19 sequences");  // (a launch has fewer than 2^32 threads)
   if (table_width > 0 && page_size > INT32_MAX / table_width)
     return fail(BFP8_ERR_UNSUPPORTED, "a page table reaches 2^31 tokens or more");
   if (!lens) return fail(BFP8_ERR_INVALID_ARGUMENT, "seq_lens must not be NULL");
@@ -1284,10 +1284,7 @@ bfp8_status_t check_int8_sizes(int64_t M, int64_t N, int64_t K) {
   if (K < 1) return fail(BFP8_ERR_INVALID_ARGUMENT, "K = %lld must be >= 1", (long long)K);
   if (K % 16 != 0) return fail(BFP8_ERR_UNSUPPORTED, "K = %lld is not a multiple of 16", (long long)K);
   if (K > bfp8::kInt8MaxK) return fail(BFP8_ERR_UNSUPPORTED, "K = %lld is more than %d", (long long)K, bfp8::kInt8MaxK);
-  if (M > kMaxDim || N > kMaxDim) return fail(BFP8_ERR_UNSUPPORTED, "M and N must each be at most 2^30");
-  if (((M + 63) / 64) * ((N + 63) / 64) > (int64_t)INT32_MAX)
-    return fail(BFP8_ERR_UNSUPPORTED, "M x N = %lld x %lld has more output tiles than one launch grid holds",
-                (long long)M, (long long)N);
+  if (M > kMaxDim || N > (int64_t)1 << 26) return fail(BFP8_ERR_UNSUPPORTED, "M must be at most 2^30, N at most 2^26");
   return BFP8_OK;
 }
 
@@ -1315,6 +1312,10 @@ bfp8_status_t check_gemm_int8(const int8_t* a, int64_t lda, const float* as, con
     return fail(BFP8_ERR_UNSUPPORTED, "out_dtype %d is not BFP8_IN_BF16 or BFP8_IN_F16", out_dtype);
   const bfp8_status_t st = check_int8_sizes(M, N, K);
   if (st != BFP8_OK) return st;
+  // (a launch has fewer than 2^32 threads)
+  if (((M + 63) / 64) * ((N + 63) / 64) > (int64_t)1 << 23)
+    return fail(BFP8_ERR_UNSUPPORTED, "M x N = %lld x %lld has more output tiles than one launch grid holds",
+                (long long)M, (long long)N);
   if (!b || !bs) return fail(BFP8_ERR_INVALID_ARGUMENT, "b and bs must not be NULL");
   if (M > 0 && (!a || !as || !c)) return fail(BFP8_ERR_INVALID_ARGUMENT, "a, as and c must not be NULL when M > 0");
   if (lda < K) return fail(BFP8_ERR_INVALID_ARGUMENT, "lda = %lld < K = %lld", (long long)lda, (long long)K);

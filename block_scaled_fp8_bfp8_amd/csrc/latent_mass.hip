@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
   __shared__ __attribute__((aligned(16))) int row_limit[kRows];
   __shared__ float sums[2][4][kTile];
   Work work;
-  if (!find_work<kRows, kTile>(a, work)) return;
+  if (!find_work<kRows, kTile, 8>(a, work)) return;  // (more than 512 sequences are not cut, so none is looked at often)
   if (work.id - work.part + work.parts > args.ids) return;  // (starts that are not rising)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, g = lane >> 5;

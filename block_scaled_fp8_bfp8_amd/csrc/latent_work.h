@@ -40,10 +40,9 @@ struct Work {
   int id;  // of all parts (a block's are neighbours)
 };
 
-// Every wave cuts the work in the same way and picks its workgroup's part. False: there is none.
-template <int kBM, int kTile>
+// Every wave cuts the work in the same way and picks its workgroup's part. False: there is none. kHeld: sequences of a lane that are read once.
+template <int kBM, int kTile, int kHeld = 4>
 __device__ __forceinline__ bool find_work(const LatentAttnArgs& a, Work& work) {
-  constexpr int kHeld = 4;   // sequences of a lane that are read once
   constexpr int kMany = 1 << 16;  // more parts than ever run at once: sums of 64 such stay in range
   const int lane = threadIdx.x & 63;
   const int per = (a.B + 63) / 64;

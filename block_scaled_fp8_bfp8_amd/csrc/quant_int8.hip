@@ -56,8 +56,14 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * 64) void quant_int8_ke
 template <int kIn, int kWaves, int kChunks>
 void run(const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ldq, float* s, hipStream_t stream) {
   constexpr int kRows = kWaves == 1 ? 4 : 1;
-  hipLaunchKernelGGL((quant_int8_kernel<kIn, kWaves, kChunks>), dim3((unsigned)((M + kRows - 1) / kRows)),
-                     dim3(kWaves == 1 ? 256 : kWaves * 64), 0, stream, x, ldx * (kIn == kInF32 ? 4 : 2), q, ldq, s, (int)M, (int)K);
+  constexpr int64_t kMost = (int64_t)1 << 21;  // rows a launch: its threads stay below 2^32
+  const int64_t row_bytes = ldx * (kIn == kInF32 ? 4 : 2);
+  for (int64_t m = 0; m < M; m += kMost) {
+    const int64_t rows = M - m < kMost ? M - m : kMost;
+    hipLaunchKernelGGL((quant_int8_kernel<kIn, kWaves, kChunks>), dim3((unsigned)((rows + kRows - 1) / kRows)),
+                       dim3(kWaves == 1 ? 256 : kWaves * 64), 0, stream, static_cast<const uint8_t*>(x) + m * row_bytes, row_bytes,
+                       q + m * ldq, ldq, s + m, (int)rows, (int)K);
+  }
 }
 
 // By the row's length alone: a wave for every 512 elements, eight at most up to 8192.

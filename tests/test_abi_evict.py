@@ -24,7 +24,7 @@ SHARED = [
     (dict(table=None), E_INV), (dict(tw=-1), E_INV), (dict(ts=3), E_INV), (dict(lens=None), E_INV), (dict(lens=P[4] + 2), E_MIS),
     (dict(width=255), E_INV), (dict(width=(1 << 31) - 1, ms=1 << 31, mos=1 << 31), E_UNS), (dict(mo=None), E_INV), (dict(mos=255), E_INV),
     (dict(ms=255), E_INV), (dict(m=P[5] + 2), E_MIS), (dict(mo=P[6] + 2), E_MIS), (dict(tw=1 << 28, ts=1 << 28), E_UNS),
-    (dict(B=(1 << 24) + 1), E_UNS),
+    (dict(B=(1 << 24) + 1), E_UNS), (dict(B=(1 << 19) + 1), E_UNS),
 ]
 
 

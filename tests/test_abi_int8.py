@@ -42,7 +42,7 @@ def _gemm(lib, a=P1, lda=256, as_=P2, b=P3, ldb=256, bs=P4, bias=P5, c=P6, dt=BF
 
 GEMM = [
     (dict(M=-1), E_INV), (dict(N=0), E_INV), (dict(K=0), E_INV), (dict(K=8), E_UNS), (dict(K=65552, lda=65552, ldb=65552), E_UNS),
-    (dict(M=(1 << 30) + 1), E_UNS), (dict(N=(1 << 30) + 1, ldc=1 << 31), E_UNS), (dict(M=1 << 30, N=1 << 20, ldc=1 << 20), E_UNS),
+    (dict(M=(1 << 30) + 1), E_UNS), (dict(N=(1 << 30) + 1, ldc=1 << 31), E_UNS), (dict(M=1 << 30, N=1 << 20, ldc=1 << 20), E_UNS), (dict(N=(1 << 26) + 1, ldc=1 << 27), E_UNS), (dict(M=1 << 30, N=1), E_UNS),
     (dict(b=None), E_INV), (dict(bs=None), E_INV), (dict(c=None), E_INV), (dict(ldb=240), E_INV), (dict(ldc=63), E_INV),
     (dict(ldb=264), E_MIS), (dict(ldb=1 << 23), E_UNS), (dict(ldc=(1 << 30) + 1), E_UNS), (dict(b=P3 + 8), E_MIS),
     (dict(bs=P4 + 2), E_MIS), (dict(bias=P5 + 1), E_MIS), (dict(c=P6 + 1), E_MIS),

@@ -136,6 +136,19 @@ def test_gemm_largest_sums(gpu):
     _check_product(bfp8.gemm_int8(q, s, w, ws), q, s, w, ws, None, "largest, tiled")
 
 
+@pytest.mark.parametrize("m", [3, 200])
+def test_weight_past_4_gib(gpu, m):
+    """Rows of a weight whose bytes lie past 2^32: the last channels against float64, and one in the middle."""
+    n, k = 66000, 65536
+    w = torch.randint(-128, 128, (n, k), dtype=torch.int8, device=gpu)
+    q = torch.randint(-128, 128, (m, k), dtype=torch.int8, device=gpu)
+    s, ws = torch.full((m,), 2.0 ** -10, device=gpu), torch.full((n,), 2.0 ** -10, device=gpu)
+    announce("gemm_int8 past 4 GiB", m)
+    got = bfp8.gemm_int8(q, s, w, ws)
+    for at in (slice(n - 130, n), slice(32768 - 5, 32768 + 5), slice(65536 - 3, 65536 + 3)):
+        _check_product(got[:, at], q, s, w[at], ws[at], None, at)
+
+
 @pytest.mark.parametrize("m", [5, 300])
 def test_gemm_views(gpu, m):
     """Operands with rows apart, whose gaps hold other codes, at the very end of their memory; an output with rows apart

@@ -157,6 +157,30 @@ def test_bad_lengths_and_pages(gpu):
     assert torch.equal(got, want) and torch.equal(got_codes, want_codes)
 
 
+@pytest.mark.parametrize("onto", [False, True])
+def test_far_pages(gpu, onto):
+    """From and to pages past 4 GiB of the cache."""
+    page, pages, n, budget = 64, 110000, 200, 130
+    g = torch.Generator().manual_seed(9)
+    cache = torch.zeros(pages, page, 640, dtype=torch.uint8, device=gpu)
+    scales = torch.zeros(pages, page, dtype=torch.uint8, device=gpu)
+    table = torch.tensor([[pages - 1, 3, pages - 7, 105000]], dtype=torch.int32)
+    to = torch.tensor([[106000, pages - 2, 12]], dtype=torch.int32)
+    rows = torch.randint(0, 256, (4, page, 640), generator=g, dtype=torch.uint8)
+    codes = torch.randint(0, 256, (4, page), generator=g, dtype=torch.uint8)
+    for i, p in enumerate(table[0].tolist()):
+        cache[p], scales[p] = rows[i].to(gpu), codes[i].to(gpu)
+    mass = torch.rand(1, 256, generator=g)
+    announce("latent_cache_evict far pages", onto)
+    bfp8.latent_cache_evict(cache, scales, table.to(gpu), torch.tensor([n], dtype=torch.int32, device=gpu), mass.to(gpu), budget,
+                            recent=20, out_table=to.to(gpu) if onto else None)
+    stay = chosen(mass[0], n, budget, 20)
+    where = (to if onto else table)[0].tolist()
+    for i, j in enumerate(stay):
+        assert torch.equal(cache[where[i // page], i % page].cpu(), rows[j // page, j % page])
+        assert int(scales[where[i // page], i % page]) == int(codes[j // page, j % page])
+
+
 def test_captured(gpu):
     """A captured call follows later masses and lengths."""
     lens, page, budget = [400, 300], 16, 200

@@ -153,11 +153,10 @@ def test_no_new_tokens(gpu):
         assert torch.equal(mass[b, :n], before[b, :n]) and bool((mass[b, n:] == 0).all())
 
 
-@pytest.mark.parametrize("heads,width", [(1, 36), (150, 36), (8, 1 << 14)])
-def test_many_sequences_of_shared_pages(gpu, heads, width):
+@pytest.mark.parametrize("b,length,heads,width", [(520, 2200, 1, 36), (520, 2200, 150, 36), (17, 700, 8, 1 << 14), (300, 700, 16, 11)])
+def test_many_sequences_of_shared_pages(gpu, b, length, heads, width):
     """520 sequences on the pages of one, so that none is cut and each walks more than 2048 keys; a page table that reaches
-    far further than its sequences (2^20 tokens, too many for scores to be kept)."""
-    b, length = (520, 2200) if width == 36 else (17, 700)
+    far further than its sequences (2^20 tokens, too many for scores to be kept); 300 sequences, some of which are cut."""
     c, keys = make(gpu, [length], [1], 1, 64, seed=77)
     table = torch.full((b, width), -1, dtype=torch.int32, device=gpu)
     table[:, :c["table"].shape[1]] = c["table"]
@@ -169,6 +168,24 @@ def test_many_sequences_of_shared_pages(gpu, heads, width):
     some = [0, 1, b // 2, b - 1]
     check(mass[some], None, q[some], keys * 4, [length] * 4, [1] * 4)
     assert bool(((mass.double().sum(dim=1) - heads).abs() <= 2.0 ** -15 * heads).all())
+
+
+def test_far_pages(gpu):
+    """Pages that lie past 4 GiB and 8 GiB of the cache."""
+    lens, heads, page = [300, 77], 16, 64
+    c, keys = make(gpu, lens, [1, 1], heads, page, seed=41)
+    pages = 220000
+    big = torch.empty(pages, page, 640, dtype=torch.uint8, device=gpu)
+    scales = torch.empty(pages, page, dtype=torch.uint8, device=gpu)
+    table = torch.full_like(c["table"], -1)
+    for b, n in enumerate(lens):
+        for i in range(-(-n // page)):
+            to = pages - 1 - 7 * i if b == 0 else 110000 + 3 * i
+            table[b, i] = to
+            big[to], scales[to] = c["cache"][c["table"][b, i]], c["scales"][c["table"][b, i]]
+    announce("latent_attention_mass far pages")
+    _, mass = bfp8.latent_attention_mass(c["q"], big, scales, table, c["lens"], SCALE)
+    check(mass, None, c["q"], keys, lens, [1, 1])
 
 
 def test_captured_beside_eager_calls(gpu):
