@@ -53,15 +53,19 @@ __device__ __forceinline__ bool find_work(const LatentAttnArgs& a, Work& work) {
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     held[k] = {0, 0, 0};
-    if (k < count) held[k] = sequence(a, b0 + k);
+    if (k < per && k < count) held[k] = sequence(a, b0 + k);
   }
+  // (up to 64 sequences are one a lane: nothing else is stepped through)
   auto each = [&](auto f) {
+    if (count > 0) f(b0, held[0], blocks_of(held[0]), tiles_of(held[0]));
+    if (per > 1) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (k < count) f(b0 + k, held[k], blocks_of(held[k]), tiles_of(held[k]));
-    for (int k = kHeld; k < count; ++k) {
-      const Seq q = sequence(a, b0 + k);
-      f(b0 + k, q, blocks_of(q), tiles_of(q));
+      for (int k = 1; k < kHeld; ++k)
+        if (k < count) f(b0 + k, held[k], blocks_of(held[k]), tiles_of(held[k]));
+      for (int k = kHeld; k < count; ++k) {
+        const Seq q = sequence(a, b0 + k);
+        f(b0 + k, q, blocks_of(q), tiles_of(q));
+      }
     }
   };
   auto cut = [](int tiles, int quantum) {  // max(ceil(tiles / quantum), 1)
@@ -76,10 +80,20 @@ __device__ __forceinline__ bool find_work(const LatentAttnArgs& a, Work& work) {
   int quantum = max(a.max_tiles, 1);
   int64_t blocks = 0;
   each([&](int, const Seq&, int n, int) { blocks += n; });
-  const bool rounds = total((int)min(blocks, (int64_t)kMany)) > a.target_parts;  // workgroups run one after the other
+  const int all_blocks = total((int)min(blocks, (int64_t)kMany));
+  const bool rounds = all_blocks > a.target_parts;  // workgroups run one after the other
   if (a.max_slots > 0) {
-    if (total((int)min(blocks, (int64_t)kMany)) < a.target_parts) {
+    if (all_blocks < a.target_parts) {
       int lo = a.min_tiles, hi = max(quantum, lo);
+      // All blocks' tiles S bound it: S / q <= parts <= S / q + blocks. (Tables that reach far further than 2^27 tokens are searched through.)
+      if (quantum < INT32_MAX / a.target_parts) {
+        int tiles_in_all = 0;
+        each([&](int, const Seq&, int n, int tiles) { tiles_in_all += n * tiles; });
+        tiles_in_all = total(tiles_in_all);
+        auto up = [&](int by) { return (int)(((unsigned)tiles_in_all + (unsigned)by - 1u) / (unsigned)by); };
+        lo = min(max(up(a.target_parts), lo), hi);
+        hi = min(max(up(a.target_parts - all_blocks), lo), hi);
+      }
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         int64_t parts = 0;
