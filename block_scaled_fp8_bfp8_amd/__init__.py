@@ -1132,7 +1132,8 @@ def latent_attention_mass(q: torch.Tensor, cache: torch.Tensor, scales: torch.Te
     weights of all new tokens and heads; tokens that are new in this call start from zero, and columns past a
     sequence are zero. out_mass: where to put it (it may be mass itself). T == 0 new tokens are
     allowed (with cu_q). Other arguments as for latent_attention; the workspace is
-    latent_attention_mass_workspace_bytes."""
+    latent_attention_mass_workspace_bytes (up to 512 MB more than latent_attention's while scores are
+    kept: 4 bytes for every query row and token that the page table reaches)."""
     _require(q, "q", torch.bfloat16, 3)
     t, heads, dim = q.shape
     if dim != LATENT_DIM + ROPE_DIM or q.stride(2) != 1:

@@ -438,21 +438,28 @@ hipError_t launch_pass(const LatentMassArgs& args, int64_t grid, hipStream_t str
 
 }  // namespace
 
-// Scores are kept where they take this much at most and a sequence has 128 rows or fewer on average: a score costs 8 bytes of
-// traffic, scoring a key again its 641 bytes and the products.
-constexpr int64_t kMostScores = (int64_t)512 << 20;
+// Scores are kept where this has both sides of it: a score costs 8 bytes of traffic, scoring a key again its 641 bytes and the products of
+// its sequence's blocks. Sequences of 32 rows or fewer (256 x 16 heads, 1000 to 8000 keys: 235 us kept, 366 scored again) keep up to 512 MB,
+// those of up to 512 rows what the MALL holds (us beside the attention, kept and scored again: 8 sequences x 3 tokens x 128 heads 64 and
+// 70, 32 x 3 x 128 heads, 147 MB, 79 and 90; above it 50 x 20 x 16 heads, 256 MB, 142 and 136, and 205 MB come out either way). With more
+// rows the products of all blocks cost less than a last launch that takes a sequence's blocks in turn (4 x 8 tokens x 128 heads
+// 88 and 86, 1 x 16 x 128 heads 92 and 32).
+constexpr int64_t kMostScores = (int64_t)512 << 20, kMostOfMany = (int64_t)192 << 20;
 
 LatentMassPlan plan_latent_mass(int64_t T, int64_t B, int64_t H, int64_t max_keys) {
   auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
   LatentMassPlan p{};
   const int64_t blocks = T * H / kRows + std::min(T, B), tiles = (max_keys + kTile - 1) / kTile;
   p.max_tiles = (int)tiles;
-  p.min_tiles = T * H <= 32 * B || blocks * tiles <= 512 ? 2 : 4;
-  p.target_parts = 512;
+  // Tiles a part at least: 2, or 4 where sequences have more than 64 rows and the parts of 2 would fill the card (us beside the attention
+  // with 2 and 4: 8 sequences of 4000 x 128 heads 29.0 and 26.2, 16 of 1000 to 4000 x 64 heads 25.0 and 27.5, 1 of 1111 x 128 heads 17.4
+  // and 20.5).
+  p.min_tiles = T * H <= 64 * B || blocks * tiles <= 512 ? 2 : 4;
+  p.target_parts = 512;  // two workgroups on every compute unit (1024: 64 x 128 heads 94 us, 85 so, 6 chunks of 40 x 128 heads 185 and 181)
   const int64_t cut = std::min<int64_t>(blocks * std::max<int64_t>((tiles + p.min_tiles - 1) / p.min_tiles, 1), p.target_parts);
   p.ids = (std::max(blocks, cut) + 15) / 16 * 16;
   p.pitch = tiles * kTile;
-  p.keeps_scores = T * H <= kRows * B && T * H <= kMostScores / 4 / std::max<int64_t>(p.pitch, 1);
+  p.keeps_scores = T * H <= 4 * kRows * B && T * H <= (T * H <= 32 * B ? kMostScores : kMostOfMany) / 4 / std::max<int64_t>(p.pitch, 1);
   p.first_bytes = up(B * (int64_t)sizeof(int2));
   p.stats_bytes = up(p.ids * kRows * (int64_t)sizeof(float2));
   p.rest_bytes = up((p.keeps_scores ? T * H : T * H / kRows + B + 1) * p.pitch * (int64_t)sizeof(float));

@@ -44,6 +44,14 @@ def test_quant(gpu, dtype, m, k):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,k", [(2049, 16), (2051, 1008), (2050, 1552), (2053, 2576), (2049, 4096), (2050, 5120), (2051, 5648), (2049, 7168),
+                                 (2050, 7184)])
+def test_quant_many_rows(gpu, dtype, m, k):
+    """One to seven waves a row, and what follows them."""
+    test_quant(gpu, dtype, m, k)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_quant_middles_and_extremes(gpu, dtype):
     """Elements at the exact middle of two codes (ties to even) and next to it, tiny and huge rows, zeros, and rows that
     are not finite."""
