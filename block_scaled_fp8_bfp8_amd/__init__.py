@@ -1113,12 +1113,14 @@ def _lens_arg(lens: torch.Tensor, name: str, b: int):
 def _mass_arg(mass: torch.Tensor, name: str, b: int, reach: int, width: int | None = None) -> int:
     """Checks masses [B, columns] and returns their row stride."""
     _require(mass, name, torch.float32, 2)
-    if mass.shape[0] != b or mass.shape[1] < reach or (width is not None and mass.shape[1] != width):
+    n, columns = mass.shape
+    if n != b or columns < reach or (width is not None and columns != width):
         raise ValueError(f"{name} must be [{b}, {reach if width is None else width}{' or more' if width is None else ''}], "
                          f"got {tuple(mass.shape)}")
-    if mass.shape[1] > 1 and mass.stride(1) != 1:
+    stride, inner = mass.stride()
+    if columns > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return mass.stride(0) if b > 1 else mass.shape[1]
+    return stride if b > 1 else columns
 
 
 def latent_attention_mass(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
@@ -1155,8 +1157,9 @@ def latent_attention_mass(q: torch.Tensor, cache: torch.Tensor, scales: torch.Te
     columns = reach if mass is None and out_mass is None else (out_mass if mass is None else mass).shape[-1]
     in_stride = columns if mass is None else _mass_arg(mass, "mass", b, reach)
     if out_mass is None:
-        out_mass = torch.empty(b, columns, dtype=torch.float32, device=q.device)
-    out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
+        out_mass, out_stride = torch.empty(b, columns, dtype=torch.float32, device=q.device), columns
+    else:
+        out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
     _same_device(q, cache=cache, page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, out=out, mass=mass,
                  out_mass=out_mass, workspace=workspace)
     if workspace is None:
@@ -1189,7 +1192,7 @@ def latent_cache_evict(cache: torch.Tensor, scales: torch.Tensor, page_table: to
     b, reach = page_table.shape[0], width * page
     _lens_arg(seq_lens, "seq_lens", b)
     in_stride = _mass_arg(mass, "mass", b, reach)
-    columns = mass.shape[1]
+    columns, device = mass.shape[1], cache.device
     if budget < 1 or not 0 <= recent <= budget:
         raise ValueError(f"budget must be at least 1 and recent 0 .. budget, got {budget} and {recent}")
     to, to_stride, to_width = None, 0, 0
@@ -1198,12 +1201,14 @@ def latent_cache_evict(cache: torch.Tensor, scales: torch.Tensor, page_table: to
         if out_table.shape[0] != b or to_width == 0:
             raise ValueError(f"out_table must have {b} rows of pages, got shape {tuple(out_table.shape)}")
     if out_mass is None:
-        out_mass = torch.empty(b, columns, dtype=torch.float32, device=cache.device)
-    out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
-    _same_device(cache, page_table=page_table, seq_lens=seq_lens, mass=mass, out_table=out_table, out_mass=out_mass)
-    kept = torch.empty(b, budget, dtype=torch.int32, device=cache.device)
-    lens = torch.empty(b, dtype=torch.int32, device=cache.device)
-    _call(cache.device, "bfp8_latent_cache_evict", rows, ps, sc, ss, pages, page, table, ts, width, seq_lens.data_ptr(), b,
+        _same_device(cache, page_table=page_table, seq_lens=seq_lens, mass=mass, out_table=out_table)
+        out_mass, out_stride = torch.empty(b, columns, dtype=torch.float32, device=device), columns
+    else:
+        out_stride = _mass_arg(out_mass, "out_mass", b, reach, columns)
+        _same_device(cache, page_table=page_table, seq_lens=seq_lens, mass=mass, out_table=out_table, out_mass=out_mass)
+    kept = seq_lens.new_empty(b, budget)
+    lens = seq_lens.new_empty(b)
+    _call(device, "bfp8_latent_cache_evict", rows, ps, sc, ss, pages, page, table, ts, width, seq_lens.data_ptr(), b,
           mass.data_ptr(), in_stride, columns, budget, recent, to, to_stride, to_width, kept.data_ptr(), lens.data_ptr(),
           out_mass.data_ptr(), out_stride)
     return kept, lens, out_mass

@@ -12,6 +12,11 @@
 //   * K-split (few rows; reading the weights is the work): the 8 waves of a workgroup take the K blocks of a small
 //     tile in turn, each from slots of its own, and add their sums through LDS.
 //   * tiled: a workgroup's waves share stages of a K block, two to four of them, with one barrier a block.
+//
+// Measured (cold weights): 8192 x 10240 x 5120 350 us, 2.46 * 10^15 operations a second, bound by power (with operands of zeros, which
+// switch nothing, 280 us; the library's product of the same operands 430); 1000 x 4096 x 4096 22 us, bound by the copies into LDS (256
+// workgroups, one round); 1 x 4096 x 4096 5.9 us and 5 x 5120 x 8192 12.1 (3.5 TB/s), bound by reading the weights once, start-up
+// included; 83 x 576 x 7168 6.9 us, 216 workgroups with 56 K blocks in a chain each.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

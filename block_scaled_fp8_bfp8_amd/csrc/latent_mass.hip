@@ -16,6 +16,11 @@
 // instruction serves both directions: with the keys first a lane holds one row and 16 keys, whose maximum and sum are near;
 // with the rows first it holds one key and 16 rows, whose weights add up in registers. Two workgroups run on a compute unit,
 // so that one's softmax and conversions (128 instructions a tile) run beside the other's products.
+//
+// Measured, beside the attention: 1 sequence of 1111 x 128 heads 11.5 us for the scores (a chain of look-ups, rows and two tiles) and 7.4 for
+// their sum; 64 of 500 to 8000 x 16 heads 38 us (186 MB of rows, 4.9 TB/s) and 12; 6 chunks of 40 x 128 heads 90 us for each of two passes (matrix
+// cores busy 36 % of the clocks: parts of 43 tiles at most where an even share is 33, and a softmax that only another workgroup's products
+// run beside) and 6.
 #include <algorithm>
 
 #include "device_latent.h"
