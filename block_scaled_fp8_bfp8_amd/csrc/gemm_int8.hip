@@ -13,8 +13,8 @@
 //     tile in turn, each from slots of its own, and add their sums through LDS.
 //   * tiled: a workgroup's waves share stages of a K block, two to four of them, with one barrier a block.
 //
-// Measured (cold weights): 8192 x 10240 x 5120 350 us, 2.46 * 10^15 operations a second, bound by power (with operands of zeros, which
-// switch nothing, 280 us; the library's product of the same operands 430); 1000 x 4096 x 4096 22 us, bound by the copies into LDS (256
+// Measured (cold weights): 8192 x 10240 x 5120 345 us, 2.49 * 10^15 operations a second, bound by power (with operands of zeros, which
+// switch nothing, 280 us; the library's product of the same operands 430); 1000 x 4096 x 4096 21 us, bound by the copies into LDS (256
 // workgroups, one round); 1 x 4096 x 4096 5.9 us and 5 x 5120 x 8192 12.1 (3.5 TB/s), bound by reading the weights once, start-up
 // included; 83 x 576 x 7168 6.9 us, 216 workgroups with 56 K blocks in a chain each.
 #include <algorithm>
@@ -462,44 +462,47 @@ __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8Gem
   }
   __syncthreads();
 
-  // result register v of lane l: weight row 8 (v / 4) + 4 (l / 32) + v % 4, activation row l % 32. Where rows of C allow
-  // it, a wave's 32 rows go through LDS (rows padded by 16 bytes) so that whole segments are stored.
+  // result register v of lane l: weight row 8 (v / 4) + 4 (l / 32) + v % 4, activation row l % 32. A wave's 32 rows go through LDS (rows
+  // padded by 16 bytes) so that neighbouring lanes store neighbours of a row: 16 bytes each where rows of C allow it, else 4 or 2 (1569
+  // tokens, 4826 channels, K = 288: 14 us, 31 with the 8 bytes that a lane holds of each row).
   constexpr int kRowBytes = WN * 2 + 16;
   static_assert(kNumWaves * 32 * kRowBytes <= STAGES * kStage, "staged output");
   uint8_t* staged = smem + w * 32 * kRowBytes;
   const bool vec16 = (args.ldc & 7) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 15) == 0;
-  const bool vec8 = (args.ldc & 3) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 7) == 0;
+  const bool vec4 = (args.ldc & 1) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 3) == 0;
 #pragma unroll
   for (int tm = 0; tm < TM; ++tm) {
-    const int m = m0 + wm * WM + tm * 32 + r;
-    const float ms = args.as[min(m, M - 1)];
+    const float ms = args.as[min(m0 + wm * WM + tm * 32 + r, M - 1)];
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int col = tn * 32 + 8 * q + 4 * g, n = n0 + wn * WN + col;
+        const int col = tn * 32 + 8 * q + 4 * g;
         const v4f ns = *reinterpret_cast<const v4f*>(&channel[0][wn * WN + col]);
         const v4f add = *reinterpret_cast<const v4f*>(&channel[1][wn * WN + col]);
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = fmaf((float)acc[tn][tm][4 * q + e] * ms, ns[e], add[e]);
         const uint32_t p0 = pack16<kF16>(y[0], y[1]), p1 = pack16<kF16>(y[2], y[3]);
-        if (vec16) *reinterpret_cast<uint2*>(staged + r * kRowBytes + col * 2) = make_uint2(p0, p1);
-        else if (m < M && n < N) store4(args.c + (int64_t)m * args.ldc + n, n, N, vec8, p0, p1);
+        *reinterpret_cast<uint2*>(staged + r * kRowBytes + col * 2) = make_uint2(p0, p1);
       }
-    if (!vec16) continue;
     // (LDS executes a wave's accesses in order; this keeps the compiler to it)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-    constexpr int kLanes = WN / 8, kPass = 64 / kLanes;  // lanes a row, rows a pass
-#pragma unroll
-    for (int p = 0; p < 32 / kPass; ++p) {
-      const int row = p * kPass + lane / kLanes, seg = lane % kLanes;
-      const v4i v = *reinterpret_cast<const v4i*>(staged + row * kRowBytes + seg * 16);
-      const int mr = m0 + wm * WM + tm * 32 + row, n = n0 + wn * WN + seg * 8;
-      if (mr < M && n < N) {
-        uint16_t* c = args.c + (int64_t)mr * args.ldc + n;
+    // pieces of kUnit columns, a lane each
+    auto rows_out = [&](auto type, auto store) __attribute__((always_inline)) {
+      using T = decltype(type);
+      constexpr int kUnit = sizeof(T) / 2, kLanes = WN / kUnit;
+#pragma unroll 4
+      for (int i = lane; i < 32 * kLanes; i += 64) {
+        const int row = i / kLanes, seg = i % kLanes;
+        const int m = m0 + wm * WM + tm * 32 + row, n = n0 + wn * WN + seg * kUnit;
+        if (m < M && n < N) store(args.c + (int64_t)m * args.ldc + n, n, *reinterpret_cast<const T*>(staged + row * kRowBytes + seg * sizeof(T)));
+      }
+    };
+    if (vec16) {
+      rows_out(v4i{}, [&](uint16_t* c, int n, const v4i& v) {
         if (n + 8 <= N) {
           *reinterpret_cast<v4i*>(c) = v;
         } else {
@@ -507,7 +510,14 @@ __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8Gem
           for (int e = 0; e < 8; ++e)
             if (n + e < N) c[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
         }
-      }
+      });
+    } else if (vec4) {
+      rows_out(uint32_t{}, [&](uint16_t* c, int n, uint32_t v) {
+        if (n + 2 <= N) *reinterpret_cast<uint32_t*>(c) = v;
+        else c[0] = (uint16_t)v;
+      });
+    } else {
+      rows_out(uint16_t{}, [&](uint16_t* c, int, uint16_t v) { c[0] = v; });
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
