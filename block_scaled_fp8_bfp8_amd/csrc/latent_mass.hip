@@ -328,15 +328,18 @@ __device__ __forceinline__ void store_mass(const LatentMassArgs& args, const Seq
 }
 
 // Weights from the scores: the lanes of a wave hold 4 keys each, and four waves take every fourth row, 4 rows at a time. Of sequences with
-// many rows lanes hold 2 keys (kVec) and waves take 8 rows at a time; 16 waves then hold a block's rows all at once. Bound by latency: what does not depend on
-// anything else is asked for at once, the masses that were there and the first scores before the rows' sums are joined.
+// many rows lanes hold 2 keys (kVec) and waves take 8 rows at a time; 16 waves then hold 128 rows all at once and join the sums of 512.
+// Bound by latency: what does not depend on anything else is asked for at once, the masses that were there and the first scores before the
+// rows' sums are joined and, by 16 waves, the next scores before these rows' weights are formed.
 template <int kWaves, int kVec>
 __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs args) {
-  constexpr int kTogether = 16 / kVec, kThreads = 64 * kWaves;
+  constexpr int kTogether = 16 / kVec, kThreads = 64 * kWaves, kAtOnce = kThreads / 2;
+  constexpr bool kAhead = kWaves == 16;  // (with more workgroups a compute unit the registers are worth more: 64 x 16 heads 49 us, 52 so)
+  static_assert(kAtOnce % kRows == 0, "rows at once are whole blocks");
   typedef float vec __attribute__((ext_vector_type(kVec)));
   const LatentAttnArgs& a = args.work;
-  __shared__ float row_lse[kRows];
-  __shared__ int row_limit[kRows];
+  __shared__ float row_lse[kAtOnce];
+  __shared__ int row_limit[kAtOnce];
   __shared__ float2 joined[kThreads];
   __shared__ __attribute__((aligned(16))) vec sums[kWaves][64];
   const int b = (int)(blockIdx.x / (unsigned)args.each), first = (int)(blockIdx.x - (unsigned)b * args.each);
@@ -344,27 +347,28 @@ __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs 
   const Seq seq = sequence(a, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t rows = (int64_t)seq.n * a.H, row0 = (int64_t)seq.q0 * a.H;
-  const int reach = reach_of(a), keys = min(seq.len, reach), blocks = (int)((rows + kRows - 1) / kRows);
+  const int reach = reach_of(a), keys = min(seq.len, reach);
   for (int k0 = first * 64 * kVec; k0 < args.width; k0 += args.each * 64 * kVec) {
     const int key = k0 + lane * kVec;
     const float before = tid < 64 * kVec ? mass_before(args, seq, b, k0 + tid) : 0.f;
     vec total = 0.f;
-    for (int blk = 0; blk < blocks && k0 < keys; ++blk) {
-      const int id = parts.x + blk * parts.y, count = (int)min(rows - (int64_t)blk * kRows, (int64_t)kRows);
-      if (id < 0 || parts.y < 1 || parts.y > args.ids - id) break;  // (starts that are not rising)
-      const float* from = args.scores + (row0 + (int64_t)blk * kRows) * args.pitch + key;
-      vec x[kTogether];
-      auto read = [&](int p) __attribute__((always_inline)) {  // (what no key of the row's block filled is not used below)
+    for (int64_t from_row = 0; from_row < rows && k0 < keys; from_row += kAtOnce) {
+      const int count = (int)min(rows - from_row, (int64_t)kAtOnce), blocks = (count + kRows - 1) / kRows;
+      const int64_t id = parts.x + from_row / kRows * parts.y;
+      if (parts.x < 0 || parts.y < 1 || (int64_t)blocks * parts.y > args.ids - id) break;  // (starts that are not rising)
+      const float* from = args.scores + (row0 + from_row) * args.pitch + key;
+      auto read = [&](int p, vec* x) __attribute__((always_inline)) {  // (what no key of the row's block filled is not used below)
 #pragma unroll
         for (int i = 0; i < kTogether; ++i)
           if (p + kWaves * i < count && key < keys) x[i] = *reinterpret_cast<const vec*>(from + (int64_t)(p + kWaves * i) * args.pitch);
       };
-      read(wave);
+      vec x[kAhead ? 2 : 1][kTogether];
+      read(wave, x[0]);
       // ---- the rows' sums: 2 to 64 threads a row take every so many parts, then one joins theirs
-      const int held = count > 64 ? 128 : count > 32 ? 64 : count > 16 ? 32 : 16, ways = kThreads / held;
-      const int of = tid & (held - 1), way = tid / held;
+      const int held = count <= 16 ? 16 : 1 << (32 - __builtin_clz(count - 1)), ways = kThreads / held;
+      const int of = min(tid & (held - 1), count - 1), way = tid / held;
       float m = kNone, l = 0.f;
-      const float2* from_stats = args.stats + (int64_t)id * kRows + min(of, count - 1);
+      const float2* from_stats = args.stats + (id + of / kRows * parts.y) * kRows + of % kRows;
       constexpr int kBatch = kWaves == 4 && kVec == 2 ? 12 : 4;
       for (int i = way; i < parts.y; i += kBatch * ways) {
         float2 f[kBatch];
@@ -381,13 +385,12 @@ __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs 
           const float2 f = joined[i * held + tid];
           join(m, l, f.x, f.y);
         }
-        const int limit = sees(seq, (blk * kRows + tid) / a.H);
+        const int limit = sees(seq, (int)((from_row + tid) / a.H));
         row_lse[tid] = log_sum(m, l, limit, reach);
         row_limit[tid] = min(limit, reach);
       }
       lds_barrier();
-      for (int p = wave; p < count; p += kWaves * kTogether) {
-        if (p > wave) read(p);
+      auto add = [&](int p, const vec* x) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
           const int at = min(p + kWaves * i, count - 1);
@@ -398,6 +401,21 @@ __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs 
             const float w = __builtin_amdgcn_exp2f(x[i][j] - lse);
             total[j] += key + j < limit ? w : 0.f;
           }
+        }
+      };
+      constexpr int kStep = kWaves * kTogether;
+      if constexpr (kAhead) {
+        for (int p = wave; p < count; p += 2 * kStep) {
+          if (p + kStep < count) read(p + kStep, x[1]);
+          add(p, x[0]);
+          if (p + kStep >= count) break;
+          if (p + 2 * kStep < count) read(p + 2 * kStep, x[0]);
+          add(p + kStep, x[1]);
+        }
+      } else {
+        for (int p = wave; p < count; p += kStep) {
+          if (p > wave) read(p, x[0]);
+          add(p, x[0]);
         }
       }
       lds_barrier();

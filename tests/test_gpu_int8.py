@@ -174,6 +174,19 @@ def test_gemm_views(gpu, m):
         assert bool((out[:, :lead] == 7).all()) and bool((out[:, lead + n:] == 7).all())
 
 
+@pytest.mark.parametrize("m", [5, 300])
+@pytest.mark.parametrize("pitch,lead,n", [(162, 2, 151), (162, 0, 150), (168, 8, 150), (164, 4, 145)])
+def test_gemm_row_pitches(gpu, m, pitch, lead, n):
+    """Outputs aligned to 4, 8 and 16 bytes, with columns that end inside such a piece."""
+    g = torch.Generator().manual_seed(m + n)
+    q, w = _codes((m, 208), g).to(gpu), _codes((n, 208), g).to(gpu)
+    s, ws = (0.02 * torch.rand(m, generator=g)).to(gpu), (0.01 * torch.rand(n, generator=g)).to(gpu)
+    out = torch.full((m, pitch), 7.0, dtype=torch.bfloat16, device=gpu)
+    announce("gemm_int8 pitches", m, pitch, lead, n)
+    _check_product(bfp8.gemm_int8(q, s, w, ws, out=out[:, lead:lead + n]), q, s, w, ws, None, (m, pitch, lead, n))
+    assert bool((out[:, :lead] == 7).all()) and bool((out[:, lead + n:] == 7).all())
+
+
 def test_bad_tokens_stay_alone(gpu):
     """A token that is not finite gives NaN outputs and leaves the others as they are, through the quantizer and all."""
     g = torch.Generator().manual_seed(8)
