@@ -463,10 +463,10 @@ hipError_t launch_pass(const LatentMassArgs& args, int64_t grid, hipStream_t str
 
 // Scores are kept where this has both sides of it: a score costs 8 bytes of traffic, scoring a key again its 641 bytes and the products of
 // its sequence's blocks. Sequences of 32 rows or fewer (256 x 16 heads, 1000 to 8000 keys: 235 us kept, 366 scored again) keep up to 512 MB,
-// those of up to 512 rows what the MALL holds (us beside the attention, kept and scored again: 8 sequences x 3 tokens x 128 heads 64 and
-// 70, 32 x 3 x 128 heads, 147 MB, 79 and 90; above it 50 x 20 x 16 heads, 256 MB, 142 and 136, and 205 MB come out either way). With more
-// rows the products of all blocks cost less than a last launch that takes a sequence's blocks in turn (4 x 8 tokens x 128 heads
-// 88 and 86, 1 x 16 x 128 heads 92 and 32).
+// those of up to 1024 rows what the MALL holds (us beside the attention, kept and scored again: 8 sequences x 3 tokens x 128 heads 60 and
+// 70, 32 x 3 x 128 heads, 147 MB, 79 and 90, 8 x 8 x 128 heads, 131 MB, 68 and 83; above it 50 x 20 x 16 heads, 256 MB, 142 and 136, and 205 MB
+// come out either way). With more rows the products of all blocks cost less than a last launch that takes a sequence's rows in turn
+// (1 sequence of 2000 tokens, 1024 rows 34 and 32, 2048 rows 50 and 32).
 constexpr int64_t kMostScores = (int64_t)512 << 20, kMostOfMany = (int64_t)192 << 20;
 
 LatentMassPlan plan_latent_mass(int64_t T, int64_t B, int64_t H, int64_t max_keys) {
@@ -482,7 +482,7 @@ LatentMassPlan plan_latent_mass(int64_t T, int64_t B, int64_t H, int64_t max_key
   const int64_t cut = std::min<int64_t>(blocks * std::max<int64_t>((tiles + p.min_tiles - 1) / p.min_tiles, 1), p.target_parts);
   p.ids = (std::max(blocks, cut) + 15) / 16 * 16;
   p.pitch = tiles * kTile;
-  p.keeps_scores = T * H <= 4 * kRows * B && T * H <= (T * H <= 32 * B ? kMostScores : kMostOfMany) / 4 / std::max<int64_t>(p.pitch, 1);
+  p.keeps_scores = T * H <= 8 * kRows * B && T * H <= (T * H <= 32 * B ? kMostScores : kMostOfMany) / 4 / std::max<int64_t>(p.pitch, 1);
   p.first_bytes = up(B * (int64_t)sizeof(int2));
   p.stats_bytes = up(p.ids * kRows * (int64_t)sizeof(float2));
   p.rest_bytes = up((p.keeps_scores ? T * H : T * H / kRows + B + 1) * p.pitch * (int64_t)sizeof(float));

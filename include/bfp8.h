@@ -628,7 +628,7 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
  *   workspace bfp8_latent_attention_mass_workspace_bytes bytes, 256-byte aligned, contents arbitrary:
  *             that of bfp8_latent_attention, at most 1 KB for each of T * H / 128 + B + 512 parts of the
  *             work, 8 bytes a sequence, and 4 bytes for every token that a page table reaches and
- *             every query row (while sequences have 512 rows or fewer on average and that is 192 MB
+ *             every query row (while sequences have 1024 rows or fewer on average and that is 192 MB
  *             or less, 512 MB with 32 rows or fewer; then scores are kept) or every 128 of them
  *
  * bfp8_latent_cache_evict: a sequence longer than `budget` keeps its last `recent` tokens and, of

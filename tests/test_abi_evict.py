@@ -55,7 +55,7 @@ def test_mass_workspace(lib):
         rest = size(t, b, h, keys) - attention(t, b, h, keys)
         pitch = -(-keys // 32) * 32
         scores = 4 * t * h * pitch
-        kept = t * h <= 512 * b and scores <= (512 if t * h <= 32 * b else 192) << 20
+        kept = t * h <= 1024 * b and scores <= (512 if t * h <= 32 * b else 192) << 20
         need = scores if kept else 4 * (t * h // 128 + b + 1) * pitch
         assert need <= rest <= need + 1024 * (t * h // 128 + b + 512 + 16) + 8 * b + 4 * 256
 

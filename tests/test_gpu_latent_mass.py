@@ -58,7 +58,7 @@ CASES = [
     ([1], [1], 1, 1), ([1111], [1], 128, 64), ([500, 64, 7, 900], [1] * 4, 16, 64), ([127, 128, 129], [1] * 3, 33, 16),
     ([40, 300, 129], [40, 7, 129], 5, 37), ([100, 50, 9], [0, 3, 0], 8, 16), ([2, 0, 31], [5, 2, 31], 4, 16),
     ([600, 33], [65, 1], 20, 64), ([2000, 17, 1300], [1] * 3, 64, 16), ([700], [40], 128, 16), ([260] * 9, [2] * 9, 16, 37),
-    ([4500], [1], 5, 1),
+    ([4500], [1], 5, 1), ([900, 300, 70], [200, 2, 70], 32, 16),
 ]
 
 
