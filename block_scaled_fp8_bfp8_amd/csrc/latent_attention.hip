@@ -34,7 +34,7 @@
 // score products, and the LDS layout (below) leaves all but a few addresses to constant offsets.
 //
 // Measured: 128 sequences of 2500 to 4096 keys x 128 heads 128 us (matrix cores busy 39 % of the clocks), 64 of 500
-// to 8000 x 16 heads 54 us (5.4 TB/s in its middle), one of 1111 x 128 heads 19.3 us.
+// to 8000 x 16 heads 54 us (5.4 TB/s in its middle), one of 1111 x 128 heads 18.6 us.
 //
 // Work is cut on the device, where the lengths are: a block is the query rows (tokens x heads)
 // of one sequence that a workgroup holds, and where there are fewer blocks than workgroups fit
