@@ -684,7 +684,8 @@ bfp8_status_t bfp8_latent_cache_evict(uint8_t* rows, int64_t page_stride, uint8_
  * bs float32 [N], bias [N] of the output's type or NULL, c [M][ldc] of out_dtype (BFP8_IN_BF16 or
  * BFP8_IN_F16). Unlike the FP8 products, rows need not be padded: nothing past K is read.
  *   K a multiple of 16, at most 65536; a and b 16-byte aligned; lda, ldb multiples of 16, >= K,
- *   below 2^23 (so a weight may pass 4 GiB); N at most 2^26, M x N at most 2^23 tiles of 64 x 64
+ *   below 2^23 (so a weight may pass 4 GiB); rows that start at multiples of 128 bytes are read
+ *   fastest; N at most 2^26, M x N at most 2^23 tiles of 64 x 64
  *
  * bfp8_linear_int8: quantizes x [M][ldx] (bf16 or fp16) and multiplies; c has x's type. The
  * workspace (bfp8_linear_int8_workspace_bytes, 256-byte aligned, contents arbitrary) holds codes
