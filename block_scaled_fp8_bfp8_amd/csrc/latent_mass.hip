@@ -348,8 +348,9 @@ __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t rows = (int64_t)seq.n * a.H, row0 = (int64_t)seq.q0 * a.H;
   const int reach = reach_of(a), keys = min(seq.len, reach);
-  for (int k0 = first * 64 * kVec; k0 < args.width; k0 += args.each * 64 * kVec) {
-    const int key = k0 + lane * kVec;
+  // (unsigned: the step past the last column may pass 2^31, but not 2^32)
+  for (unsigned at = (unsigned)first * 64 * kVec; at < (unsigned)args.width; at += (unsigned)args.each * 64 * kVec) {
+    const int k0 = (int)at, key = k0 + lane * kVec;
     const float before = tid < 64 * kVec ? mass_before(args, seq, b, k0 + tid) : 0.f;
     vec total = 0.f;
     for (int64_t from_row = 0; from_row < rows && k0 < keys; from_row += kAtOnce) {
@@ -440,7 +441,9 @@ __global__ __launch_bounds__(kSumKeys) void latent_blocks_kernel(LatentMassArgs 
   const Seq seq = sequence(a, b);
   const int64_t rows = (int64_t)seq.n * a.H, row0 = (int64_t)seq.q0 * a.H;
   const int reach = reach_of(a), blocks = (int)((rows + kRows - 1) / kRows);
-  for (int key = first * kSumKeys + threadIdx.x; key < args.width; key += args.each * kSumKeys) {
+  // (unsigned: the step past the last column may pass 2^31, but not 2^32)
+  for (unsigned at = (unsigned)first * kSumKeys + threadIdx.x; at < (unsigned)args.width; at += (unsigned)args.each * kSumKeys) {
+    const int key = (int)at;
     float total = 0.f;
     if (blocks > 0 && key < min(seq.len, reach)) {
       // the first block whose last row sees the key: later ones all do
