@@ -40,7 +40,7 @@ constexpr int kBlockBytes = 8 * 128, kGroupBytes = 5 * kBlockBytes + 64;
 constexpr int kTileBytes = 4 * kGroupBytes;
 constexpr int kBuffers = 3;
 constexpr int kMap = 2048;  // keys that are looked up at a time
-constexpr float kNone = -1e30f;
+constexpr float kNone = -__FLT_MAX__;  // a maximum over no keys: no finite score is below it
 constexpr float kNegInf = -__builtin_inff();
 constexpr uint32_t kNowhere = 0xffffffffu;
 
@@ -66,10 +66,13 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
   l = l * __builtin_amdgcn_exp2f(m - top) + l2 * __builtin_amdgcn_exp2f(m2 - top);
   m = top;
 }
-// log2 of the sum over all keys: infinity for a row that sees none (its weights are zero), NaN for one that sees a key past the table.
-__device__ __forceinline__ float log_sum(float m, float l, int limit, int reach) {
-  if (limit > reach) return __builtin_nanf("");
-  return l == 0.f ? __builtin_inff() : m + __builtin_amdgcn_logf(l);  // (logf: base 2)
+// What a row's weights are formed with, 2^(x - top) * share: the maximum over all keys that it sees and one over its sum. (They are not one
+// number, top + log2(sum): for scores far from zero that rounds the sum away.) A row whose softmax is none (a key past the table, a sum that is
+// NaN, or zero, as all its scores are minus infinity) has a NaN maximum and a finite share, so that a weight masked to zero stays zero.
+__device__ __forceinline__ float2 row_sum(float m, float l, int limit, int reach) {
+  if (limit == 0) return make_float2(0.f, 0.f);
+  if (limit > reach || !(l > 0.f)) return make_float2(__builtin_nanf(""), 1.f);
+  return make_float2(m, 1.f / l);
 }
 
 enum class Pass { kSums, kScores, kWeights };  // maxima and sums; the scores too; sums of weights by key
@@ -81,7 +84,8 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
   __shared__ __attribute__((aligned(1024))) uint8_t tiles_lds[kBuffers * kTileBytes];
   __shared__ __attribute__((aligned(16))) uint32_t map_unit[kMap];  // where a key lies, in 128 bytes
   __shared__ __attribute__((aligned(16))) float map_scale[kMap];    // its scale times scale log2(e)
-  __shared__ __attribute__((aligned(16))) float row_lse[kRows];
+  __shared__ __attribute__((aligned(16))) float row_top[kRows];
+  __shared__ __attribute__((aligned(16))) float row_share[kRows];
   __shared__ __attribute__((aligned(16))) int row_limit[kRows];
   __shared__ float sums[2][4][kTile];
   Work work;
@@ -108,6 +112,8 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
   // keys that every row of the wave sees: tiles before need no mask
   const int all = uniform(wave * 32 + 32 <= rows ? limit : 0);
   const float c = a.scale * 1.44269504088896341f;
+  // (rounded alike in both passes, so that no weight is above one)
+  auto score = [&](float lat, float unit, float rot) { return fmaf(lat, unit, rot * c); };
   if (!kWeights && work.block == 0 && work.part == 0 && tid == 0) args.first[work.index] = make_int2(work.id, work.parts);
 
   if constexpr (kWeights) {
@@ -122,18 +128,21 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
           const float2 f = p[(int64_t)i * kRows];
           join(m, l, f.x, f.y);
         }
-      row_lse[tid] = tid < rows ? log_sum(m, l, lim, reach) : __builtin_inff();
+      const float2 sum = row_sum(m, l, lim, reach);
+      row_top[tid] = sum.x;
+      row_share[tid] = sum.y;
       row_limit[tid] = lim;
     }
   }
-  float lse[kWeights ? 16 : 1];
+  float tops[kWeights ? 16 : 1], shares[kWeights ? 16 : 1];
   if constexpr (kWeights) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const v4f v = *reinterpret_cast<const v4f*>(&row_lse[wave * 32 + 8 * i + 4 * g]);
+      const v4f top = *reinterpret_cast<const v4f*>(&row_top[wave * 32 + 8 * i + 4 * g]);
+      const v4f share = *reinterpret_cast<const v4f*>(&row_share[wave * 32 + 8 * i + 4 * g]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) lse[4 * i + j] = v[j];
+      for (int j = 0; j < 4; ++j) tops[4 * i + j] = top[j], shares[4 * i + j] = share[j];
     }
   }
 
@@ -271,7 +280,7 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
         const float unit = map_scale[i * kTile + r];
         float total = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __builtin_amdgcn_exp2f(fmaf(lat[j], unit, fmaf(rot[j], c, -lse[j])));
+        for (int j = 0; j < 16; ++j) x[j] = __builtin_amdgcn_exp2f(score(lat[j], unit, rot[j]) - tops[j]);
         if (t * kTile + kTile > all) {
 #pragma unroll
           for (int j4 = 0; j4 < 4; ++j4) {
@@ -281,7 +290,7 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
           }
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) total += x[j];
+        for (int j = 0; j < 16; ++j) total = fmaf(x[j], shares[j], total);
         total += __shfl_xor(total, 32);
         if (g == 0) sums[t & 1][wave][r] = total;
       } else {
@@ -289,7 +298,7 @@ __global__ __launch_bounds__(256, 2) void latent_mass_kernel(LatentMassArgs args
         for (int j4 = 0; j4 < 4; ++j4) {
           const v4f unit = *reinterpret_cast<const v4f*>(&map_scale[i * kTile + 8 * j4 + 4 * g]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[4 * j4 + j] = fmaf(lat[4 * j4 + j], unit[j], rot[4 * j4 + j] * c);
+          for (int j = 0; j < 4; ++j) x[4 * j4 + j] = score(lat[4 * j4 + j], unit[j], rot[4 * j4 + j]);
         }
         if (t * kTile + kTile > all) {
           const int left = limit - t * kTile - 4 * g;
@@ -338,7 +347,7 @@ __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs 
   static_assert(kAtOnce % kRows == 0, "rows at once are whole blocks");
   typedef float vec __attribute__((ext_vector_type(kVec)));
   const LatentAttnArgs& a = args.work;
-  __shared__ float row_lse[kAtOnce];
+  __shared__ float2 row_sums[kAtOnce];
   __shared__ int row_limit[kAtOnce];
   __shared__ float2 joined[kThreads];
   __shared__ __attribute__((aligned(16))) vec sums[kWaves][64];
@@ -387,7 +396,7 @@ __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs 
           join(m, l, f.x, f.y);
         }
         const int limit = sees(seq, (int)((from_row + tid) / a.H));
-        row_lse[tid] = log_sum(m, l, limit, reach);
+        row_sums[tid] = row_sum(m, l, limit, reach);
         row_limit[tid] = min(limit, reach);
       }
       lds_barrier();
@@ -395,12 +404,12 @@ __global__ __launch_bounds__(kWaves * 64) void latent_sum_kernel(LatentMassArgs 
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
           const int at = min(p + kWaves * i, count - 1);
-          const float lse = row_lse[at];
+          const float2 sum = row_sums[at];
           const int limit = p + kWaves * i < count ? row_limit[at] : 0;
 #pragma unroll
           for (int j = 0; j < kVec; ++j) {
-            const float w = __builtin_amdgcn_exp2f(x[i][j] - lse);
-            total[j] += key + j < limit ? w : 0.f;
+            const float w = __builtin_amdgcn_exp2f(x[i][j] - sum.x);
+            total[j] = fmaf(key + j < limit ? w : 0.f, sum.y, total[j]);
           }
         }
       };

@@ -620,8 +620,9 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
  *                    softmax_j(scale * q[t, h] . [c_j, r_j])
  * for the tokens j that were there before, the sum alone for those that are new in this call, and
  * 0 in the columns past the sequence. The weights are those of exact products of q with the cached
- * values, in float32 throughout. A row that is NaN (see bfp8_latent_attention) adds NaN to the
- * tokens it sees.
+ * values, in float32 throughout, and a row's add up to one wherever in float32's range its scores
+ * lie. A row that is NaN (see bfp8_latent_attention), or whose scores are all minus infinity, adds
+ * NaN to the tokens it sees.
  *   mass_in   NULL: zeros; may be mass_out
  *   width     columns of mass_in and mass_out, at least table_width * page_size
  *   T == 0    is allowed: mass_in is copied, with zeros past each sequence
