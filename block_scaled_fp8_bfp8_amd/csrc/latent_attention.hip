@@ -63,7 +63,7 @@ constexpr int kRefBytes = 2 * 128;         // their exponents
 constexpr int kKeyBytes = 2 * 256;         // a wave's scale codes of a tile as floats, and 2^-e
 constexpr float kSlack = 32.f;             // weights may pass the accumulator's reference by a factor of 2^kSlack
 constexpr float kTop = 8.f;                // the largest of 32 weights is held at 2^(kTop - 1) .. 2^kTop <= 448
-constexpr float kNone = -1e30f;            // exponent of no weight at all
+constexpr float kNone = -__FLT_MAX__;      // exponent of no weight at all: no finite score is below it
 constexpr float kNegInf = -__builtin_inff();
 
 // The row that a key without a page stands on: finite codes, so that rows that do not see it (weight zero) stay finite.

@@ -1,4 +1,4 @@
-"""GPU test of latent attention where every score of a row lies below -10^30."""
+"""GPU tests of latent attention with scores of every magnitude in float32's range: where all of a row's lie below -10^30."""
 
 import pytest
 import torch
