@@ -371,7 +371,9 @@ __global__ __launch_bounds__(kPairs * 128, 1) void latent_attn_kernel(LatentAttn
       const unsigned bits = __float_as_uint(top);
       const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
       top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
-      w.ref = top == kNegInf ? kNone : ceilf(top) - kTop;
+      // (where whole numbers are 16 apart, 2^27 on, top - kTop may be rounded to top - 16: the weights would pass 448)
+      const float low = ceilf(top) - kTop;
+      w.ref = top == kNegInf ? kNone : low + kTop < top ? top : low;
       w.sum[0] = w.sum[1] = 0.f;
     };
     // Weights of keys 2 k and 2 k + 1; the same into the two terms.
