@@ -1158,6 +1158,9 @@ bfp8_status_t check_mass(int64_t B, int64_t page_size, int64_t table_width, cons
   if (width > 0 && !mass_out) return fail(BFP8_ERR_INVALID_ARGUMENT, "the masses must not be NULL");
   if (B > 1 && (out_stride < width || (mass_in && in_stride < width)))
     return fail(BFP8_ERR_INVALID_ARGUMENT, "strides of the masses must be at least %lld", (long long)width);
+  // (else a sequence's row would be written over what another's workgroups still read)
+  if (mass_in && mass_in == mass_out && B > 1 && in_stride != out_stride)
+    return fail(BFP8_ERR_INVALID_ARGUMENT, "masses updated in place have one stride");
   if (!aligned(mass_in, 4) || !aligned(mass_out, 4) || !aligned(lens, 4))
     return fail(BFP8_ERR_MISALIGNED, "masses and lengths must be 4-byte aligned");
   return BFP8_OK;
@@ -1262,8 +1265,6 @@ bfp8_status_t bfp8_latent_cache_evict(uint8_t* rows, int64_t page_stride, uint8_
   if (width > 0 && !mass) return fail(BFP8_ERR_INVALID_ARGUMENT, "the masses must not be NULL");
   if (!kept || !lens_out) return fail(BFP8_ERR_INVALID_ARGUMENT, "kept and lens_out must not be NULL");
   if (!aligned(kept, 4) || !aligned(lens_out, 4)) return fail(BFP8_ERR_MISALIGNED, "kept and lens_out must be 4-byte aligned");
-  if (mass == mass_out && B > 1 && mass_stride != mass_out_stride)
-    return fail(BFP8_ERR_INVALID_ARGUMENT, "masses updated in place have one stride");
   st = check_device();
   if (st != BFP8_OK) return st;
   const bfp8::LatentEvictArgs args{

@@ -623,7 +623,7 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
  * values, in float32 throughout, and a row's add up to one wherever in float32's range its scores
  * lie. A row that is NaN (see bfp8_latent_attention), or whose scores are all minus infinity, adds
  * NaN to the tokens it sees.
- *   mass_in   NULL: zeros; may be mass_out
+ *   mass_in   NULL: zeros; may be mass_out (then with its stride; else the two may not overlap)
  *   width     columns of mass_in and mass_out, at least table_width * page_size
  *   T == 0    is allowed: mass_in is copied, with zeros past each sequence
  *   workspace bfp8_latent_attention_mass_workspace_bytes bytes, 256-byte aligned, contents arbitrary:
@@ -638,7 +638,7 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
  *   kept      int32 [B][budget]: which token became token i, -1 past the new length
  *   lens_out  int32 [B]: the new lengths; may be seq_lens
  *   mass_out  the masses of the kept tokens in their new places, then zeros up to `width`; may be
- *             mass (then with its stride)
+ *             mass (then with its stride; else the two may not overlap)
  *   out_table NULL: tokens move within their own pages, of which no page may appear twice in the
  *             call's tables (pages past the new length are then free). Or int32
  *             [B][out_table_stride]: every kept token goes to out_table_width pages of its own,
