@@ -43,6 +43,13 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   else return pack_bf16(lo, hi);
 }
 
+// An output is fl(fl(sum * token's scale) * channel's scale + bias). The sum (2^30 at most) times the scale of a token whose largest element
+// passes 2^104 or so may pass float32 though the channel's brings the output back: such a token's outputs are formed 2^32 times smaller first.
+__device__ __forceinline__ bool scale_is_far(float ms) { return fabsf(ms) >= 0x1p97f; }
+__device__ __forceinline__ float far_output(int sum, float ms, float ns, float add) {
+  return fmaf((float)sum * (ms * 0x1p-32f) * ns, 0x1p32f, add);
+}
+
 // 4 neighbouring outputs n .. n + 3 of a row.
 __device__ __forceinline__ void store4(uint16_t* c, int n, int N, bool vec_ok, uint32_t p0, uint32_t p1) {
   if (vec_ok && n + 3 < N) {
@@ -185,6 +192,9 @@ __global__ __launch_bounds__(kWaves * 64) void gemm_int8_ksplit_kernel(Int8GemmA
     float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = fmaf((float)v[e] * ms, ns[e], add[e]);
+    if (__builtin_expect(scale_is_far(ms), 0))
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = far_output(v[e], ms, ns[e], add[e]);
     store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
   }
 }
@@ -302,7 +312,8 @@ __global__ __launch_bounds__(kWaves * 64) void linear_int8_kernel(Int8GemmArgs a
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int at = min(n + e, N - 1);
-      y[e] = fmaf((float)sum[e] * ms, args.bs[at], args.bias != nullptr ? bias_value<kF16>(args.bias[at]) : 0.f);
+      const float ns = args.bs[at], add = args.bias != nullptr ? bias_value<kF16>(args.bias[at]) : 0.f;
+      y[e] = scale_is_far(ms) ? far_output(sum[e], ms, ns, add) : fmaf((float)sum[e] * ms, ns, add);
     }
     store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
   }
@@ -473,19 +484,23 @@ __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8Gem
 #pragma unroll
   for (int tm = 0; tm < TM; ++tm) {
     const float ms = args.as[min(m0 + wm * WM + tm * 32 + r, M - 1)];
+    auto stage = [&](auto output) __attribute__((always_inline)) {
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn)
+      for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = tn * 32 + 8 * q + 4 * g;
-        const v4f ns = *reinterpret_cast<const v4f*>(&channel[0][wn * WN + col]);
-        const v4f add = *reinterpret_cast<const v4f*>(&channel[1][wn * WN + col]);
-        float y[4];
+        for (int q = 0; q < 4; ++q) {
+          const int col = tn * 32 + 8 * q + 4 * g;
+          const v4f ns = *reinterpret_cast<const v4f*>(&channel[0][wn * WN + col]);
+          const v4f add = *reinterpret_cast<const v4f*>(&channel[1][wn * WN + col]);
+          float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = fmaf((float)acc[tn][tm][4 * q + e] * ms, ns[e], add[e]);
-        const uint32_t p0 = pack16<kF16>(y[0], y[1]), p1 = pack16<kF16>(y[2], y[3]);
-        *reinterpret_cast<uint2*>(staged + r * kRowBytes + col * 2) = make_uint2(p0, p1);
-      }
+          for (int e = 0; e < 4; ++e) y[e] = output(acc[tn][tm][4 * q + e], ns[e], add[e]);
+          const uint32_t p0 = pack16<kF16>(y[0], y[1]), p1 = pack16<kF16>(y[2], y[3]);
+          *reinterpret_cast<uint2*>(staged + r * kRowBytes + col * 2) = make_uint2(p0, p1);
+        }
+    };
+    if (__builtin_expect(scale_is_far(ms), 0)) stage([&](int sum, float ns, float add) { return far_output(sum, ms, ns, add); });
+    else stage([&](int sum, float ns, float add) { return fmaf((float)sum * ms, ns, add); });
     // (LDS executes a wave's accesses in order; this keeps the compiler to it)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();

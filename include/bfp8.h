@@ -670,7 +670,8 @@ bfp8_status_t bfp8_latent_cache_evict(uint8_t* rows, int64_t page_stride, uint8_
 /*
  * 8-bit integer products with one scale a token and one a channel ("W8A8" with integer codes):
  *   C[m, n] = round16((sum_k a[m, k] * b[n, k]) * as[m] * bs[n] + bias[n])
- * The sum is exact (32-bit integers); it is scaled and biased in float32 and rounded once.
+ * The sum is exact (32-bit integers); it is scaled and biased in float32 and rounded once (a sum
+ * whose product with as[m] alone passes float32 is scaled as it should be, too).
  *
  * bfp8_quant_act_int8: for every row m of x [M][ldx] (any BFP8_IN_ type):
  *   top = max(max_k |x[m, k]|, 1e-10),  s[m] = fl32(top / 127)      (correctly rounded divide)
