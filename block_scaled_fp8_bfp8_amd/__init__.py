@@ -32,7 +32,7 @@ __all__ = [
     "rmsnorm_quant", "rmsnorm_quant_ue8m0", "latent_cache_write", "latent_cache_read", "latent_cache_gather",
     "latent_attention", "latent_attention_workspace_bytes", "latent_attention_expanded",
     "latent_attention_mass", "latent_attention_mass_workspace_bytes", "latent_cache_evict",
-    "quant_act_int8", "gemm_int8", "linear_int8", "linear_int8_workspace_bytes",
+    "quant_act_int8", "gemm_int8", "gemm_int8_kernel_for", "linear_int8", "linear_int8_workspace_bytes",
     "abi_version", "BfpError", "LibraryMissing",
 ]
 
@@ -1302,6 +1302,13 @@ def gemm_int8(a_q: torch.Tensor, a_s: torch.Tensor, w_q: torch.Tensor, w_s: torc
           _row_stride(w_q, 16), w_s.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
           _IN_DTYPES[dtype], ldc, m, n, k)
     return out
+
+
+def gemm_int8_kernel_for(m: int, n: int, k: int) -> tuple[str, int, int] | None:
+    """The kernel that gemm_int8 runs for these sizes: ("split_k" or "tiled", channels, tokens of its tile); None for
+    sizes that have none."""
+    v = _native.lib().bfp8_gemm_int8_kernel_for(m, n, k)
+    return ("split_k" if v < 0 else "tiled", abs(v) >> 16, abs(v) & 0xFFFF) if v else None
 
 
 def linear_int8_workspace_bytes(m: int, k: int) -> int:

@@ -93,6 +93,7 @@ SIGNATURES = [
     ("bfp8_quant_act_int8", ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
     ("bfp8_gemm_int8", ctypes.c_int,
      [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp]),
+    ("bfp8_gemm_int8_kernel_for", ctypes.c_int, [_i64, _i64, _i64]),
     ("bfp8_linear_int8_workspace_bytes", _sz, [_i64, _i64]),
     ("bfp8_linear_int8", ctypes.c_int,
      [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),

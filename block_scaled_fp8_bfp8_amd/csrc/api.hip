@@ -1289,6 +1289,9 @@ bfp8_status_t check_int8_sizes(int64_t M, int64_t N, int64_t K) {
   return BFP8_OK;
 }
 
+// (a launch has fewer than 2^32 threads)
+bool int8_grid_fits(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64) <= (int64_t)1 << 23; }
+
 bfp8_status_t check_quant_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, const int8_t* q, int64_t ldq,
                                const float* s) {
   if (x_dtype != BFP8_IN_F32 && x_dtype != BFP8_IN_BF16 && x_dtype != BFP8_IN_F16)
@@ -1313,8 +1316,7 @@ bfp8_status_t check_gemm_int8(const int8_t* a, int64_t lda, const float* as, con
     return fail(BFP8_ERR_UNSUPPORTED, "out_dtype %d is not BFP8_IN_BF16 or BFP8_IN_F16", out_dtype);
   const bfp8_status_t st = check_int8_sizes(M, N, K);
   if (st != BFP8_OK) return st;
-  // (a launch has fewer than 2^32 threads)
-  if (((M + 63) / 64) * ((N + 63) / 64) > (int64_t)1 << 23)
+  if (!int8_grid_fits(M, N))
     return fail(BFP8_ERR_UNSUPPORTED, "M x N = %lld x %lld has more output tiles than one launch grid holds",
                 (long long)M, (long long)N);
   if (!b || !bs) return fail(BFP8_ERR_INVALID_ARGUMENT, "b and bs must not be NULL");
@@ -1361,6 +1363,13 @@ bfp8_status_t bfp8_gemm_int8(const int8_t* a, int64_t lda, const float* as, cons
   if (st != BFP8_OK) return st;
   const bfp8::Int8GemmArgs args{a, lda, as, b, ldb, bs, bias, c, ldc, (int)M, (int)N, (int)K, out_dtype == BFP8_IN_F16};
   return launched(bfp8::launch_gemm_int8(args, (hipStream_t)stream), "gemm_int8");
+}
+
+int bfp8_gemm_int8_kernel_for(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || check_int8_sizes(M, N, K) != BFP8_OK || !int8_grid_fits(M, N)) return 0;
+  const bfp8::Int8Choice c = bfp8::choose_gemm_int8(M, N, K);
+  const int tile = c.bn << 16 | c.bm;
+  return c.splits_k ? -tile : tile;
 }
 
 size_t bfp8_linear_int8_workspace_bytes(int64_t M, int64_t K) {

@@ -584,27 +584,34 @@ struct SplitShape {
 constexpr SplitShape kSplit[] = {{16, 16, ksplit<1, 1, 2>}, {16, 32, ksplit<1, 2, 2>}, {32, 16, ksplit<2, 1, 3>}, {32, 32, ksplit<2, 2, 2>},
                                  {64, 16, ksplit<4, 1, 1>}, {32, 64, ksplit<2, 4, 1>}, {64, 64, ksplit<4, 4, 1>}};
 
-}  // namespace
-
-hipError_t launch_gemm_int8(const Int8GemmArgs& a, hipStream_t stream) {
-  const double blocks = (a.K + kBlock - 1) / kBlock, weights = 1e-6 * a.N * (double)a.K, outputs = 1e-6 * a.N * (double)a.M;
+struct Choice {
+  Int8Choice kernel;
+  hipError_t (*launch)(const Int8GemmArgs&, hipStream_t);
+};
+Choice choose(int64_t M, int64_t N, int64_t K) {
+  const double blocks = (double)((K + kBlock - 1) / kBlock), weights = 1e-6 * N * (double)K, outputs = 1e-6 * N * (double)M;
   double best = 1e30;
-  hipError_t (*launch)(const Int8GemmArgs&, hipStream_t) = nullptr;
-  auto tiles = [&](int bn, int bm) { return (double)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm); };
+  Choice choice{};
+  auto tiles = [&](int bn, int bm) { return (double)((N + bn - 1) / bn) * (double)((M + bm - 1) / bm); };
   for (const SplitShape& s : kSplit) {
-    if ((a.M + s.bm - 1) / s.bm > 65535) continue;  // the grid's second dimension
+    if ((M + s.bm - 1) / s.bm > 65535) continue;  // the grid's second dimension
     const double n = tiles(s.bn, s.bm), rounds = std::ceil(n / 256), mb = 1e-6 * kBlock * (s.bn + s.bm) * blocks;
     const double us = 1.91 + 0.107 * weights + 9.02 * rounds * mb + 0.0146 * n * mb + 0.354 * rounds +
                       0.000238 * rounds * s.bn * s.bm + 0.893 * outputs;
-    if (us < best) best = us, launch = s.launch;
+    if (us < best) best = us, choice = {{s.bn, s.bm, true}, s.launch};
   }
   for (const Shape& s : kTiled) {
     const double n = tiles(s.bn, s.bm), rounds = std::ceil(n / 256), mb = 1e-6 * kBlock * (s.bn + s.bm) * blocks;
     const double us = s.base + rounds * (s.per_block * blocks + s.per_round) + s.copied * n * mb + s.weights * weights + s.outputs * outputs;
-    if (us < best) best = us, launch = s.launch;
+    if (us < best) best = us, choice = {{s.bn, s.bm, false}, s.launch};
   }
-  return launch(a, stream);
+  return choice;
 }
+
+}  // namespace
+
+Int8Choice choose_gemm_int8(int64_t M, int64_t N, int64_t K) { return choose(M, N, K).kernel; }
+hipError_t launch_gemm_int8(const Int8GemmArgs& a, hipStream_t stream) { return choose(a.M, a.N, a.K).launch(a, stream); }
 
 namespace {
 template <int kIn, int kRows>

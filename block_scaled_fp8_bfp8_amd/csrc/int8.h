@@ -26,6 +26,12 @@ struct Int8GemmArgs {
   bool out_f16;
 };
 hipError_t launch_gemm_int8(const Int8GemmArgs& args, hipStream_t stream);
+// The tile of the kernel that launch_gemm_int8 chooses (bn channels x bm tokens), and whether its waves split K.
+struct Int8Choice {
+  int bn, bm;
+  bool splits_k;
+};
+Int8Choice choose_gemm_int8(int64_t M, int64_t N, int64_t K);
 // The linear layer in one launch, for the sizes that linear_int8_fuses accepts (args.a, lda and as unused).
 bool linear_int8_fuses(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_int8(const Int8GemmArgs& args, const uint16_t* x, int64_t ldx, hipStream_t stream);

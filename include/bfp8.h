@@ -698,6 +698,10 @@ bfp8_status_t bfp8_quant_act_int8(const void* x, int x_dtype, int64_t M, int64_t
 bfp8_status_t bfp8_gemm_int8(const int8_t* a, int64_t lda, const float* as, const int8_t* b, int64_t ldb,
                              const float* bs, const uint16_t* bias, uint16_t* c, int out_dtype, int64_t ldc,
                              int64_t M, int64_t N, int64_t K, void* stream);
+/* The kernel that bfp8_gemm_int8 runs for these sizes: 65536 times its tile's channels plus the
+ * tile's tokens, negative where the waves of a workgroup split K between them; 0 for sizes that
+ * have none. Host arithmetic only. */
+int bfp8_gemm_int8_kernel_for(int64_t M, int64_t N, int64_t K);
 size_t bfp8_linear_int8_workspace_bytes(int64_t M, int64_t K);
 bfp8_status_t bfp8_linear_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, const int8_t* b,
                                int64_t ldb, const float* bs, const uint16_t* bias, uint16_t* c, int64_t ldc,
