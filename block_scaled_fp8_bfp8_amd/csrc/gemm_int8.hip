@@ -43,11 +43,29 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   else return pack_bf16(lo, hi);
 }
 
-// An output is fl(fl(sum * token's scale) * channel's scale + bias). The sum (2^30 at most) times the scale of a token whose largest element
+// An output is fl(sum * token's scale) * channel's scale + bias. The sum (2^30 at most) times the scale of a token whose largest element
 // passes 2^104 or so may pass float32 though the channel's brings the output back: such a token's outputs are formed 2^32 times smaller first.
 __device__ __forceinline__ bool scale_is_far(float ms) { return fabsf(ms) >= 0x1p97f; }
-__device__ __forceinline__ float far_output(int sum, float ms, float ns, float add) {
-  return fmaf((float)sum * (ms * 0x1p-32f) * ns, 0x1p32f, add);
+// Four of a row's outputs, packed. In fp16 the compiler makes the sum with the bias and the rounding one instruction; where a branch formed
+// both kinds before a common rounding it would not, and the last bit would go by the kernel: so each kind is packed where it is formed.
+template <bool kF16>
+__device__ __forceinline__ uint2 outputs4(const int* sum, float ms, const float* ns, const float* add) {
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = fmaf((float)sum[e] * ms, ns[e], add[e]);
+  return make_uint2(pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
+}
+template <bool kF16>
+__device__ __forceinline__ uint2 far_outputs4(const int* sum, float ms, const float* ns, const float* add) {
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[e] = fmaf((float)sum[e] * (ms * 0x1p-32f) * ns[e], 0x1p32f, add[e]);
+    asm volatile("" : "+v"(y[e]));
+  }
+  uint2 p = make_uint2(pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
+  asm volatile("" : "+v"(p.x), "+v"(p.y));
+  return p;
 }
 
 // 4 neighbouring outputs n .. n + 3 of a row.
@@ -189,13 +207,10 @@ __global__ __launch_bounds__(kWaves * 64) void gemm_int8_ksplit_kernel(Int8GemmA
     v4i v = {0, 0, 0, 0};
 #pragma unroll
     for (int ww = 0; ww < kWaves; ++ww) v += *reinterpret_cast<const v4i*>(reinterpret_cast<const int*>(&slots[ww][0][0]) + q * 4);
-    float y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = fmaf((float)v[e] * ms, ns[e], add[e]);
-    if (__builtin_expect(scale_is_far(ms), 0))
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = far_output(v[e], ms, ns[e], add[e]);
-    store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
+    const int sum[4] = {v[0], v[1], v[2], v[3]};
+    uint2 out = outputs4<kF16>(sum, ms, ns, add);
+    if (__builtin_expect(scale_is_far(ms), 0)) out = far_outputs4<kF16>(sum, ms, ns, add);
+    store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, out.x, out.y);
   }
 }
 
@@ -305,17 +320,20 @@ __global__ __launch_bounds__(kWaves * 64) void linear_int8_kernel(Int8GemmArgs a
   const int m = r, n = n0 + 4 * kc;
   if (w == 0 && m < M && n < N) {
     const float ms = scales[m];
-    v4i sum = {0, 0, 0, 0};
+    v4i v = {0, 0, 0, 0};
 #pragma unroll
-    for (int ww = 0; ww < kWaves; ++ww) sum += *reinterpret_cast<const v4i*>(reinterpret_cast<const int*>(&slots[ww][0][0]) + lane * 4);
-    float y[4];
+    for (int ww = 0; ww < kWaves; ++ww) v += *reinterpret_cast<const v4i*>(reinterpret_cast<const int*>(&slots[ww][0][0]) + lane * 4);
+    const int sum[4] = {v[0], v[1], v[2], v[3]};
+    float ns[4], add[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int at = min(n + e, N - 1);
-      const float ns = args.bs[at], add = args.bias != nullptr ? bias_value<kF16>(args.bias[at]) : 0.f;
-      y[e] = scale_is_far(ms) ? far_output(sum[e], ms, ns, add) : fmaf((float)sum[e] * ms, ns, add);
+      ns[e] = args.bs[at];
+      add[e] = args.bias != nullptr ? bias_value<kF16>(args.bias[at]) : 0.f;
     }
-    store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, pack16<kF16>(y[0], y[1]), pack16<kF16>(y[2], y[3]));
+    uint2 out = outputs4<kF16>(sum, ms, ns, add);
+    if (__builtin_expect(scale_is_far(ms), 0)) out = far_outputs4<kF16>(sum, ms, ns, add);
+    store4(args.c + (int64_t)m * args.ldc + n, n, N, vec_ok, out.x, out.y);
   }
 }
 
@@ -484,23 +502,23 @@ __global__ __launch_bounds__(WGN * WGM * 64) void gemm_int8_tiled_kernel(Int8Gem
 #pragma unroll
   for (int tm = 0; tm < TM; ++tm) {
     const float ms = args.as[min(m0 + wm * WM + tm * 32 + r, M - 1)];
-    auto stage = [&](auto output) __attribute__((always_inline)) {
+    auto stage = [&](auto outputs) __attribute__((always_inline)) {
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int col = tn * 32 + 8 * q + 4 * g;
-          const v4f ns = *reinterpret_cast<const v4f*>(&channel[0][wn * WN + col]);
-          const v4f add = *reinterpret_cast<const v4f*>(&channel[1][wn * WN + col]);
-          float y[4];
+          const v4f s = *reinterpret_cast<const v4f*>(&channel[0][wn * WN + col]);
+          const v4f b = *reinterpret_cast<const v4f*>(&channel[1][wn * WN + col]);
+          int sum[4];
+          float ns[4], add[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = output(acc[tn][tm][4 * q + e], ns[e], add[e]);
-          const uint32_t p0 = pack16<kF16>(y[0], y[1]), p1 = pack16<kF16>(y[2], y[3]);
-          *reinterpret_cast<uint2*>(staged + r * kRowBytes + col * 2) = make_uint2(p0, p1);
+          for (int e = 0; e < 4; ++e) sum[e] = acc[tn][tm][4 * q + e], ns[e] = s[e], add[e] = b[e];
+          *reinterpret_cast<uint2*>(staged + r * kRowBytes + col * 2) = outputs(sum, ms, ns, add);
         }
     };
-    if (__builtin_expect(scale_is_far(ms), 0)) stage([&](int sum, float ns, float add) { return far_output(sum, ms, ns, add); });
-    else stage([&](int sum, float ns, float add) { return fmaf((float)sum * ms, ns, add); });
+    if (__builtin_expect(scale_is_far(ms), 0)) stage([](auto... v) __attribute__((always_inline)) { return far_outputs4<kF16>(v...); });
+    else stage([](auto... v) __attribute__((always_inline)) { return outputs4<kF16>(v...); });
     // (LDS executes a wave's accesses in order; this keeps the compiler to it)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
