@@ -1134,8 +1134,11 @@ def latent_attention_mass(q: torch.Tensor, cache: torch.Tensor, scales: torch.Te
     weights of all new tokens and heads; tokens that are new in this call start from zero, and columns past a
     sequence are zero. out_mass: where to put it (it may be mass itself). T == 0 new tokens are
     allowed (with cu_q). Other arguments as for latent_attention; the workspace is
-    latent_attention_mass_workspace_bytes (up to 512 MB more than latent_attention's while scores are
-    kept: 4 bytes for every query row and token that the page table reaches)."""
+    latent_attention_mass_workspace_bytes: up to 512 MB more than latent_attention's while scores are
+    kept (4 bytes for every query row and token that the page table reaches), else 4 bytes for every such token and
+    every 128 query rows and sequence, which has no bound (4.0 GiB for 8192 tokens of 128 heads over
+    131072). The default workspace is as large as the largest call's so far. A chunk of hundreds
+    of tokens is faster in a call of its own than among sequences with one new token each."""
     _require(q, "q", torch.bfloat16, 3)
     t, heads, dim = q.shape
     if dim != LATENT_DIM + ROPE_DIM or q.stride(2) != 1:
@@ -1319,7 +1322,7 @@ def linear_int8_workspace_bytes(m: int, k: int) -> int:
 def linear_int8(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, bias: torch.Tensor | None = None,
                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Linear layer on 8-bit integers: quant_act_int8 of x [M, K] (bf16 or fp16), gemm_int8 with w_q
-    [N, K] and w_s [N], and the bias; the output and the bias have x's dtype.
+    [N, K] and w_s [N], and the bias; the output and the bias have x's dtype. out may not overlap x.
 
     workspace: optional uint8 buffer of at least linear_int8_workspace_bytes(M, K) bytes; by default one
     buffer per (device, stream, host thread) is kept, and a call that is being captured takes one

@@ -1334,8 +1334,8 @@ bfp8_status_t check_gemm_int8(const int8_t* a, int64_t lda, const float* as, con
   return BFP8_OK;
 }
 
-// Workspace of the integer linear layer: codes in rows of K bytes, then the scales.
-// Codes of the linear layer lie in rows of whole 128-byte lines (64 tokens, 25101 x 6832: 54 us, 65 with rows of 6832 bytes).
+// Workspace of the integer linear layer: codes in rows of whole 128-byte lines (64 tokens, 25101 x 6832: 54 us, 65 with rows of 6832 bytes), then
+// the scales, from a multiple of 256 bytes on.
 int64_t int8_row(int64_t K) { return (K + 127) / 128 * 128; }
 size_t int8_scales_at(int64_t M, int64_t K) { return ((size_t)M * (size_t)int8_row(K) + 255) / 256 * 256; }
 

@@ -16,7 +16,8 @@
 // Measured (cold weights): 8192 x 10240 x 5120 345 us, 2.49 * 10^15 operations a second, bound by power (with operands of zeros, which
 // switch nothing, 280 us; the library's product of the same operands 430); 1000 x 4096 x 4096 21 us, bound by the copies into LDS (256
 // workgroups, one round); 1 x 4096 x 4096 5.9 us and 5 x 5120 x 8192 12.1 (3.5 TB/s), bound by reading the weights once, start-up
-// included; 83 x 576 x 7168 6.9 us, 216 workgroups with 56 K blocks in a chain each.
+// included; 83 x 576 x 7168 6.6 us, 216 workgroups whose waves take 7 of the 56 K blocks each, two of them in flight: about four memory
+// latencies one after another.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -579,8 +580,9 @@ hipError_t tiled(const Int8GemmArgs& a, hipStream_t stream) {
 }
 
 // A kernel's predicted time in microseconds, as sums of what it moves and does, fitted to times measured with cold weights
-// over 19 weight shapes from 12 x 25600 to 51200 x 5120 and 1 to 8192 tokens: the choice by it takes 1 % longer than
-// the fastest of the 13 on (geometric) average, 30 % at worst. (Per workgroup round: 256 run at once.)
+// over 19 weight shapes from 12 x 25600 to 51200 x 5120 and 1 to 8192 tokens, rows as long as K: the choice by it takes 1.1 % longer than the
+// fastest of the 13 on (geometric) average over 151 of them, 32 % at worst. (A round is counted as 256 workgroups, one a compute unit; kernels of which
+// several share one run more at once, for which their fitted terms stand. That a row pitch of no whole 128-byte lines costs up to 45 % is not in it.)
 struct Shape {
   int bn, bm;
   hipError_t (*launch)(const Int8GemmArgs&, hipStream_t);

@@ -12,7 +12,7 @@
 // moves by HBM, in place by the latency of a chunk where sequences are few.
 //
 // Measured: 64 sequences of 500 to 8000 tokens to 4096, onto other pages: selection 15 us, moves 60 us (267 MB, 4.5 TB/s); one of 1111 to
-// 1024: 8.1 and 3.8 us. In place, both together: 64 of 8000 82 us, 64 of 4097 46 us, one of 4097 22 us.
+// 1024: 8.1 and 3.8 us. In place, both together: 64 of 8000 83 us, 64 of 4097 48 us, one of 4097 20 to 22 us, one of 32769 to 32768 139 us.
 #include <algorithm>
 
 #include "device_latent.h"

@@ -17,10 +17,13 @@
 // with the rows first it holds one key and 16 rows, whose weights add up in registers. Two workgroups run on a compute unit,
 // so that one's softmax and conversions (128 instructions a tile) run beside the other's products.
 //
-// Measured, beside the attention: 1 sequence of 1111 x 128 heads 11.5 us for the scores (a chain of look-ups, rows and two tiles) and 7.4 for
-// their sum; 64 of 500 to 8000 x 16 heads 38 us (186 MB of rows, 4.9 TB/s) and 12; 6 chunks of 40 x 128 heads 90 us for each of two passes (matrix
+// Measured, beside the attention: 1 sequence of 1111 x 128 heads 11.5 us for the scores (a chain of look-ups, rows and two tiles) and 7.7 for
+// their sum; 64 of 500 to 8000 x 16 heads 38 us (186 MB of rows, 4.9 TB/s) and 12; 6 chunks of 40 x 128 heads 92 us for each of two passes (matrix
 // cores busy 36 % of the clocks: parts of 43 tiles at most where an even share is 33, and a softmax that only another workgroup's products
 // run beside) and 6.
+//
+// A row's weights are formed with its maximum and its sum apart, from scores that both passes round alike, so they add up to one wherever the scores
+// lie in float32's range.
 #include <algorithm>
 
 #include "device_latent.h"
@@ -474,11 +477,13 @@ hipError_t launch_pass(const LatentMassArgs& args, int64_t grid, hipStream_t str
 }  // namespace
 
 // Scores are kept where this has both sides of it: a score costs 8 bytes of traffic, scoring a key again its 641 bytes and the products of
-// its sequence's blocks. Sequences of 32 rows or fewer (256 x 16 heads, 1000 to 8000 keys: 235 us kept, 366 scored again) keep up to 512 MB,
-// those of up to 1024 rows what the MALL holds (us beside the attention, kept and scored again: 8 sequences x 3 tokens x 128 heads 60 and
+// its sequence's blocks. Batches of 32 rows a sequence or fewer (256 x 16 heads, 1000 to 8000 keys: 235 us kept, 366 scored again) keep up to 512 MB,
+// those of up to 1024 what the MALL holds (us beside the attention, kept and scored again: 8 sequences x 3 tokens x 128 heads 60 and
 // 70, 32 x 3 x 128 heads, 147 MB, 79 and 90, 8 x 8 x 128 heads, 131 MB, 68 and 83; above it 50 x 20 x 16 heads, 256 MB, 142 and 136, and 205 MB
 // come out either way). With more rows the products of all blocks cost less than a last launch that takes a sequence's rows in turn
-// (1 sequence of 2000 tokens, 1024 rows 34 and 32, 2048 rows 50 and 32).
+// (1 sequence of 2000 tokens, 1024 rows 34 and 32, 2048 rows 50 and 32). Rows are counted on average, as the host does not know the sequences' own; a
+// long chunk among decoding sequences so has all its rows taken in turn: 63 sequences of 1024 tokens x 16 heads 47 us with the attention, 234 with a
+// chunk of 256 tokens beside them and 738 with one of 1024, which by themselves take 68 and 106.
 constexpr int64_t kMostScores = (int64_t)512 << 20, kMostOfMany = (int64_t)192 << 20;
 
 LatentMassPlan plan_latent_mass(int64_t T, int64_t B, int64_t H, int64_t max_keys) {

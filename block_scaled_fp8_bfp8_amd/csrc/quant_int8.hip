@@ -68,9 +68,10 @@ void run(const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ld
 }
 
 // Many rows (more than run at once): as few waves a row as hold it in two chunks each, so that the fewest lanes have nothing to do and more
-// rows are under way. Few: a wave for every 512 elements, eight at most up to 8192. (us, as few and as many waves: 16384 x 2560 22.4 and
-// 33.8, 8192 x 4096 18.8 and 22.8, 4096 x 4096 11.6 and 13.3, 2100 x 4096 7.9 and 8.6; 2100 x 1024 4.8 and 4.2, 1024 x 4096 5.9 and 5.5, 1 x 7168 3.3
-// and 3.0.)
+// rows are under way. Few: a wave for every 512 elements, eight at most up to 8192. (us in a captured graph, as few and as many waves: 16384 x
+// 2560 24.4 and 34.1, 8192 x 4096 20.8 and 23.2, 4096 x 4096 10.5 and 11.9, 2100 x 4096 7.5 and 8.0, 4096 x 512 3.4 and 3.7; 1024 x 4096 5.4 and 5.2,
+// 1536 x 1024 4.0 and 3.5. One border for every length: rows of 513 to 1536 elements, of which more fit the card at once, lose up to 0.6 us just past it,
+// 2100 x 1024 4.3 and 3.8, 3000 x 1024 4.6 and 4.3, 2049 x 1536 4.7 and 4.4, and gain from about 4096 and 3000 rows on.)
 template <int kIn>
 void choose(const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ldq, float* s, hipStream_t stream) {
   const int64_t pieces = (K + 511) / 512;  // 64 lanes of 8 elements

@@ -630,7 +630,10 @@ bfp8_status_t bfp8_latent_attention_expanded(const uint16_t* q, int dtype, int64
  *             that of bfp8_latent_attention, at most 1 KB for each of T * H / 128 + B + 512 parts of the
  *             work, 8 bytes a sequence, and 4 bytes for every token that a page table reaches and
  *             every query row (while sequences have 1024 rows or fewer on average and that is 192 MB
- *             or less, 512 MB with 32 rows or fewer; then scores are kept) or every 128 of them
+ *             or less, 512 MB with 32 rows or fewer; then scores are kept) or every 128 of them and
+ *             every sequence (not bounded: 4.0 GiB for 8192 tokens of 128 heads over 131072)
+ * Where scores are kept, a sequence's rows are taken in turn: a chunk of hundreds of tokens is faster
+ * in a call of its own than among sequences with one new token each.
  *
  * bfp8_latent_cache_evict: a sequence longer than `budget` keeps its last `recent` tokens and, of
  * the earlier ones, the budget - recent with the largest mass (NaN above all others, of equal ones
@@ -687,11 +690,12 @@ bfp8_status_t bfp8_latent_cache_evict(uint8_t* rows, int64_t page_stride, uint8_
  * BFP8_IN_F16). Unlike the FP8 products, rows need not be padded: nothing past K is read.
  *   K a multiple of 16, at most 65536; a and b 16-byte aligned; lda, ldb multiples of 16, >= K,
  *   below 2^23 (so a weight may pass 4 GiB); rows that start at multiples of 128 bytes are read
- *   fastest; N at most 2^26, M x N at most 2^23 tiles of 64 x 64
+ *   fastest; N at most 2^26, M x N at most 2^23 tiles of 64 x 64; c may not overlap any input
  *
  * bfp8_linear_int8: quantizes x [M][ldx] (bf16 or fp16) and multiplies; c has x's type. The
  * workspace (bfp8_linear_int8_workspace_bytes, 256-byte aligned, contents arbitrary) holds codes
- * and scales between its launches. Bit-identical to the two calls above.
+ * and scales between its launches. Bit-identical to the two calls above. c may not overlap x or any
+ * other input.
  */
 bfp8_status_t bfp8_quant_act_int8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int8_t* q,
                                   int64_t ldq, float* s, void* stream);
